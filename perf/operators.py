@@ -245,10 +245,12 @@ def _prepare_own(s):
         flags = (c3d.CONV3D_F_BF16 if bf16 else 0) | (c3d.CONV3D_F_POSITIONS if case["given"] else 0)
         pairing = {"adjacent": c3d.ROPE3D_PAIR_ADJACENT, "halves": c3d.ROPE3D_PAIR_HALVES}[case["pairing"]]
         q, k = s["q"], s["k"]
+        # the tensors given are a gradient's incoming side when the call is the gradient's
+        side = ("q_out_stride", "k_out_stride") if case["grad"] else ("q_stride", "k_stride")
+        strides = dict(zip(side, (q.stride()[:3], k.stride()[:3])))
         s["plan"] = c3d.rope3d_plan(c3d.make_rope3d_desc(
             case["n"], case["t"], case["h"], case["w"], case["heads_q"], case["heads_k"], case["head_dim"],
-            _dims(case), base=_BASE, pairing=pairing, flags=flags, q_stride=q.stride()[:3],
-            k_stride=k.stride()[:3]))
+            _dims(case), base=_BASE, pairing=pairing, flags=flags, **strides))
         s["qo"], s["ko"] = out(*q.shape), out(*k.shape)
 
 
