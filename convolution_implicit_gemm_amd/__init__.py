@@ -31,6 +31,16 @@ CONV3D_F_NO_T1_FASTPATH = 4
 CONV3D_F_BF16 = 8
 CONV3D_F_CHUNK = 16
 CONV3D_F_GN_STATS = 32
+CONV3D_F_PREACT = 64
+CONV3D_F_POSITIONS = 128
+
+CONV3D_ACT_NONE = 0
+CONV3D_ACT_SILU = 1
+CONV3D_ACT_GELU = 2
+CONV3D_ACT_GELU_TANH = 3
+
+ROPE3D_PAIR_ADJACENT = 0
+ROPE3D_PAIR_HALVES = 1
 
 CONV3D_PATH_GENERAL = 0
 CONV3D_PATH_T1_FOLD = 1
@@ -41,6 +51,11 @@ EXPORTED = ("conv3d_plan", "conv3d_plan_query", "conv3d_plan_destroy", "conv3d_f
             "groupnorm_silu_workspace", "groupnorm_silu", "groupnorm_silu_bf16",
             "groupnorm_silu_from_stats_workspace", "groupnorm_silu_from_stats", "groupnorm_silu_from_stats_bf16",
             "groupnorm_silu_noalloc_max_bytes", "groupnorm_silu_noalloc",
+            "linear_plan", "linear_plan_query", "linear_plan_destroy", "linear_forward",
+            "linear_backward_workspace", "linear_backward",
+            "layernorm", "layernorm_bf16", "layernorm_backward_workspace", "layernorm_backward",
+            "layernorm_backward_bf16",
+            "rope3d_plan", "rope3d_plan_destroy", "rope3d_forward", "rope3d_backward",
             "conv3d_calibrate_scratch_bytes",
             "conv3d_calibrate_mfma", "conv3d_calibrate_hbm", "conv3d_clock_stamp_bytes",
             "conv3d_clock_stamp", "conv3d_status_str",
@@ -63,6 +78,26 @@ class conv3d_plan_info(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t), ("kernel_name", ctypes.c_char * 64),
                 ("split_tiles", ctypes.c_int32), ("split_pieces", ctypes.c_int32),
                 ("gn_stats_slots", ctypes.c_int32), ("gn_stats_offset", ctypes.c_size_t)]
+
+
+class linear_desc(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("residual_stride", ctypes.c_int64)]
+
+
+class linear_plan_info(ctypes.Structure):
+    _fields_ = [("tile_m", ctypes.c_int32), ("tile_n", ctypes.c_int32), ("tile_k", ctypes.c_int32),
+                ("threads", ctypes.c_int32), ("grid", ctypes.c_int64), ("split_tiles", ctypes.c_int32),
+                ("split_pieces", ctypes.c_int32), ("workspace_bytes", ctypes.c_size_t),
+                ("backward_workspace_bytes", ctypes.c_size_t), ("kernel_name", ctypes.c_char * 64)]
+
+
+class rope3d_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n", "t", "h", "w", "heads_q", "heads_k", "head_dim", "dim_t", "dim_h", "dim_w", "pairing")] + \
+               [("flags", ctypes.c_uint32), ("base", ctypes.c_double)] + \
+               [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
 
 
 class Conv3dError(RuntimeError):
@@ -124,6 +159,25 @@ def load_library(path: str = LIB_PATH):
     lib.conv3d_version.restype = i32
     lib.conv3d_selftest.argtypes = []
     lib.conv3d_selftest.restype = i32
+    f32 = ctypes.c_float
+    for fn, args, res in (
+            ("linear_plan", [ctypes.POINTER(linear_desc), ctypes.POINTER(vp), ctypes.POINTER(sz)], ctypes.c_int),
+            ("linear_plan_query", [vp, ctypes.POINTER(linear_plan_info)], ctypes.c_int),
+            ("linear_plan_destroy", [vp], None),
+            ("linear_forward", [vp] * 8 + [sz, vp], ctypes.c_int),
+            ("linear_backward_workspace", [vp], sz),
+            ("linear_backward", [vp] * 9 + [sz, vp], ctypes.c_int),
+            ("layernorm", [vp] * 5 + [i64, i32, i64, i64, f32, vp], ctypes.c_int),
+            ("layernorm_bf16", [vp] * 5 + [i64, i32, i64, i64, f32, vp], ctypes.c_int),
+            ("layernorm_backward_workspace", [i64, i32], sz),
+            ("layernorm_backward", [vp] * 8 + [i64, i32, i64, i64, vp, sz, vp], ctypes.c_int),
+            ("layernorm_backward_bf16", [vp] * 8 + [i64, i32, i64, i64, vp, sz, vp], ctypes.c_int),
+            ("rope3d_plan", [ctypes.POINTER(rope3d_desc), ctypes.POINTER(vp)], ctypes.c_int),
+            ("rope3d_plan_destroy", [vp], None),
+            ("rope3d_forward", [vp] * 6 + [i32, vp], ctypes.c_int),
+            ("rope3d_backward", [vp] * 6 + [i32, vp], ctypes.c_int)):
+        getattr(lib, fn).argtypes = args
+        getattr(lib, fn).restype = res
     dp = ctypes.POINTER(ctypes.c_double)
     lib.conv3d_calibrate_scratch_bytes.argtypes = []
     lib.conv3d_calibrate_scratch_bytes.restype = sz
@@ -329,6 +383,227 @@ def groupnorm_silu_noalloc(x, gamma, beta, y, n, thw, c, groups, eps, apply_silu
     _check(load_library().groupnorm_silu_noalloc(_addr(x, "x", ne, dt), _addr(gamma, "gamma", c, dt),
                                                  _addr(beta, "beta", c, dt), _addr(y, "y", ne, dt), n, thw, c,
                                                  groups, float(eps), 1 if apply_silu else 0, _stream(stream)))
+
+
+# ---- the token operators
+
+def _strided_addr(t, what, sizes, strides, dtype):
+    """Device address of a tensor whose elements, at the given sizes and strides
+    (in elements, outermost first) from its first one, lie inside its storage."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.device.type != "cuda":
+        raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is on %s, not on a GPU" % (what, t.device))
+    if t.dtype != dtype:
+        raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is %s, %s expected" % (what, t.dtype, dtype))
+    if any(n == 0 for n in sizes):
+        return t.data_ptr() or None
+    if t.dim() >= 2 and t.dim() == len(sizes):
+        # a view of the same shape has to be laid out as the call reads it
+        for n, have, want in zip(t.shape, t.stride(), strides):
+            if n > 1 and have != want:
+                raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s has strides %s, the call reads %s"
+                                  % (what, tuple(t.stride()), tuple(strides)))
+    elif not t.is_contiguous():
+        raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is not contiguous" % what)
+    last = sum((n - 1) * st for n, st in zip(sizes, strides))
+    have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    if last >= have:
+        raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s holds %d elements, %d needed" % (what, have, last + 1))
+    return t.data_ptr()
+
+
+def _rows_addr(t, what, rows, cols, stride, dtype):
+    return _strided_addr(t, what, (rows, cols), (stride or cols, 1), dtype)
+
+
+def _workspace_bytes(workspace, workspace_bytes, planned=0):
+    if workspace_bytes is not None:
+        return workspace_bytes
+    if workspace is None:
+        return 0
+    return planned if isinstance(workspace, int) else workspace.numel() * workspace.element_size()
+
+
+class LinearPlan:
+    """Owns a linear_plan_t; destroyed with the object."""
+
+    def __init__(self, handle, workspace_bytes, desc):
+        self.handle = handle
+        self.workspace_bytes = workspace_bytes
+        self.desc = desc
+
+    def info(self) -> linear_plan_info:
+        return linear_plan_query(self)
+
+    def __del__(self):
+        if self.handle and _lib is not None:
+            _lib.linear_plan_destroy(self.handle)
+            self.handle = None
+
+
+def make_linear_desc(m, n, k, act=CONV3D_ACT_NONE, flags=0, x_stride=0, y_stride=0, residual_stride=0) -> linear_desc:
+    return linear_desc(m, n, k, act, flags, x_stride, y_stride, residual_stride)
+
+
+def linear_plan(desc: linear_desc) -> LinearPlan:
+    lib = load_library()
+    h = ctypes.c_void_p()
+    ws = ctypes.c_size_t()
+    _check(lib.linear_plan(ctypes.byref(desc), ctypes.byref(h), ctypes.byref(ws)))
+    return LinearPlan(h.value, ws.value, desc)
+
+
+def linear_plan_query(plan: LinearPlan) -> linear_plan_info:
+    info = linear_plan_info()
+    _check(load_library().linear_plan_query(plan.handle, ctypes.byref(info)))
+    return info
+
+
+def linear_plan_destroy(plan: LinearPlan) -> None:
+    if plan.handle:
+        load_library().linear_plan_destroy(plan.handle)
+        plan.handle = None
+
+
+def linear_forward(plan: LinearPlan, x, w, bias, residual, y, preact=None, workspace=None, workspace_bytes=None,
+                   stream=None) -> None:
+    """Enqueue y = act(x w^T + bias) + residual (and preact, the value before act) on ``stream``."""
+    d, dt = plan.desc, _elem_dtype(plan.desc.flags & CONV3D_F_BF16)
+    _check(load_library().linear_forward(
+        plan.handle, _rows_addr(x, "x", d.m, d.k, d.x_stride, dt), _addr(w, "w", d.n * d.k, dt),
+        _addr(bias, "bias", d.n, dt), _rows_addr(residual, "residual", d.m, d.n, d.residual_stride, dt),
+        _rows_addr(y, "y", d.m, d.n, d.y_stride, dt), _rows_addr(preact, "preact", d.m, d.n, 0, dt),
+        _addr(workspace, "workspace"), _workspace_bytes(workspace, workspace_bytes, plan.workspace_bytes),
+        _stream(stream)))
+
+
+def linear_backward_workspace(plan: LinearPlan) -> int:
+    return load_library().linear_backward_workspace(plan.handle)
+
+
+def linear_backward(plan: LinearPlan, dy, x, w, preact, dx, dw, dbias, workspace, workspace_bytes=None,
+                    stream=None) -> None:
+    """Enqueue the gradients dx, dw and dbias (each may be None) of one product on ``stream``."""
+    d, dt = plan.desc, _elem_dtype(plan.desc.flags & CONV3D_F_BF16)
+    _check(load_library().linear_backward(
+        plan.handle, _rows_addr(dy, "dy", d.m, d.n, d.y_stride, dt), _rows_addr(x, "x", d.m, d.k, d.x_stride, dt),
+        _addr(w, "w", d.n * d.k, dt), _rows_addr(preact, "preact", d.m, d.n, 0, dt),
+        _rows_addr(dx, "dx", d.m, d.k, d.x_stride, dt), _addr(dw, "dw", d.n * d.k, dt), _addr(dbias, "dbias", d.n, dt),
+        _addr(workspace, "workspace"),
+        _workspace_bytes(workspace, workspace_bytes, linear_backward_workspace(plan)), _stream(stream)))
+
+
+def layernorm(x, gamma, beta, y, stats, rows, c, eps, x_stride=0, y_stride=0, stream=None, bf16=False) -> None:
+    """Enqueue y = LayerNorm(x) over the c channels of each row on ``stream``;
+    gamma, beta and stats (fp32 [rows][2]: mean, 1 / sqrt(var + eps)) may be None."""
+    lib, dt = load_library(), _elem_dtype(bf16)
+    import torch
+    fn = lib.layernorm_bf16 if bf16 else lib.layernorm
+    _check(fn(_rows_addr(x, "x", rows, c, x_stride, dt), _addr(gamma, "gamma", c, dt), _addr(beta, "beta", c, dt),
+              _rows_addr(y, "y", rows, c, y_stride, dt), _addr(stats, "stats", 2 * rows, torch.float32), rows, c,
+              x_stride, y_stride, float(eps), _stream(stream)))
+
+
+def layernorm_bf16(x, gamma, beta, y, stats, rows, c, eps, x_stride=0, y_stride=0, stream=None) -> None:
+    """layernorm with bf16 x, gamma, beta and y."""
+    layernorm(x, gamma, beta, y, stats, rows, c, eps, x_stride, y_stride, stream, bf16=True)
+
+
+def layernorm_backward_workspace(rows, c) -> int:
+    return load_library().layernorm_backward_workspace(rows, c)
+
+
+def layernorm_backward(dy, x, gamma, stats, dres, dx, dgamma, dbeta, rows, c, workspace, x_stride=0, y_stride=0,
+                       workspace_bytes=None, stream=None, bf16=False) -> None:
+    """Enqueue dx (+ dres), dgamma and dbeta of layernorm on ``stream``; gamma,
+    dres, dgamma and dbeta may be None."""
+    lib, dt = load_library(), _elem_dtype(bf16)
+    import torch
+    fn = lib.layernorm_backward_bf16 if bf16 else lib.layernorm_backward
+    _check(fn(_rows_addr(dy, "dy", rows, c, y_stride, dt), _rows_addr(x, "x", rows, c, x_stride, dt),
+              _addr(gamma, "gamma", c, dt), _addr(stats, "stats", 2 * rows, torch.float32),
+              _rows_addr(dres, "dres", rows, c, x_stride, dt), _rows_addr(dx, "dx", rows, c, x_stride, dt),
+              _addr(dgamma, "dgamma", c, dt), _addr(dbeta, "dbeta", c, dt), rows, c, x_stride, y_stride,
+              _addr(workspace, "workspace"),
+              _workspace_bytes(workspace, workspace_bytes, layernorm_backward_workspace(rows, c)), _stream(stream)))
+
+
+def layernorm_backward_bf16(dy, x, gamma, stats, dres, dx, dgamma, dbeta, rows, c, workspace, x_stride=0, y_stride=0,
+                            workspace_bytes=None, stream=None) -> None:
+    """layernorm_backward with bf16 tensors (stats and workspace fp32 as before)."""
+    layernorm_backward(dy, x, gamma, stats, dres, dx, dgamma, dbeta, rows, c, workspace, x_stride, y_stride,
+                       workspace_bytes, stream, bf16=True)
+
+
+class RopePlan:
+    """Owns a rope3d_plan_t; destroyed with the object."""
+
+    def __init__(self, handle, desc):
+        self.handle = handle
+        self.desc = desc
+
+    def __del__(self):
+        if self.handle and _lib is not None:
+            _lib.rope3d_plan_destroy(self.handle)
+            self.handle = None
+
+
+def make_rope3d_desc(n, t, h, w, heads_q, heads_k, head_dim, dims, base=10000.0, pairing=ROPE3D_PAIR_ADJACENT,
+                     flags=0, q_stride=(0, 0, 0), k_stride=(0, 0, 0), q_out_stride=(0, 0, 0),
+                     k_out_stride=(0, 0, 0)) -> rope3d_desc:
+    """dims: the elements of a head that turn with time, height and width;
+    strides: elements between samples, tokens and heads (all 0: contiguous)."""
+    arr = ctypes.c_int64 * 3
+    return rope3d_desc(n, t, h, w, heads_q, heads_k, head_dim, *dims, pairing, flags, base, arr(*q_stride),
+                       arr(*k_stride), arr(*q_out_stride), arr(*k_out_stride))
+
+
+def rope3d_plan(desc: rope3d_desc) -> RopePlan:
+    h = ctypes.c_void_p()
+    _check(load_library().rope3d_plan(ctypes.byref(desc), ctypes.byref(h)))
+    return RopePlan(h.value, desc)
+
+
+def rope3d_plan_destroy(plan: RopePlan) -> None:
+    if plan.handle:
+        load_library().rope3d_plan_destroy(plan.handle)
+        plan.handle = None
+
+
+def _rope_call(name, plan, q, k, q_out, k_out, positions, t_offset, stream, strides):
+    import torch
+    d = plan.desc
+    tokens, dt = d.t * d.h * d.w, _elem_dtype(d.flags & CONV3D_F_BF16)
+
+    def addr(t, what, heads, stride):
+        stride = tuple(stride)
+        if not any(stride):
+            stride = (tokens * heads * d.head_dim, heads * d.head_dim, d.head_dim)
+        return _strided_addr(t, what, (d.n, tokens, heads, d.head_dim), stride + (1,), dt)
+
+    if d.heads_k == 0:
+        k = k_out = None
+    if not d.flags & CONV3D_F_POSITIONS:
+        positions = None
+    _check(getattr(load_library(), name)(
+        plan.handle, addr(q, "q", d.heads_q, strides[0]), addr(k, "k", d.heads_k, strides[1]),
+        addr(q_out, "q_out", d.heads_q, strides[2]), addr(k_out, "k_out", d.heads_k, strides[3]),
+        _addr(positions, "positions", d.n * tokens * 3, torch.int32), t_offset, _stream(stream)))
+
+
+def rope3d_forward(plan: RopePlan, q, k, q_out, k_out, positions=None, t_offset=0, stream=None) -> None:
+    """Enqueue the rotation of q into q_out and k into k_out on ``stream``."""
+    d = plan.desc
+    _rope_call("rope3d_forward", plan, q, k, q_out, k_out, positions, t_offset, stream,
+               (d.q_stride, d.k_stride, d.q_out_stride, d.k_out_stride))
+
+
+def rope3d_backward(plan: RopePlan, dq_out, dk_out, dq, dk, positions=None, t_offset=0, stream=None) -> None:
+    """Enqueue the gradient of rope3d_forward (strides: those of the outputs, then of the inputs)."""
+    d = plan.desc
+    _rope_call("rope3d_backward", plan, dq_out, dk_out, dq, dk, positions, t_offset, stream,
+               (d.q_out_stride, d.k_out_stride, d.q_stride, d.k_stride))
 
 
 def conv3d_calibrate_scratch_bytes() -> int:

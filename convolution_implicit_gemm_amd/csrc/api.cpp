@@ -13,6 +13,7 @@
 
 #include "c3d_internal.h"
 #include "conv3d.h"
+#include "token_internal.h"
 
 namespace {
 
@@ -140,6 +141,18 @@ Decomp decompose(const c3d::TileCfg &t, int64_t tiles, int niter, int mode) {
 }
 
 }  // namespace
+
+conv3d_status c3d::api_fail(conv3d_status s, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+conv3d_status c3d::api_ok() { return ok(); }
+
+conv3d_status c3d::api_check_device() { return check_device(); }
 
 struct conv3d_plan_s {
     conv3d_desc d;

@@ -1,0 +1,383 @@
+// Device helpers of the matrix-product kernels (linear.hip): operand tiles in
+// LDS for both storage orders, their MFMA fragments, activations, and the
+// epilogue.
+#pragma once
+
+#include "igemm_common.h"
+#include "token_internal.h"
+
+namespace c3d {
+
+constexpr int kGemmBK = 32;                 // contraction per stage
+constexpr int kGemmRow = kGemmBK * 2;       // bytes of one LDS row, contraction contiguous
+
+// z -> act(z), fp32.  GELU (erf form) through Abramowitz and Stegun 7.1.26,
+// erf(x) = 1 - (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x),
+// absolute error 1.5e-7; the tanh form as z * sigmoid(2u).
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kGeluA = 0.797884560802865356f, kGeluB = 0.044715f;
+
+__device__ __forceinline__ float sigmoid_f(float v) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * v));
+}
+// (Phi(z), exp(-z^2 / 2)) of the standard normal distribution
+__device__ __forceinline__ float normal_cdf(float z, float &ex) {
+    const float x = fabsf(z) * 0.707106781186547524f;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+    ex = __builtin_amdgcn_exp2f(-kLog2e * x * x);
+    float q = fmaf(t, 1.061405429f, -1.453152027f);
+    q = fmaf(t, q, 1.421413741f);
+    q = fmaf(t, q, -0.284496736f);
+    q = fmaf(t, q, 0.254829592f);
+    const float tail = 0.5f * q * t * ex;  // Phi(-|z|)
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+template <int ACT>
+__device__ __forceinline__ float act_f(float z) {
+    if constexpr (ACT == CONV3D_ACT_SILU) return z * sigmoid_f(z);
+    if constexpr (ACT == CONV3D_ACT_GELU) {
+        float ex;
+        return z * normal_cdf(z, ex);
+    }
+    if constexpr (ACT == CONV3D_ACT_GELU_TANH) return z * sigmoid_f(2.0f * kGeluA * fmaf(kGeluB * z, z * z, z));
+    return z;
+}
+// act'(z).  The arguments whose powers could overflow are bounded where the
+// derivative is 0 or 1 to the last bit anyway.
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+    if constexpr (ACT == CONV3D_ACT_NONE) return 1.0f;
+    z = fminf(fmaxf(z, -1e4f), 1e4f);
+    if constexpr (ACT == CONV3D_ACT_SILU) {
+        const float s = sigmoid_f(z);
+        return s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    if constexpr (ACT == CONV3D_ACT_GELU) {
+        float ex;
+        const float cdf = normal_cdf(z, ex);
+        return fmaf(z * 0.398942280401432678f, ex, cdf);
+    }
+    const float s = sigmoid_f(2.0f * kGeluA * fmaf(kGeluB * z, z * z, z));
+    return s * fmaf(z * (1.0f - s), 2.0f * kGeluA * fmaf(3.0f * kGeluB * z, z, 1.0f), 1.0f);
+}
+
+// Calls f(std::integral_constant<int, ACT>) for the activation chosen at run time.
+template <typename F>
+__device__ __forceinline__ void act_switch(int act, F &&f) {
+    switch (act) {
+        case CONV3D_ACT_SILU: f(std::integral_constant<int, CONV3D_ACT_SILU>{}); break;
+        case CONV3D_ACT_GELU: f(std::integral_constant<int, CONV3D_ACT_GELU>{}); break;
+        case CONV3D_ACT_GELU_TANH: f(std::integral_constant<int, CONV3D_ACT_GELU_TANH>{}); break;
+        default: f(std::integral_constant<int, CONV3D_ACT_NONE>{}); break;
+    }
+}
+
+// ---- operand tiles in LDS.  An operand tile is ROWS output rows (or columns)
+// x 32 of the contraction, ROWS x 64 bytes in either order:
+//   contraction contiguous (TR = false): ROWS rows of 64 bytes; 16-byte chunk c
+//     of row r sits at chunk c ^ swz<32>(r);
+//   transposed (TR = true): 32 rows (one per contraction index) of 2 ROWS
+//     bytes; chunk c of row r sits at chunk c ^ ((r & 3) << 2), so that the 4
+//     rows x 64 bytes that a half-wave's transposing reads take fill all banks.
+// Loads are 16 bytes per lane, 1 KiB per instruction, straight into LDS; the
+// swizzle is applied to the global side.
+
+// One operand as a workgroup reads it: a moving buffer resource and the lane's
+// offsets for its NI load instructions per stage.
+template <bool TR, int ROWS, int NI>
+struct Operand {
+    const _Float16 *base;   // TR: row it * 32 of the tile's columns; else the tile's first row
+    int64_t stride;
+    int left;               // contraction not yet loaded, from the current stage on
+    int ncols;              // TR: columns of the tile inside the matrix
+    uint32_t records;
+    uint32_t voff[NI];
+    int kc[NI];             // !TR: the contraction index of the lane's chunk within the stage
+
+    // instruction ids: first, first + step, ... (NI of them)
+    __device__ __forceinline__ void init(const _Float16 *m, int64_t stride_, int row0, int rows_total, int k0, int kend,
+                                         int first, int step, int lane) {
+        stride = stride_;
+        left = kend - k0;
+        const int rows = rows_total - row0 < ROWS ? rows_total - row0 : ROWS;
+        ncols = rows;
+        if constexpr (TR) {
+            base = m + (int64_t)k0 * stride + row0;
+            constexpr int CH = ROWS / 8;
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                const int lin = (first + j * step) * 64 + lane;
+                const int r = lin / CH, c = (lin % CH) ^ ((r & 3) << 2);
+                voff[j] = c * 8 < ncols ? (uint32_t)(r * (int)stride + c * 8) * 2u : kOOB;
+                kc[j] = 0;
+            }
+        } else {
+            base = m + (int64_t)row0 * stride + k0;
+            records = (uint32_t)((rows - 1) * (int)stride + left) * 2u;
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                const int lin = (first + j * step) * 64 + lane;
+                const int r = lin >> 2, c = (lin & 3) ^ swz<kGemmBK>(r);
+                kc[j] = c * 8;
+                voff[j] = r < rows ? (uint32_t)(r * (int)stride + c * 8) * 2u : kOOB;
+            }
+        }
+    }
+    // Load instructions J0 .. J0 + CNT - 1 of the current stage into `lds` (the
+    // operand's stage buffer); the contraction past its end reads as zeros.
+    template <int J0, int CNT>
+    __device__ __forceinline__ void load(char *lds, int first, int step, uint32_t soff) {
+        if constexpr (TR) {
+            const int rows = left < kGemmBK ? left : kGemmBK;
+            const uint32_t rec = rows > 0 ? (uint32_t)((rows - 1) * (int)stride + ncols) * 2u : 0u;
+            const buf_rsrc r = make_rsrc(base, rec);
+#pragma unroll
+            for (int j = J0; j < J0 + CNT; ++j) dma16(r, lds + (first + j * step) * 1024, voff[j], 0u);
+        } else {
+            const buf_rsrc r = make_rsrc(base, records);
+#pragma unroll
+            for (int j = J0; j < J0 + CNT; ++j)
+                dma16(r, lds + (first + j * step) * 1024, kc[j] < left ? voff[j] : kOOB, soff);
+        }
+    }
+    __device__ __forceinline__ void advance() {
+        left -= kGemmBK;
+        if constexpr (TR) base += kGemmBK * stride;
+    }
+};
+
+// Byte offsets of a lane's MFMA fragments within an operand's stage buffer.
+// A fragment covers 32 output rows (from row0, a multiple of 32) x 16 of the
+// contraction: lane l holds output row l % 32, contraction 8 (l / 32) .. + 7.
+template <bool TR, int ROWS, int NF>
+struct Fragments {
+    int off[TR ? NF : 2];
+    __device__ __forceinline__ void init(int row0, int lane) {
+        if constexpr (TR) {
+            const int j = lane & 15, g = (lane >> 4) & 1, r = (lane >> 5) * 8 + (j >> 2);
+#pragma unroll
+            for (int i = 0; i < NF; ++i) {
+                const int chunk = ((row0 + i * 32 + 16 * g) >> 3) + ((j & 3) >> 1);
+                off[i] = r * ROWS * 2 + ((chunk ^ ((j >> 2) << 2)) << 4) + (j & 1) * 8;
+            }
+        } else {
+            const int r = lane & 31, hi = lane >> 5;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) off[kk] = (row0 + r) * kGemmRow + (((2 * kk + hi) ^ swz<kGemmBK>(r)) * 16);
+        }
+    }
+    // fragment i of k-step KK
+    template <int KK>
+    __device__ __forceinline__ half8_t read(const char *lds, int i) const {
+        if constexpr (TR) {
+#if defined(__HIP_DEVICE_COMPILE__)
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s16x4 lds_s4;
+            const char *a = lds + off[i] + KK * 16 * ROWS * 2;
+            const half4_t lo = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)a));
+            const half4_t hi =
+                __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(a + 4 * ROWS * 2)));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#else
+            return half8_t{};
+#endif
+        } else {
+            return *reinterpret_cast<const half8_t *>(lds + off[KK] + i * 32 * kGemmRow);
+        }
+    }
+};
+
+// 16-byte buffer store; out-of-range stores are dropped.
+__device__ __forceinline__ void gemm_store16(buf_rsrc r, uint32_t off, half8_t v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, off, 0, 0);
+#else
+    (void)r;
+    (void)off;
+    (void)v;
+#endif
+}
+
+__device__ __forceinline__ void gemm_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+template <int N>
+__device__ __forceinline__ void gemm_wait_loads() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A 16-bit output tile in LDS, rows of BN elements: 16-byte chunk c of row v at
+// chunk c ^ (v mod chunks), and rows with bit 4 set keep the two 8-byte halves
+// of a chunk swapped, so that both the fragments' 8-byte accesses (32 rows at
+// one chunk) and the rows' 16-byte accesses spread over all banks.
+template <int BN>
+__device__ __forceinline__ int tile_chunk(int v, int c) {
+    return v * BN * 2 + ((c ^ (v & (BN / 8 - 1))) << 4);
+}
+
+// Tile rows between LDS and global memory in whole rows, 16 bytes per lane.
+template <int BM, int BN, int THREADS>
+__device__ __forceinline__ void store_rows(const char *smem, _Float16 *out, int64_t stride, int rows, int cols) {
+    constexpr int CH = BN / 8;
+    const buf_rsrc r = make_rsrc(out, (uint32_t)((rows - 1) * (int)stride + cols) * 2u);
+#pragma unroll
+    for (int k = 0; k < BM * CH / THREADS; ++k) {
+        const int lin = k * THREADS + threadIdx.x;
+        const int v = lin / CH, c = lin % CH;
+        half8_t h = *reinterpret_cast<const half8_t *>(smem + tile_chunk<BN>(v, c));
+        if (v & 16) h = __builtin_shufflevector(h, h, 4, 5, 6, 7, 0, 1, 2, 3);
+        gemm_store16(r, v < rows && c * 8 < cols ? (uint32_t)(v * (int)stride + c * 8) * 2u : kOOB, h);
+    }
+}
+// The residual's rows into the same places.  The 8-byte halves are not swapped
+// (they arrive as they are); the fragments read them so.
+template <int BM, int BN, int THREADS>
+__device__ __forceinline__ void load_rows(char *smem, const _Float16 *in, int64_t stride, int rows, int cols) {
+    constexpr int CH = BN / 8;
+    const buf_rsrc r = make_rsrc(in, (uint32_t)((rows - 1) * (int)stride + cols) * 2u);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int k = 0; k < BM * CH / THREADS; ++k) {
+        const int lin = k * THREADS + threadIdx.x;
+        const int v = lin / CH, c = (lin % CH) ^ (v & (CH - 1));
+        dma16(r, smem + (k * THREADS + wave * 64) * 16,
+              v < rows && c * 8 < cols ? (uint32_t)(v * (int)stride + c * 8) * 2u : kOOB, 0u);
+    }
+}
+
+// Epilogue of a whole tile: z = acc (the bias is in it), stored when asked
+// for; y = act(z) + residual; each rounded once.  Staged through LDS so that it
+// leaves in whole rows.  Lane's register 4g + e of fragment (i, j): column
+// WN * wni + 32 i + 8 g + 4 (lane / 32) + e, row WM * wmi + 32 j + lane % 32.
+// Every LDS buffer of the K loop is free, and every wave is past it.
+template <typename E, int BM, int BN, int WM, int WN, int THREADS>
+__device__ __forceinline__ void gemm_store_tile(const GemmParams &p, f32x16 (&acc)[WN / 32][WM / 32], char *smem, int m0,
+                                                int n0, int wmi, int wni, int lane) {
+    constexpr int TN = WN / 32, TM = WM / 32;
+    const int rows = p.M - m0 < BM ? p.M - m0 : BM, cols = p.N - n0 < BN ? p.N - n0 : BN;
+    const int rrow = lane & 31, rhi = lane >> 5;
+    auto stage = [&](auto resc) {
+        constexpr bool RES = decltype(resc)::value;
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int j = 0; j < TM; ++j) {
+                    const int v = wmi * WM + j * 32 + rrow;
+                    char *chunk = smem + tile_chunk<BN>(v, wni * (WN / 8) + i * 4 + g);
+                    half4_t h;
+                    if constexpr (RES) {
+                        const half4_t r = *reinterpret_cast<const half4_t *>(chunk + rhi * 8);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) h[e] = from_f32<E>(acc[i][j][4 * g + e] + to_f32<E>(r[e]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) h[e] = from_f32<E>(acc[i][j][4 * g + e]);
+                    }
+                    *reinterpret_cast<half4_t *>(chunk + ((rhi ^ ((v >> 4) & 1)) << 3)) = h;
+                }
+        gemm_barrier();
+    };
+    if (p.z) {
+        stage(std::false_type{});
+        store_rows<BM, BN, THREADS>(smem, p.z + (int64_t)m0 * p.N + n0, p.N, rows, cols);
+        gemm_barrier();
+    }
+    if (p.res) load_rows<BM, BN, THREADS>(smem, p.res + (int64_t)m0 * p.res_stride + n0, p.res_stride, rows, cols);
+    act_switch(p.act, [&](auto ac) {
+        constexpr int ACT = decltype(ac)::value;
+        if constexpr (ACT != CONV3D_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[i][j][e] = act_f<ACT>(acc[i][j][e]);
+        }
+    });
+    if (p.res) {
+        gemm_wait_loads<0>();
+        gemm_barrier();
+        stage(std::true_type{});
+    } else {
+        stage(std::false_type{});
+    }
+    store_rows<BM, BN, THREADS>(smem, p.y + (int64_t)m0 * p.y_stride + n0, p.y_stride, rows, cols);
+}
+
+// The bias of a lane's columns as the accumulators' start value.
+template <typename E, int WM, int WN>
+__device__ __forceinline__ void gemm_init_acc(const GemmParams &p, f32x16 (&acc)[WN / 32][WM / 32], bool bias, int col0,
+                                              int lane) {
+    const buf_rsrc rb = make_rsrc(bias ? p.bias : p.p, bias ? (uint32_t)p.N * 2u : 0u);
+#pragma unroll
+    for (int i = 0; i < WN / 32; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int co = col0 + i * 32 + 8 * g + 4 * (lane >> 5);
+            const half4_t b = load8(rb, bias && co < p.N ? (uint32_t)co * 2u : kOOB);
+#pragma unroll
+            for (int j = 0; j < WM / 32; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][4 * g + e] = to_f32<E>(b[e]);
+        }
+}
+
+// A K-piece's fp32 partial tile, in fragment order.
+template <int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void gemm_store_partial(const GemmParams &p, const f32x16 (&acc)[WN / 32][WM / 32], int slot,
+                                                   int wave, int lane) {
+    constexpr int TN = WN / 32, TM = WM / 32;
+    f32x4 *pp = reinterpret_cast<f32x4 *>(p.partial + (size_t)slot * (BM * BN));
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                f32x4 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
+                pp[(((wave * TN + i) * TM + j) * 4 + g) * 64 + lane] = v;
+            }
+}
+
+// Work unit u: a whole tile (slot < 0) or K-piece `slot` of a split tile, and
+// its range of stages.  Tiles are walked in groups of kGemmGroup rows of tiles,
+// down the rows first: the workgroups that an XCD runs at once (a contiguous
+// range of units) then share both operands' tiles in its L2.
+constexpr int kGemmGroup = 8;
+__device__ __forceinline__ void gemm_unit(const GemmParams &p, int u, int &m_tile, int &n_tile, int &it0, int &it1,
+                                          int &slot) {
+    it0 = 0;
+    it1 = p.niter;
+    slot = -1;
+    int tile = u;
+    if (u >= p.dp_tiles) {
+        slot = u - p.dp_tiles;
+        const int piece = slot % p.sk_pieces;
+        tile = p.dp_tiles + slot / p.sk_pieces;
+        it0 = (int)((int64_t)p.niter * piece / p.sk_pieces);
+        it1 = (int)((int64_t)p.niter * (piece + 1) / p.sk_pieces);
+    }
+    const int per_group = kGemmGroup * p.n_tiles;
+    const int g0 = tile / per_group * kGemmGroup;
+    const int rows = p.m_tiles - g0 < kGemmGroup ? p.m_tiles - g0 : kGemmGroup;
+    const int r = tile - g0 * p.n_tiles;
+    m_tile = g0 + r % rows;
+    n_tile = r / rows;
+}
+// Workgroups are dealt to the XCDs in turn; XCD x takes the x-th contiguous
+// range of the units [first, first + count).
+__device__ __forceinline__ int xcd_range(int b, int count) {
+    const int per = count >> 3, rem = count & 7, x = b & 7;
+    return x * per + (x < rem ? x : rem) + (b >> 3);
+}
+
+}  // namespace c3d

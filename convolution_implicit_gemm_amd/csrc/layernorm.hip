@@ -1,0 +1,303 @@
+// Layer norm over the channels of token rows, forward and backward, gfx950.
+//
+//   forward:  mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps),
+//             y = (x - mu) r gamma + beta
+//   backward: g = dy gamma, xh = (x - mu) r,
+//             dx = r (g - mean(g) - xh mean(g xh)) (+ dres),
+//             dgamma = sum over rows of dy xh, dbeta = sum over rows of dy
+//
+// Both are streams over HBM (2 reads and writes of a row forward, 3 or 4
+// backward), so a row is read once and stays in registers: a team of WPR waves
+// holds one row as NV 16-byte vectors per lane, and the second moment is taken
+// about the mean in a second sweep over the registers (no cancellation, at no
+// traffic).  Sums are fp32; y, dx and the weight gradients are rounded once.
+// The weights' gradients: every team walks rows blockwise and keeps its
+// columns' sums in registers, the block adds its teams through LDS and writes
+// one fp32 partial, and a second kernel adds the blocks in a fixed order (no
+// atomics: the result does not depend on the order blocks finish in).
+#include "elem16.h"
+#include "token_internal.h"
+
+namespace c3d {
+
+namespace {
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+    return v;
+}
+
+// Sum over the WPR waves of a row's team.  slot: this team's 2 x WPR floats of
+// LDS; `turn` alternates, so that one barrier per sum is enough.
+template <int WPR>
+__device__ __forceinline__ float team_sum(float v, float *slot, int wave_in_team, int turn) {
+    v = wave_sum(v);
+    if constexpr (WPR > 1) {
+        float *s = slot + turn * WPR;
+        if ((threadIdx.x & 63) == 0) s[wave_in_team] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) v += s[i];
+    }
+    return v;
+}
+
+template <typename E>
+__device__ __forceinline__ e16x8_t load_vec(const _Float16 *p) {
+    return *reinterpret_cast<const e16x8_t *>(p);
+}
+
+// Threads of a block: one row's team, or four one-wave teams.
+template <int WPR>
+constexpr int ln_threads() {
+    return (WPR > 4 ? WPR : 4) * 64;
+}
+
+template <typename E, int NV, int WPR>
+__global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_kernel(LnParams p) {
+    constexpr int TEAMS = ln_threads<WPR>() / 64 / WPR;
+    __shared__ float red[TEAMS * 2 * WPR];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int team = wave / WPR, wt = wave % WPR;
+    const int first = (wt * 64 + lane) * 8;
+    float *slot = red + team * 2 * WPR;
+    const float inv_c = 1.0f / (float)p.c;
+    for (int64_t row0 = (int64_t)blockIdx.x * TEAMS; row0 < p.rows; row0 += (int64_t)gridDim.x * TEAMS) {
+        const int64_t row = row0 + team;
+        const bool live = row < p.rows;  // a team past the end keeps the barriers' count
+        e16x8_t v[NV];
+        const _Float16 *xr = p.x + row * p.x_stride;
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = first + i * WPR * 512;
+            v[i] = live && c < p.c ? load_vec<E>(xr + c) : e16x8_t{};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += to_f32<E>(v[i][e]);
+        }
+        const float mean = team_sum<WPR>(s, slot, wt, 0) * inv_c;
+        float s2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (first + i * WPR * 512 < p.c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float d = to_f32<E>(v[i][e]) - mean;
+                    s2 = fmaf(d, d, s2);
+                }
+        const float rstd = 1.0f / sqrtf(team_sum<WPR>(s2, slot, wt, 1) * inv_c + p.eps);
+        if (!live) continue;
+        _Float16 *yr = p.y + row * p.y_stride;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = first + i * WPR * 512;
+            if (c >= p.c) continue;
+            const e16x8_t ga = p.gamma ? load_vec<E>(p.gamma + c) : e16x8_t{};
+            const e16x8_t be = p.beta ? load_vec<E>(p.beta + c) : e16x8_t{};
+            e16x8_t o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float a = p.gamma ? rstd * to_f32<E>(ga[e]) : rstd;
+                o[e] = from_f32<E>(fmaf(to_f32<E>(v[i][e]) - mean, a, to_f32<E>(be[e])));
+            }
+            *reinterpret_cast<e16x8_t *>(yr + c) = o;
+        }
+        if (p.stats && wt == 0 && lane == 0) p.stats[row] = make_float2(mean, rstd);
+    }
+}
+
+template <typename E, int NV, int WPR>
+__global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGradParams p) {
+    constexpr int TEAMS = ln_threads<WPR>() / 64 / WPR;
+    __shared__ float red[TEAMS * 2 * WPR];
+    __shared__ float join[TEAMS > 1 ? NV * WPR * 512 : 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int team = wave / WPR, wt = wave % WPR;
+    const int first = (wt * 64 + lane) * 8;
+    float *slot = red + team * 2 * WPR;
+    const float inv_c = 1.0f / (float)p.c;
+    e16x8_t ga[NV];
+    float dg[NV][8], db[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = first + i * WPR * 512;
+        ga[i] = p.gamma && c < p.c ? load_vec<E>(p.gamma + c) : e16x8_t{};
+        for (int e = 0; e < 8; ++e) {
+            if (!p.gamma) ga[i][e] = from_f32<E>(1.0f);
+            dg[i][e] = db[i][e] = 0.0f;
+        }
+    }
+    for (int64_t row0 = (int64_t)blockIdx.x * TEAMS; row0 < p.rows; row0 += (int64_t)gridDim.x * TEAMS) {
+        const int64_t row = row0 + team;
+        const bool live = row < p.rows;
+        const _Float16 *xr = p.x + row * p.x_stride, *gr = p.dy + row * p.y_stride;
+        const float2 st = live ? p.stats[row] : make_float2(0.0f, 0.0f);
+        e16x8_t xv[NV], gv[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = first + i * WPR * 512;
+            const bool in = live && c < p.c;
+            xv[i] = in ? load_vec<E>(xr + c) : e16x8_t{};
+            gv[i] = in ? load_vec<E>(gr + c) : e16x8_t{};
+        }
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (live && first + i * WPR * 512 < p.c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float xh = (to_f32<E>(xv[i][e]) - st.x) * st.y, d = to_f32<E>(gv[i][e]);
+                    const float g = d * to_f32<E>(ga[i][e]);
+                    s1 += g;
+                    s2 = fmaf(g, xh, s2);
+                    dg[i][e] = fmaf(d, xh, dg[i][e]);
+                    db[i][e] += d;
+                }
+        s1 = team_sum<WPR>(s1, slot, wt, 0) * inv_c;
+        s2 = team_sum<WPR>(s2, slot, wt, 1) * inv_c;
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = first + i * WPR * 512;
+            if (c >= p.c) continue;
+            const e16x8_t rv = p.dres ? load_vec<E>(p.dres + row * p.x_stride + c) : e16x8_t{};
+            e16x8_t o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xh = (to_f32<E>(xv[i][e]) - st.x) * st.y;
+                const float g = to_f32<E>(gv[i][e]) * to_f32<E>(ga[i][e]);
+                o[e] = from_f32<E>(fmaf(st.y, g - s1 - xh * s2, to_f32<E>(rv[e])));
+            }
+            *reinterpret_cast<e16x8_t *>(p.dx + row * p.x_stride + c) = o;
+        }
+    }
+    if (!p.part) return;
+    float *out = p.part + (int64_t)blockIdx.x * 2 * p.c;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        if constexpr (TEAMS > 1) {  // add the teams in turn
+            for (int t = 0; t < TEAMS; ++t) {
+                __syncthreads();
+                if (team == t)
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float *j = join + first + i * WPR * 512 + e;
+                            const float v = which ? db[i][e] : dg[i][e];
+                            *j = t == 0 ? v : *j + v;
+                        }
+            }
+            __syncthreads();
+            for (int c = threadIdx.x; c < p.c; c += ln_threads<WPR>()) out[which * p.c + c] = join[c];
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = first + i * WPR * 512;
+                if (c < p.c)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) out[which * p.c + c + e] = which ? db[i][e] : dg[i][e];
+            }
+        }
+    }
+}
+
+// Column sums of fp32 partials [rows][cols]: a block takes 16 columns, 16
+// threads per column add every 16th row, then the 16 sums in order.
+template <typename E>
+__global__ __launch_bounds__(256) void column_sum_kernel(const float *part, int rows, int cols, _Float16 *out0,
+                                                         _Float16 *out1, int split) {
+    __shared__ float s[16][17];
+    const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4;
+    const int c = blockIdx.x * 16 + tc;
+    float v = 0.0f;
+    if (c < cols)
+        for (int r = tr; r < rows; r += 16) v += part[(int64_t)r * cols + c];
+    s[tr][tc] = v;
+    __syncthreads();
+    if (tr == 0 && c < cols) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t += s[i][tc];
+        _Float16 *o = c < split ? out0 : out1;
+        if (o) o[c < split ? c : c - split] = from_f32<E>(t);
+    }
+}
+
+__global__ __launch_bounds__(256) void zero_rows_kernel(_Float16 *y, int64_t rows, int width, int64_t stride) {
+    const int64_t total = rows * width;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256)
+        y[i / width * stride + i % width] = (_Float16)0.0f;
+}
+
+// (vectors per lane, waves per row) of a channel count.
+template <typename F>
+hipError_t ln_dispatch(int c, F &&f) {
+    using std::integral_constant;
+    if (c <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    if (c <= 1024) return f(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+    if (c <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    if (c <= 4096) return f(integral_constant<int, 2>{}, integral_constant<int, 4>{});
+    if (c <= 8192) return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+    return f(integral_constant<int, 2>{}, integral_constant<int, 16>{});
+}
+
+int ln_teams(int c) { return c <= 2048 ? 4 : 1; }
+
+}  // namespace
+
+hipError_t launch_layernorm(const LnParams &p, hipStream_t s) {
+    const int64_t want = (p.rows + ln_teams(p.c) - 1) / ln_teams(p.c);
+    const unsigned grid = (unsigned)(want < 65536 ? want : 65536);
+    return ln_dispatch(p.c, [&](auto nv, auto wpr) {
+        constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
+        if (p.bf16)
+            hipLaunchKernelGGL((layernorm_kernel<__bf16, NV, WPR>), dim3(grid), dim3(ln_threads<WPR>()), 0, s, p);
+        else
+            hipLaunchKernelGGL((layernorm_kernel<_Float16, NV, WPR>), dim3(grid), dim3(ln_threads<WPR>()), 0, s, p);
+        return hipGetLastError();
+    });
+}
+
+int32_t ln_grad_blocks(int64_t rows, int32_t c) {
+    const int64_t want = (rows + ln_teams(c) - 1) / ln_teams(c);
+    return (int32_t)(want < 512 ? want : 512);
+}
+
+hipError_t launch_layernorm_grad(const LnGradParams &p, hipStream_t s) {
+    const unsigned grid = (unsigned)ln_grad_blocks(p.rows, p.c);
+    hipError_t e = ln_dispatch(p.c, [&](auto nv, auto wpr) {
+        constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
+        if (p.bf16)
+            hipLaunchKernelGGL((layernorm_grad_kernel<__bf16, NV, WPR>), dim3(grid), dim3(ln_threads<WPR>()), 0, s, p);
+        else
+            hipLaunchKernelGGL((layernorm_grad_kernel<_Float16, NV, WPR>), dim3(grid), dim3(ln_threads<WPR>()), 0, s,
+                               p);
+        return hipGetLastError();
+    });
+    if (e != hipSuccess || !p.part) return e;
+    return launch_column_sum(p.part, (int32_t)grid, 2 * p.c, p.dgamma, p.dbeta, 2, p.bf16, s);
+}
+
+hipError_t launch_column_sum(const float *part, int32_t rows, int32_t cols, _Float16 *out0, _Float16 *out1,
+                             int32_t parts, int32_t bf16, hipStream_t s) {
+    const int split = cols / parts;
+    const dim3 grid((unsigned)((cols + 15) / 16));
+    if (bf16)
+        hipLaunchKernelGGL((column_sum_kernel<__bf16>), grid, dim3(256), 0, s, part, rows, cols, out0, out1, split);
+    else
+        hipLaunchKernelGGL((column_sum_kernel<_Float16>), grid, dim3(256), 0, s, part, rows, cols, out0, out1, split);
+    return hipGetLastError();
+}
+
+hipError_t launch_zero_rows(_Float16 *y, int64_t rows, int32_t width, int64_t stride, hipStream_t s) {
+    const int64_t blocks = (rows * width + 1023) / 1024;
+    hipLaunchKernelGGL(zero_rows_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, y, rows,
+                       width, stride);
+    return hipGetLastError();
+}
+
+}  // namespace c3d

@@ -1,0 +1,256 @@
+// The matrix product behind `linear` and its gradients, for gfx950.
+//
+//   forward  y  = act(x w^T + bias) + residual     columns: w  [n][k], rows: x  [m][k]
+//   dx       dx = dz w                             columns: w^T,       rows: dz [m][n]
+//   dw       dw = dz^T x                           columns: x^T,       rows: dz^T
+//
+// One kernel template serves all three: each operand tile is staged through
+// LDS in the order it is stored in, and the operands whose contraction is not
+// contiguous are read back through the transposing LDS read, so that no
+// transposed copy of a tensor is ever made.
+//
+// The MFMA's A operand is the output's columns, so a lane's accumulators hold 4
+// adjacent columns of one row.  Sums are fp32; y and z are rounded once.
+#include "gemm_common.h"
+
+namespace c3d {
+
+namespace {
+
+// ---- ring kernel: 4 waves, a ring of NS stages, one barrier per stage.
+template <typename E, bool PT, bool QT, int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(256) void gemm_ring_kernel(GemmParams p) {
+    constexpr int TN = WN / 32, TM = WM / 32, WAVES = 4;
+    constexpr int PB = BN * kGemmRow, QB = BM * kGemmRow, STAGE = PB + QB;
+    constexpr int NP = PB / 1024 / WAVES, NQ = QB / 1024 / WAVES;
+    constexpr int LDS = NS * STAGE > BM * BN * 2 ? NS * STAGE : BM * BN * 2;
+    static_assert((BM / WM) * (BN / WN) == WAVES, "4 waves");
+    __shared__ __attribute__((aligned(1024))) char smem[LDS];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wmi = wave / (BN / WN), wni = wave % (BN / WN);
+
+    const int b = blockIdx.x;
+    const int u = b < p.dp_tiles ? xcd_range(b, p.dp_tiles)
+                                 : p.dp_tiles + xcd_range(b - p.dp_tiles, p.sk_tiles * p.sk_pieces);
+    int mt, nt, it0, it1, slot;
+    gemm_unit(p, u, mt, nt, it0, it1, slot);
+    const int m0 = mt * BM, n0 = nt * BN;
+    const int k0 = it0 * kGemmBK, kend = it1 * kGemmBK < p.K ? it1 * kGemmBK : p.K;
+
+    Operand<PT, BN, NP> op;
+    Operand<QT, BM, NQ> oq;
+    op.init(p.p, p.p_stride, n0, p.N, k0, kend, wave, WAVES, lane);
+    oq.init(p.q, p.q_stride, m0, p.M, k0, kend, wave, WAVES, lane);
+    uint32_t soff = 0;
+    int wbuf = 0;
+    auto fire = [&]() {
+        char *s = smem + wbuf * STAGE;
+        op.template load<0, NP>(s, wave, WAVES, soff);
+        oq.template load<0, NQ>(s + PB, wave, WAVES, soff);
+        op.advance();
+        oq.advance();
+        soff += kGemmRow;
+        wbuf = wbuf + 1 == NS ? 0 : wbuf + 1;
+    };
+    Fragments<PT, BN, TN> fp;
+    Fragments<QT, BM, TM> fq;
+    fp.init(wni * WN, lane);
+    fq.init(wmi * WM, lane);
+
+    f32x16 acc[TN][TM];
+    gemm_init_acc<E, WM, WN>(p, acc, slot < 0 && p.bias, n0 + wni * WN, lane);
+    // stages past the end load zeros (their reads are out of range), so that
+    // every wave's load count stays the same
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) fire();
+    int rbuf = 0;
+    for (int it = it0; it < it1; ++it) {
+        gemm_wait_loads<(NS - 2) * (NP + NQ)>();
+        gemm_barrier();  // the stage has landed, and everyone is done with the one before it
+        fire();
+        const char *s = smem + rbuf * STAGE;
+        static_for<2>([&](auto kc) {
+            constexpr int KK = decltype(kc)::value;
+            half8_t a[TN], bq[TM];
+#pragma unroll
+            for (int i = 0; i < TN; ++i) a[i] = fp.template read<KK>(s, i);
+#pragma unroll
+            for (int j = 0; j < TM; ++j) bq[j] = fq.template read<KK>(s + PB, j);
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j) acc[i][j] = mfma_32x32x16<E>(a[i], bq[j], acc[i][j]);
+        });
+        rbuf = rbuf + 1 == NS ? 0 : rbuf + 1;
+    }
+    gemm_wait_loads<0>();
+    if (slot >= 0) {
+        gemm_store_partial<BM, BN, WM, WN>(p, acc, slot, wave, lane);
+        return;
+    }
+    gemm_barrier();
+    gemm_store_tile<E, BM, BN, WM, WN, 256>(p, acc, smem, m0, n0, wmi, wni, lane);
+}
+
+// ---- the pieces of the split tiles, added in order, then the epilogue.  One
+// thread per 4 adjacent columns; blocks of the tile's fragment order.
+template <typename E, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p) {
+    constexpr int TN = WN / 32, TM = WM / 32, QUADS = BM * BN / 4;
+    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int st = (int)(idx / QUADS), qd = (int)(idx - (int64_t)st * QUADS);
+    if (st >= p.sk_tiles) return;
+    int mt, nt, it0, it1, slot;
+    gemm_unit(p, p.dp_tiles + st * p.sk_pieces, mt, nt, it0, it1, slot);
+    const int lane = qd & 63;
+    int r = qd >> 6;
+    const int g = r & 3;
+    r >>= 2;
+    const int j = r % TM;
+    r /= TM;
+    const int i = r % TN, wave = r / TN;
+    const int wmi = wave / (BN / WN), wni = wave % (BN / WN);
+    const int m = mt * BM + wmi * WM + j * 32 + (lane & 31);
+    const int n = nt * BN + wni * WN + i * 32 + 8 * g + 4 * (lane >> 5);
+    if (m >= p.M || n >= p.N) return;
+    const f32x4 *pp = reinterpret_cast<const f32x4 *>(p.partial) + (size_t)st * p.sk_pieces * QUADS + qd;
+    f32x4 v = pp[0];
+#pragma unroll 4
+    for (int k = 1; k < p.sk_pieces; ++k) v += pp[(size_t)k * QUADS];
+    if (p.bias) {
+        const half4_t bv = *reinterpret_cast<const half4_t *>(p.bias + n);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += to_f32<E>(bv[e]);
+    }
+    half4_t h;
+    if (p.z) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = from_f32<E>(v[e]);
+        *reinterpret_cast<half4_t *>(p.z + (int64_t)m * p.N + n) = h;
+    }
+    act_switch(p.act, [&](auto ac) {
+        constexpr int ACT = decltype(ac)::value;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = act_f<ACT>(v[e]);
+    });
+    if (p.res) {
+        const half4_t rv = *reinterpret_cast<const half4_t *>(p.res + (int64_t)m * p.res_stride + n);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += to_f32<E>(rv[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = from_f32<E>(v[e]);
+    *reinterpret_cast<half4_t *>(p.y + (int64_t)m * p.y_stride + n) = h;
+}
+
+// ---- dz = dy act'(z) and its column sums.  A block walks a strip of rows for
+// 256 groups of 8 columns (or, where there are fewer, several rows at once) and
+// writes the strip's fp32 sums.
+template <typename E, int ACT, bool DZ>
+__global__ __launch_bounds__(256) void act_grad_kernel(ActGradParams p, int groups, int rows_at_once) {
+    __shared__ float s[256 * 8];
+    const int gl = threadIdx.x % groups, rl = threadIdx.x / groups;
+    const int c = (blockIdx.x * groups + gl) * 8;
+    float sum[8] = {};
+    if (rl < rows_at_once && c < p.n) {
+        const int64_t r0 = p.m * blockIdx.y / p.strips, r1 = p.m * (blockIdx.y + 1) / p.strips;
+        for (int64_t r = r0 + rl; r < r1; r += rows_at_once) {
+            const half8_t d = *reinterpret_cast<const half8_t *>(p.dy + r * p.dy_stride + c);
+            half8_t o;
+            if constexpr (DZ) {
+                const half8_t zv = *reinterpret_cast<const half8_t *>(p.z + r * p.n + c);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v = to_f32<E>(d[e]) * act_slope<ACT>(to_f32<E>(zv[e]));
+                    sum[e] += v;
+                    o[e] = from_f32<E>(v);
+                }
+                *reinterpret_cast<half8_t *>(p.dz + r * p.n + c) = o;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += to_f32<E>(d[e]);
+            }
+        }
+    }
+    if (!p.colpart) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[threadIdx.x * 8 + e] = sum[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < groups * 8; i += 256) {
+        const int col = blockIdx.x * groups * 8 + i;
+        if (col >= p.n) break;
+        float t = 0.0f;
+        for (int q = 0; q < rows_at_once; ++q) t += s[q * groups * 8 + i];
+        p.colpart[(int64_t)blockIdx.y * p.n + col] = t;
+    }
+}
+
+const GemmTile kTiles[] = {
+    {"m128n128k32", 128, 128, kGemmBK, 256, 2, 1.0},
+};
+
+template <typename E, bool PT, bool QT>
+hipError_t launch_tile(const GemmParams &p, int tile, hipStream_t s) {
+    (void)tile;
+    const unsigned grid = (unsigned)(p.dp_tiles + p.sk_tiles * p.sk_pieces);
+    hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 128, 128, 64, 64, 4>), dim3(grid), dim3(256), 0, s, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !p.sk_tiles) return e;
+    const unsigned jb = (unsigned)((int64_t)p.sk_tiles * (128 * 128 / 4) / 256);
+    hipLaunchKernelGGL((gemm_join_kernel<E, 128, 128, 64, 64>), dim3(jb), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+const GemmTile *gemm_tiles(int *count) {
+    *count = (int)(sizeof(kTiles) / sizeof(kTiles[0]));
+    return kTiles;
+}
+
+hipError_t launch_gemm(const GemmParams &p, int tile, GemmLayout layout, hipStream_t s) {
+    switch (layout) {
+        case kGemmForward:
+            return p.bf16 ? launch_tile<__bf16, false, false>(p, tile, s)
+                          : launch_tile<_Float16, false, false>(p, tile, s);
+        case kGemmDx:
+            return p.bf16 ? launch_tile<__bf16, true, false>(p, tile, s)
+                          : launch_tile<_Float16, true, false>(p, tile, s);
+        default:
+            return p.bf16 ? launch_tile<__bf16, true, true>(p, tile, s) : launch_tile<_Float16, true, true>(p, tile, s);
+    }
+}
+
+namespace {
+int act_groups(int32_t n) { return n / 8 < 256 ? n / 8 : 256; }
+}  // namespace
+
+int32_t act_grad_strips(int64_t m, int32_t n) {
+    const int g = act_groups(n), at_once = 256 / g;
+    const int64_t col_blocks = (n / 8 + g - 1) / g;
+    int64_t strips = (1024 + col_blocks - 1) / col_blocks;
+    const int64_t most = (m + 4 * at_once - 1) / (4 * at_once);  // at least 4 steps each
+    if (strips > most) strips = most;
+    return (int32_t)(strips < 1 ? 1 : strips);
+}
+
+hipError_t launch_act_grad(const ActGradParams &p, hipStream_t s) {
+    const int g = act_groups(p.n), at_once = 256 / g;
+    const dim3 grid((unsigned)((p.n / 8 + g - 1) / g), (unsigned)p.strips);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, p, g, at_once);
+        return hipGetLastError();
+    };
+#define C3D_ACT_GRAD(ACT, DZ)                                       \
+    (p.bf16 ? go(act_grad_kernel<__bf16, ACT, DZ>) : go(act_grad_kernel<_Float16, ACT, DZ>))
+    switch (p.act) {
+        case CONV3D_ACT_SILU: return C3D_ACT_GRAD(CONV3D_ACT_SILU, true);
+        case CONV3D_ACT_GELU: return C3D_ACT_GRAD(CONV3D_ACT_GELU, true);
+        case CONV3D_ACT_GELU_TANH: return C3D_ACT_GRAD(CONV3D_ACT_GELU_TANH, true);
+        default: return C3D_ACT_GRAD(CONV3D_ACT_NONE, false);
+    }
+#undef C3D_ACT_GRAD
+}
+
+}  // namespace c3d

@@ -61,7 +61,9 @@ enum {
     CONV3D_F_NO_T1_FASTPATH = 4u,  /* never fold temporal taps, even when it is exact */
     CONV3D_F_BF16 = 8u,            /* x, weight, bias, residual and y are bf16, not fp16 */
     CONV3D_F_CHUNK = 16u,          /* chunked causal decoding: see conv3d_forward_chunk */
-    CONV3D_F_GN_STATS = 32u        /* also write GroupNorm partial statistics of y: see below */
+    CONV3D_F_GN_STATS = 32u,       /* also write GroupNorm partial statistics of y: see below */
+    CONV3D_F_PREACT = 64u,         /* linear only: keep the value before the activation */
+    CONV3D_F_POSITIONS = 128u      /* rope3d only: positions are given per token */
 };
 
 /* Execution paths a plan may choose. */
@@ -280,6 +282,182 @@ size_t groupnorm_silu_noalloc_max_bytes(void);
 conv3d_status groupnorm_silu_noalloc(const void *x, const void *gamma, const void *beta, void *y,
                                      int32_t n, int64_t thw, int32_t c, int32_t groups, float eps,
                                      int32_t apply_silu, void *stream);
+
+/*
+ * The token operators: what a transformer over the voxels of the latent grid
+ * runs on its token rows in front of the decoder, besides attention.  A token
+ * is one row; rows may lie inside wider ones (a stride in elements between
+ * rows, a multiple of 8, 0 for contiguous rows; at most 2^20).  Sizes of zero
+ * rows are valid: such a call enqueues nothing but the zeros of weight
+ * gradients.  Like every entry point, they take the caller's stream, allocate
+ * nothing and can be captured in a HIP graph.
+ */
+
+/* Activations of linear.  GELU is z * Phi(z) with the normal distribution's
+ * Phi; GELU_TANH its form 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+typedef enum {
+    CONV3D_ACT_NONE = 0,
+    CONV3D_ACT_SILU = 1,
+    CONV3D_ACT_GELU = 2,
+    CONV3D_ACT_GELU_TANH = 3
+} conv3d_act;
+
+/*
+ * A matrix product with its epilogue: z = x w^T (+ bias), y = act(z) (+ residual).
+ *   x:        [m][k], x_stride            w:    [n][k]
+ *   bias:     [n] (CONV3D_F_BIAS)         residual: [m][n], residual_stride (CONV3D_F_RESIDUAL)
+ *   y:        [m][n], y_stride            preact (z): [m][n] contiguous (CONV3D_F_PREACT)
+ * Sums are fp32 and bias, activation and residual are applied in fp32; y and
+ * preact are rounded once each, from the same fp32 z.  With CONV3D_F_BF16 all
+ * are bf16, otherwise fp16.
+ */
+typedef struct {
+    int64_t m;
+    int32_t n, k;
+    int32_t act;     /* conv3d_act */
+    uint32_t flags;  /* CONV3D_F_BIAS | CONV3D_F_RESIDUAL | CONV3D_F_PREACT | CONV3D_F_BF16 */
+    int64_t x_stride, y_stride, residual_stride;
+} linear_desc;
+
+/* A host-only, immutable object: safe to share between threads. */
+typedef struct linear_plan_s *linear_plan_t;
+
+/* What a plan chose for the forward product. */
+typedef struct {
+    int32_t tile_m, tile_n, tile_k, threads;
+    int64_t grid;                 /* workgroups of the product kernel */
+    int32_t split_tiles;          /* tiles whose contraction is split over several workgroups */
+    int32_t split_pieces;         /* pieces per split tile (0 if none) */
+    size_t workspace_bytes, backward_workspace_bytes;
+    char kernel_name[64];
+} linear_plan_info;
+
+/*
+ * Validate *d and choose the kernels.  Host only.  *workspace_bytes: device
+ * workspace of linear_forward (0 if none).
+ * Errors: INVALID_ARG for null pointers, negative m, non-positive n or k, an
+ * unknown activation or flag, or a stride that is negative, not a multiple of
+ * 8 or shorter than its rows; UNSUPPORTED for n or k not a multiple of 8 or
+ * above 65536, m of 2^30 or more, or strides above 2^20.
+ * Products of few rows, or with few tiles, split the contraction over several
+ * workgroups, which leave fp32 partials in the workspace that a second small
+ * kernel adds in a fixed order.  The environment variable
+ * CONV3D_LINEAR_TILE=<name> forces a kernel.
+ */
+conv3d_status linear_plan(const linear_desc *d, linear_plan_t *out, size_t *workspace_bytes);
+conv3d_status linear_plan_query(linear_plan_t p, linear_plan_info *info);
+void linear_plan_destroy(linear_plan_t p);
+
+/*
+ * Enqueue the product on stream.  bias, residual and preact are required when
+ * the plan's flags say so, otherwise ignored.  y and preact must not overlap
+ * any input or each other.  The workspace is scratch, overwritten by each
+ * call; calls on different streams must not share one.
+ * Errors: INVALID_ARG (null or misaligned pointers, overlaps), WORKSPACE, HIP.
+ */
+conv3d_status linear_forward(linear_plan_t p, const void *x, const void *w, const void *bias, const void *residual,
+                             void *y, void *preact, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The gradients of one product, from dy, the gradient of y (its stride is
+ * y_stride):  dz = dy * act'(preact), dx = dz w (stride x_stride),
+ * dw = dz^T x, dbias = the sum of dz over the rows.  (The residual's gradient
+ * is dy itself.)  dx, dw and dbias may each be null and are then not computed;
+ * x is needed for dw, w for dx, preact for any activation.  dz is rounded once
+ * to the element type, as the operand of both products (dbias is summed before
+ * that rounding); dx, dw and dbias are rounded once.  Sums run in a fixed order:
+ * results do not vary from call to call.
+ * Errors: as linear_forward, and INVALID_ARG if every gradient is null.
+ */
+size_t linear_backward_workspace(linear_plan_t p);
+conv3d_status linear_backward(linear_plan_t p, const void *dy, const void *x, const void *w, const void *preact,
+                              void *dx, void *dw, void *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Layer norm of each row over its c channels:
+ *   y = (x - mean) / sqrt(var + eps) * gamma + beta,  var the biased variance.
+ *   x: [rows][c], x_stride;  y: [rows][c], y_stride;  gamma, beta: [c], either may be null (1, 0)
+ *   stats: fp32 [rows][2], or null: (mean, 1 / sqrt(var + eps)) for the backward pass
+ * fp32 arithmetic, y rounded once.  y may equal x with the same stride.
+ * layernorm_backward: from dy (stride y_stride) and the forward pass's stats,
+ *   dx (stride x_stride) = LayerNorm's gradient (+ dres, stride x_stride, the
+ *   gradient that reaches x along a residual path; may be null),
+ *   dgamma, dbeta: [c], either may be null: sums over the rows in a fixed order.
+ * dx may equal dy, x or dres where their strides are the same.  The workspace
+ * (layernorm_backward_workspace bytes, 0 for sizes that layernorm_backward
+ * would reject) is scratch; it may be null when dgamma and dbeta are.
+ * Errors: INVALID_ARG (null or misaligned pointers, negative rows, c < 1, bad
+ * strides, eps < 0, overlaps), UNSUPPORTED (c not a multiple of 8 or above
+ * 16384, 2^40 rows or more, strides above 2^20), WORKSPACE, HIP.
+ */
+conv3d_status layernorm(const void *x, const void *gamma, const void *beta, void *y, void *stats, int64_t rows,
+                        int32_t c, int64_t x_stride, int64_t y_stride, float eps, void *stream);
+conv3d_status layernorm_bf16(const void *x, const void *gamma, const void *beta, void *y, void *stats, int64_t rows,
+                             int32_t c, int64_t x_stride, int64_t y_stride, float eps, void *stream);
+size_t layernorm_backward_workspace(int64_t rows, int32_t c);
+conv3d_status layernorm_backward(const void *dy, const void *x, const void *gamma, const void *stats,
+                                 const void *dres, void *dx, void *dgamma, void *dbeta, int64_t rows, int32_t c,
+                                 int64_t x_stride, int64_t y_stride, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+conv3d_status layernorm_backward_bf16(const void *dy, const void *x, const void *gamma, const void *stats,
+                                      const void *dres, void *dx, void *dgamma, void *dbeta, int64_t rows,
+                                      int32_t c, int64_t x_stride, int64_t y_stride, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/* Which two elements of a head form pair p. */
+typedef enum {
+    ROPE3D_PAIR_ADJACENT = 0, /* 2p and 2p + 1 */
+    ROPE3D_PAIR_HALVES = 1    /* p and p + (dim_t + dim_h + dim_w) / 2 */
+} rope3d_pairing;
+
+/*
+ * Rotary positions over (time, height, width).  The first dim_t + dim_h +
+ * dim_w elements of a head form pairs: dim_t / 2 pairs turn with the token's
+ * time, then dim_h / 2 with its height, then dim_w / 2 with its width; pair i
+ * of an axis of dim elements at position s turns by s * base^(-2 i / dim):
+ * (u, v) -> (u cos - v sin, u sin + v cos).  The other elements are copied.
+ *   q, q_out: [n][t*h*w tokens][heads_q][head_dim]; k, k_out: the same with heads_k
+ * *_stride: elements between samples, tokens and heads of each tensor
+ * (multiples of 8; all three 0 for the contiguous layout above), so that heads
+ * can be read inside the rows of a fused projection, or written heads first.
+ * Tokens are the grid's in (t, h, w) order, at positions (t_offset + t, h, w),
+ * or, with CONV3D_F_POSITIONS, at given int32 positions [n][tokens][3] of any
+ * size and sign.  Angles are reduced in 64 bits.
+ */
+typedef struct {
+    int32_t n, t, h, w;
+    int32_t heads_q, heads_k, head_dim; /* heads_k may be 0: no k */
+    int32_t dim_t, dim_h, dim_w;
+    int32_t pairing; /* rope3d_pairing */
+    uint32_t flags;  /* CONV3D_F_POSITIONS | CONV3D_F_BF16 */
+    double base;
+    int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+} rope3d_desc;
+
+typedef struct rope3d_plan_s *rope3d_plan_t; /* host-only, immutable */
+
+/*
+ * Errors: INVALID_ARG for null pointers, negative extents, heads_q < 1, odd or
+ * negative dims, dims that exceed head_dim or are all 0, a base that is not
+ * positive and finite, or bad strides; UNSUPPORTED for head_dim not a multiple
+ * of 8 or above 512, dims above 256 together, dims not a multiple of 16
+ * together for ROPE3D_PAIR_HALVES, or 2^31 tokens or more.
+ */
+conv3d_status rope3d_plan(const rope3d_desc *d, rope3d_plan_t *out);
+void rope3d_plan_destroy(rope3d_plan_t p);
+/*
+ * Enqueue the rotation of q into q_out and k into k_out (k, k_out ignored when
+ * heads_k is 0).  Each output may be its input (same pointer and strides), and
+ * must not overlap it otherwise.  positions is required with
+ * CONV3D_F_POSITIONS, otherwise ignored; t_offset is added to the grid's times
+ * (the frames before this chunk), and ignored with given positions.
+ * rope3d_backward is the gradient: dq, dk from dq_out, dk_out, with the
+ * outputs' strides on the incoming gradients and the inputs' on the results.
+ */
+conv3d_status rope3d_forward(rope3d_plan_t p, const void *q, const void *k, void *q_out, void *k_out,
+                             const void *positions, int32_t t_offset, void *stream);
+conv3d_status rope3d_backward(rope3d_plan_t p, const void *dq_out, const void *dk_out, void *dq, void *dk,
+                              const void *positions, int32_t t_offset, void *stream);
 
 /*
  * Measurement aids, not on the convolution path: the ceilings of the machine
