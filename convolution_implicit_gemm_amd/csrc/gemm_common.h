@@ -128,9 +128,10 @@ struct Operand {
     template <int J0, int CNT>
     __device__ __forceinline__ void load(char *lds, int first, int step, uint32_t soff) {
         if constexpr (TR) {
+            // past the end: no record, so every offset is out of range
             const int rows = left < kGemmBK ? left : kGemmBK;
-            const uint32_t rec = rows > 0 ? (uint32_t)((rows - 1) * (int)stride + ncols) * 2u : 0u;
-            const buf_rsrc r = make_rsrc(base, rec);
+            const int rec = ((rows - 1) * (int)stride + ncols) * 2;
+            const buf_rsrc r = make_rsrc(base, (uint32_t)(rec < 0 || left <= 0 ? 0 : rec));
 #pragma unroll
             for (int j = J0; j < J0 + CNT; ++j) dma16(r, lds + (first + j * step) * 1024, voff[j], 0u);
         } else {
@@ -146,12 +147,45 @@ struct Operand {
     }
 };
 
+// The transposing LDS reads.  Within 16 lanes, lane j reads 8 bytes of row j / 4
+// and lane i receives column i of those 4 rows; two reads, 4 rows apart, make
+// one lane's 8 contraction values.  Written as assembly that waits for its own
+// results: for the compiler's own form of the read it waits for every load into
+// LDS still in flight, stages ahead included.  ROW: bytes of one LDS row.
+#define C3D_TR(d, a, o) "ds_read_b64_tr_b16 %" #d ", %" #a " offset:%" #o "\n\t"
+template <int ROW>
+__device__ __forceinline__ void tr_read2(const uint32_t (&a)[2], uint64_t (&v)[8]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile(C3D_TR(0, 8, 10) C3D_TR(1, 8, 11) C3D_TR(2, 9, 10) C3D_TR(3, 9, 11) C3D_TR(4, 8, 12) C3D_TR(5, 8, 13)
+                     C3D_TR(6, 9, 12) C3D_TR(7, 9, 13) "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]),
+                   "=&v"(v[7])
+                 : "v"(a[0]), "v"(a[1]), "n"(0), "n"(4 * ROW), "n"(16 * ROW), "n"(20 * ROW)
+                 : "memory");
+#endif
+}
+template <int ROW>
+__device__ __forceinline__ void tr_read4(const uint32_t (&a)[4], uint64_t (&v)[16]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile(C3D_TR(0, 16, 20) C3D_TR(1, 16, 21) C3D_TR(2, 17, 20) C3D_TR(3, 17, 21) C3D_TR(4, 18, 20)
+                     C3D_TR(5, 18, 21) C3D_TR(6, 19, 20) C3D_TR(7, 19, 21) C3D_TR(8, 16, 22) C3D_TR(9, 16, 23)
+                         C3D_TR(10, 17, 22) C3D_TR(11, 17, 23) C3D_TR(12, 18, 22) C3D_TR(13, 18, 23)
+                             C3D_TR(14, 19, 22) C3D_TR(15, 19, 23) "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]),
+                   "=&v"(v[7]), "=&v"(v[8]), "=&v"(v[9]), "=&v"(v[10]), "=&v"(v[11]), "=&v"(v[12]), "=&v"(v[13]),
+                   "=&v"(v[14]), "=&v"(v[15])
+                 : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(0), "n"(4 * ROW), "n"(16 * ROW), "n"(20 * ROW)
+                 : "memory");
+#endif
+}
+#undef C3D_TR
+
 // Byte offsets of a lane's MFMA fragments within an operand's stage buffer.
 // A fragment covers 32 output rows (from row0, a multiple of 32) x 16 of the
 // contraction: lane l holds output row l % 32, contraction 8 (l / 32) .. + 7.
 template <bool TR, int ROWS, int NF>
 struct Fragments {
-    int off[TR ? NF : 2];
+    uint32_t off[TR ? NF : 2];
     __device__ __forceinline__ void init(int row0, int lane) {
         if constexpr (TR) {
             const int j = lane & 15, g = (lane >> 4) & 1, r = (lane >> 5) * 8 + (j >> 2);
@@ -166,23 +200,32 @@ struct Fragments {
             for (int kk = 0; kk < 2; ++kk) off[kk] = (row0 + r) * kGemmRow + (((2 * kk + hi) ^ swz<kGemmBK>(r)) * 16);
         }
     }
-    // fragment i of k-step KK
-    template <int KK>
-    __device__ __forceinline__ half8_t read(const char *lds, int i) const {
+    // the fragments of one stage, both k-steps
+    __device__ __forceinline__ void read(const char *lds, half8_t (&f)[2][NF]) const {
         if constexpr (TR) {
-#if defined(__HIP_DEVICE_COMPILE__)
-            typedef short s16x4 __attribute__((ext_vector_type(4)));
-            typedef __attribute__((address_space(3))) s16x4 lds_s4;
-            const char *a = lds + off[i] + KK * 16 * ROWS * 2;
-            const half4_t lo = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)a));
-            const half4_t hi =
-                __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(a + 4 * ROWS * 2)));
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-#else
-            return half8_t{};
-#endif
+            static_assert(NF == 2 || NF == 4, "one assembly block per operand");
+            const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)lds;
+            uint32_t a[NF];
+            uint64_t v[4 * NF];
+#pragma unroll
+            for (int i = 0; i < NF; ++i) a[i] = base + off[i];
+            if constexpr (NF == 2)
+                tr_read2<ROWS * 2>(a, v);
+            else
+                tr_read4<ROWS * 2>(a, v);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int i = 0; i < NF; ++i)
+                    f[kk][i] = __builtin_shufflevector(__builtin_bit_cast(half4_t, v[(kk * NF + i) * 2]),
+                                                       __builtin_bit_cast(half4_t, v[(kk * NF + i) * 2 + 1]), 0, 1, 2,
+                                                       3, 4, 5, 6, 7);
         } else {
-            return *reinterpret_cast<const half8_t *>(lds + off[KK] + i * 32 * kGemmRow);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int i = 0; i < NF; ++i)
+                    f[kk][i] = *reinterpret_cast<const half8_t *>(lds + off[kk] + i * 32 * kGemmRow);
         }
     }
 };
@@ -256,12 +299,13 @@ __device__ __forceinline__ void load_rows(char *smem, const _Float16 *in, int64_
 // WN * wni + 32 i + 8 g + 4 (lane / 32) + e, row WM * wmi + 32 j + lane % 32.
 // Every LDS buffer of the K loop is free, and every wave is past it.
 template <typename E, int BM, int BN, int WM, int WN, int THREADS>
-__device__ __forceinline__ void gemm_store_tile(const GemmParams &p, f32x16 (&acc)[WN / 32][WM / 32], char *smem, int m0,
-                                                int n0, int wmi, int wni, int lane) {
+__device__ __forceinline__ void gemm_store_tile(const GemmParams &p, const f32x16 (&acc)[WN / 32][WM / 32], char *smem,
+                                                int m0, int n0, int wmi, int wni, int lane) {
     constexpr int TN = WN / 32, TM = WM / 32;
     const int rows = p.M - m0 < BM ? p.M - m0 : BM, cols = p.N - n0 < BN ? p.N - n0 : BN;
     const int rrow = lane & 31, rhi = lane >> 5;
-    auto stage = [&](auto resc) {
+    auto stage = [&](auto actc, auto resc) {
+        constexpr int ACT = decltype(actc)::value;
         constexpr bool RES = decltype(resc)::value;
 #pragma unroll
         for (int i = 0; i < TN; ++i)
@@ -275,38 +319,27 @@ __device__ __forceinline__ void gemm_store_tile(const GemmParams &p, f32x16 (&ac
                     if constexpr (RES) {
                         const half4_t r = *reinterpret_cast<const half4_t *>(chunk + rhi * 8);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) h[e] = from_f32<E>(acc[i][j][4 * g + e] + to_f32<E>(r[e]));
+                        for (int e = 0; e < 4; ++e) h[e] = from_f32<E>(act_f<ACT>(acc[i][j][4 * g + e]) + to_f32<E>(r[e]));
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) h[e] = from_f32<E>(acc[i][j][4 * g + e]);
+                        for (int e = 0; e < 4; ++e) h[e] = from_f32<E>(act_f<ACT>(acc[i][j][4 * g + e]));
                     }
                     *reinterpret_cast<half4_t *>(chunk + ((rhi ^ ((v >> 4) & 1)) << 3)) = h;
                 }
         gemm_barrier();
     };
     if (p.z) {
-        stage(std::false_type{});
+        stage(std::integral_constant<int, CONV3D_ACT_NONE>{}, std::false_type{});
         store_rows<BM, BN, THREADS>(smem, p.z + (int64_t)m0 * p.N + n0, p.N, rows, cols);
         gemm_barrier();
     }
-    if (p.res) load_rows<BM, BN, THREADS>(smem, p.res + (int64_t)m0 * p.res_stride + n0, p.res_stride, rows, cols);
-    act_switch(p.act, [&](auto ac) {
-        constexpr int ACT = decltype(ac)::value;
-        if constexpr (ACT != CONV3D_ACT_NONE) {
-#pragma unroll
-            for (int i = 0; i < TN; ++i)
-#pragma unroll
-                for (int j = 0; j < TM; ++j)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[i][j][e] = act_f<ACT>(acc[i][j][e]);
-        }
-    });
     if (p.res) {
+        load_rows<BM, BN, THREADS>(smem, p.res + (int64_t)m0 * p.res_stride + n0, p.res_stride, rows, cols);
         gemm_wait_loads<0>();
         gemm_barrier();
-        stage(std::true_type{});
+        act_switch(p.act, [&](auto ac) { stage(ac, std::true_type{}); });
     } else {
-        stage(std::false_type{});
+        act_switch(p.act, [&](auto ac) { stage(ac, std::false_type{}); });
     }
     store_rows<BM, BN, THREADS>(smem, p.y + (int64_t)m0 * p.y_stride + n0, p.y_stride, rows, cols);
 }

@@ -70,18 +70,15 @@ __global__ __launch_bounds__(256) void gemm_ring_kernel(GemmParams p) {
         gemm_barrier();  // the stage has landed, and everyone is done with the one before it
         fire();
         const char *s = smem + rbuf * STAGE;
-        static_for<2>([&](auto kc) {
-            constexpr int KK = decltype(kc)::value;
-            half8_t a[TN], bq[TM];
+        half8_t a[2][TN], bq[2][TM];
+        fp.read(s, a);
+        fq.read(s + PB, bq);
 #pragma unroll
-            for (int i = 0; i < TN; ++i) a[i] = fp.template read<KK>(s, i);
-#pragma unroll
-            for (int j = 0; j < TM; ++j) bq[j] = fq.template read<KK>(s + PB, j);
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int i = 0; i < TN; ++i)
 #pragma unroll
-                for (int j = 0; j < TM; ++j) acc[i][j] = mfma_32x32x16<E>(a[i], bq[j], acc[i][j]);
-        });
+                for (int j = 0; j < TM; ++j) acc[i][j] = mfma_32x32x16<E>(a[kk][i], bq[kk][j], acc[i][j]);
         rbuf = rbuf + 1 == NS ? 0 : rbuf + 1;
     }
     gemm_wait_loads<0>();
@@ -91,6 +88,103 @@ __global__ __launch_bounds__(256) void gemm_ring_kernel(GemmParams p) {
     }
     gemm_barrier();
     gemm_store_tile<E, BM, BN, WM, WN, 256>(p, acc, smem, m0, n0, wmi, wni, lane);
+}
+
+// ---- ping-pong kernel: 8 waves in two groups of 4, one wave of each on every
+// SIMD (waves w and w + 4 share one).  Group g owns half of the tile's columns
+// and alternates between a memory phase (all MFMA fragments of one stage from
+// LDS into registers, its share of the loads of a later stage) and a compute
+// phase (that stage's MFMAs, at raised priority); the groups run one phase
+// apart with one workgroup barrier per phase, so that each SIMD's matrix core
+// is fed by one wave while the other reads LDS.
+//
+// Stage s (32 of the contraction) is read by group g in phase 2s + g and its
+// buffer in the ring of NS is refilled with stage s + NS by loads issued from
+// phase 2s + 2 on, that is NS - 1 stages ahead of their use.  A wave waits for
+// its own loads of stage s + 1 before the barrier that ends phase 2s + 1.
+template <typename E, bool PT, bool QT, int BM, int BN, int NS>
+__global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p) {
+    constexpr int WM = BM / 4, WN = BN / 2, TN = WN / 32, TM = WM / 32, WAVES = 8;
+    constexpr int PB = BN * kGemmRow, QB = BM * kGemmRow, STAGE = PB + QB;
+    constexpr int NP = PB / 1024 / WAVES, NQ = QB / 1024 / WAVES;
+    constexpr int LDS = NS * STAGE > BM * BN * 2 ? NS * STAGE : BM * BN * 2;
+    static_assert(LDS <= 160 * 1024, "LDS is 160 KiB per CU");
+    __shared__ __attribute__((aligned(1024))) char smem[LDS];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int grp = wave >> 2, wmi = wave & 3, wni = grp;
+
+    const int b = blockIdx.x;
+    const int u = b < p.dp_tiles ? xcd_range(b, p.dp_tiles)
+                                 : p.dp_tiles + xcd_range(b - p.dp_tiles, p.sk_tiles * p.sk_pieces);
+    int mt, nt, it0, it1, slot;
+    gemm_unit(p, u, mt, nt, it0, it1, slot);
+    const int m0 = mt * BM, n0 = nt * BN;
+    const int k0 = it0 * kGemmBK, kend = it1 * kGemmBK < p.K ? it1 * kGemmBK : p.K;
+
+    Operand<PT, BN, NP> op;
+    Operand<QT, BM, NQ> oq;
+    op.init(p.p, p.p_stride, n0, p.N, k0, kend, wave, WAVES, lane);
+    oq.init(p.q, p.q_stride, m0, p.M, k0, kend, wave, WAVES, lane);
+    uint32_t soff = 0;
+    int wbuf = 0;
+    auto fire = [&]() {
+        char *s = smem + wbuf * STAGE;
+        op.template load<0, NP>(s, wave, WAVES, soff);
+        oq.template load<0, NQ>(s + PB, wave, WAVES, soff);
+        op.advance();
+        oq.advance();
+        soff += kGemmRow;
+        wbuf = wbuf + 1 == NS ? 0 : wbuf + 1;
+    };
+    Fragments<PT, BN, TN> fp;
+    Fragments<QT, BM, TM> fq;
+    fp.init(wni * WN, lane);
+    fq.init(wmi * WM, lane);
+
+    f32x16 acc[TN][TM];
+    // loads past the contraction's end read zeros, so that every wave's load
+    // count stays the same
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) fire();
+    gemm_init_acc<E, WM, WN>(p, acc, slot < 0 && p.bias, n0 + wni * WN, lane);
+    gemm_wait_loads<0>();
+    gemm_barrier();
+    if (grp) gemm_barrier();  // group 1 runs one phase behind
+    half8_t a[2][TN], bq[2][TM];
+    int rbuf = 0;
+    for (int it = it0; it < it1; ++it) {
+        const char *s = smem + rbuf * STAGE;
+        if constexpr (PT || QT) {  // the transposing reads wait for themselves
+            fire();
+            fq.read(s + PB, bq);
+            fp.read(s, a);
+        } else {
+            fp.read(s, a);
+            fq.read(s + PB, bq);
+            fire();
+        }
+        if (grp) gemm_wait_loads<(NS - 2) * (NP + NQ)>();
+        gemm_barrier();
+        __builtin_amdgcn_s_setprio(2);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j) acc[i][j] = mfma_32x32x16<E>(a[kk][i], bq[kk][j], acc[i][j]);
+        __builtin_amdgcn_s_setprio(0);
+        if (!grp) gemm_wait_loads<(NS - 2) * (NP + NQ)>();
+        if (!(grp && it + 1 == it1)) gemm_barrier();  // group 1's last would pair with nothing
+        rbuf = rbuf + 1 == NS ? 0 : rbuf + 1;
+    }
+    gemm_wait_loads<0>();
+    if (slot >= 0) {
+        gemm_store_partial<BM, BN, WM, WN>(p, acc, slot, wmi * 2 + wni, lane);
+        return;
+    }
+    gemm_barrier();
+    gemm_store_tile<E, BM, BN, WM, WN, 512>(p, acc, smem, m0, n0, wmi, wni, lane);
 }
 
 // ---- the pieces of the split tiles, added in order, then the epilogue.  One
@@ -187,18 +281,25 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradParams p, int grou
 }
 
 const GemmTile kTiles[] = {
-    {"m128n128k32", 128, 128, kGemmBK, 256, 2, 1.0},
+    {"m256n256k32", 256, 256, kGemmBK, 512, 1, 1.0},
+    {"m128n128k32", 128, 128, kGemmBK, 256, 2, 0.62},
 };
 
 template <typename E, bool PT, bool QT>
 hipError_t launch_tile(const GemmParams &p, int tile, hipStream_t s) {
-    (void)tile;
-    const unsigned grid = (unsigned)(p.dp_tiles + p.sk_tiles * p.sk_pieces);
-    hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 128, 128, 64, 64, 4>), dim3(grid), dim3(256), 0, s, p);
+    const dim3 grid((unsigned)(p.dp_tiles + p.sk_tiles * p.sk_pieces));
+    if (tile == 0)
+        hipLaunchKernelGGL((gemm_pp_kernel<E, PT, QT, 256, 256, 5>), grid, dim3(512), 0, s, p);
+    else
+        hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 128, 128, 64, 64, 4>), grid, dim3(256), 0, s, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.sk_tiles) return e;
-    const unsigned jb = (unsigned)((int64_t)p.sk_tiles * (128 * 128 / 4) / 256);
-    hipLaunchKernelGGL((gemm_join_kernel<E, 128, 128, 64, 64>), dim3(jb), dim3(256), 0, s, p);
+    const GemmTile &t = kTiles[tile];
+    const dim3 jb((unsigned)((int64_t)p.sk_tiles * (t.bm * t.bn / 4) / 256));
+    if (tile == 0)
+        hipLaunchKernelGGL((gemm_join_kernel<E, 256, 256, 64, 128>), jb, dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((gemm_join_kernel<E, 128, 128, 64, 64>), jb, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 

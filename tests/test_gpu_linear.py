@@ -10,7 +10,7 @@ from token_helpers import (ACTS, DTYPES, U24, act64, assert_unmarked_only, asser
 
 pytestmark = pytest.mark.gpu
 
-TILES = [None, "m128n128k32"]
+TILES = [None, "m128n128k32", "m256n256k32"]
 
 
 def run_forward(m, n, k, act, dtype, bias, residual, keep, gap, seed, tile=None, x=None, w=None):
