@@ -8,7 +8,7 @@
 
 namespace c3d {
 
-constexpr int kGemmBK = 32;                 // contraction per stage
+constexpr int kGemmBK = 64;                 // contraction per stage
 constexpr int kGemmRow = kGemmBK * 2;       // bytes of one LDS row, contraction contiguous
 
 // z -> act(z), fp32.  GELU (erf form) through Abramowitz and Stegun 7.1.26,
@@ -73,10 +73,12 @@ __device__ __forceinline__ void act_switch(int act, F &&f) {
 }
 
 // ---- operand tiles in LDS.  An operand tile is ROWS output rows (or columns)
-// x 32 of the contraction, ROWS x 64 bytes in either order:
-//   contraction contiguous (TR = false): ROWS rows of 64 bytes; 16-byte chunk c
-//     of row r sits at chunk c ^ swz<32>(r);
-//   transposed (TR = true): 32 rows (one per contraction index) of 2 ROWS
+// x 64 of the contraction, ROWS x 128 bytes in either order (a whole cache line
+// of every row per stage: with 32 of the contraction and half lines the forward
+// product ran at 1130 instead of 1250 TFLOP/s):
+//   contraction contiguous (TR = false): ROWS rows of 128 bytes; 16-byte chunk
+//     c of row r sits at chunk c ^ swz<64>(r);
+//   transposed (TR = true): 64 rows (one per contraction index) of 2 ROWS
 //     bytes; chunk c of row r sits at chunk c ^ ((r & 3) << 2), so that the 4
 //     rows x 64 bytes that a half-wave's transposing reads take fill all banks.
 // Loads are 16 bytes per lane, 1 KiB per instruction, straight into LDS; the
@@ -86,11 +88,11 @@ __device__ __forceinline__ void act_switch(int act, F &&f) {
 // offsets for its NI load instructions per stage.
 template <bool TR, int ROWS, int NI>
 struct Operand {
-    const _Float16 *base;   // TR: row it * 32 of the tile's columns; else the tile's first row
+    const _Float16 *base;   // TR: the stage's first row, at the tile's columns; else the tile's first row
     int64_t stride;
     int left;               // contraction not yet loaded, from the current stage on
     int ncols;              // TR: columns of the tile inside the matrix
-    uint32_t records;
+    uint32_t records, soff;
     uint32_t voff[NI];
     int kc[NI];             // !TR: the contraction index of the lane's chunk within the stage
 
@@ -99,15 +101,16 @@ struct Operand {
                                          int first, int step, int lane) {
         stride = stride_;
         left = kend - k0;
+        soff = 0;
         const int rows = rows_total - row0 < ROWS ? rows_total - row0 : ROWS;
         ncols = rows;
         if constexpr (TR) {
             base = m + (int64_t)k0 * stride + row0;
-            constexpr int CH = ROWS / 8;
+            constexpr unsigned CH = ROWS / 8;
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
-                const int lin = (first + j * step) * 64 + lane;
-                const int r = lin / CH, c = (lin % CH) ^ ((r & 3) << 2);
+                const unsigned lin = (unsigned)((first + j * step) * 64 + lane);
+                const int r = (int)(lin / CH), c = (int)(lin % CH) ^ ((r & 3) << 2);
                 voff[j] = c * 8 < ncols ? (uint32_t)(r * (int)stride + c * 8) * 2u : kOOB;
                 kc[j] = 0;
             }
@@ -117,33 +120,31 @@ struct Operand {
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
                 const int lin = (first + j * step) * 64 + lane;
-                const int r = lin >> 2, c = (lin & 3) ^ swz<kGemmBK>(r);
+                const int r = lin >> 3, c = (lin & 7) ^ swz<kGemmBK>(r);
                 kc[j] = c * 8;
                 voff[j] = r < rows ? (uint32_t)(r * (int)stride + c * 8) * 2u : kOOB;
             }
         }
     }
-    // Load instructions J0 .. J0 + CNT - 1 of the current stage into `lds` (the
-    // operand's stage buffer); the contraction past its end reads as zeros.
-    template <int J0, int CNT>
-    __device__ __forceinline__ void load(char *lds, int first, int step, uint32_t soff) {
+    // The current stage into `lds` (the operand's stage buffer), then on to the
+    // next; the contraction past its end reads as zeros.
+    __device__ __forceinline__ void load(char *lds, int first, int step) {
         if constexpr (TR) {
             // past the end: no record, so every offset is out of range
             const int rows = left < kGemmBK ? left : kGemmBK;
             const int rec = ((rows - 1) * (int)stride + ncols) * 2;
             const buf_rsrc r = make_rsrc(base, (uint32_t)(rec < 0 || left <= 0 ? 0 : rec));
 #pragma unroll
-            for (int j = J0; j < J0 + CNT; ++j) dma16(r, lds + (first + j * step) * 1024, voff[j], 0u);
+            for (int j = 0; j < NI; ++j) dma16(r, lds + (first + j * step) * 1024, voff[j], 0u);
+            base += kGemmBK * stride;
         } else {
             const buf_rsrc r = make_rsrc(base, records);
 #pragma unroll
-            for (int j = J0; j < J0 + CNT; ++j)
+            for (int j = 0; j < NI; ++j)
                 dma16(r, lds + (first + j * step) * 1024, kc[j] < left ? voff[j] : kOOB, soff);
+            soff += kGemmRow;
         }
-    }
-    __device__ __forceinline__ void advance() {
         left -= kGemmBK;
-        if constexpr (TR) base += kGemmBK * stride;
     }
 };
 
@@ -151,20 +152,20 @@ struct Operand {
 // and lane i receives column i of those 4 rows; two reads, 4 rows apart, make
 // one lane's 8 contraction values.  Written as assembly that waits for its own
 // results: for the compiler's own form of the read it waits for every load into
-// LDS still in flight, stages ahead included.  ROW: bytes of one LDS row.
+// LDS still in flight, stages ahead included.  ROW: bytes of one LDS row; K0: the first row.
 #define C3D_TR(d, a, o) "ds_read_b64_tr_b16 %" #d ", %" #a " offset:%" #o "\n\t"
-template <int ROW>
+template <int ROW, int K0>
 __device__ __forceinline__ void tr_read2(const uint32_t (&a)[2], uint64_t (&v)[8]) {
 #if defined(__HIP_DEVICE_COMPILE__)
     asm volatile(C3D_TR(0, 8, 10) C3D_TR(1, 8, 11) C3D_TR(2, 9, 10) C3D_TR(3, 9, 11) C3D_TR(4, 8, 12) C3D_TR(5, 8, 13)
                      C3D_TR(6, 9, 12) C3D_TR(7, 9, 13) "s_waitcnt lgkmcnt(0)"
                  : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]),
                    "=&v"(v[7])
-                 : "v"(a[0]), "v"(a[1]), "n"(0), "n"(4 * ROW), "n"(16 * ROW), "n"(20 * ROW)
+                 : "v"(a[0]), "v"(a[1]), "n"(K0 * ROW), "n"((K0 + 4) * ROW), "n"((K0 + 16) * ROW), "n"((K0 + 20) * ROW)
                  : "memory");
 #endif
 }
-template <int ROW>
+template <int ROW, int K0>
 __device__ __forceinline__ void tr_read4(const uint32_t (&a)[4], uint64_t (&v)[16]) {
 #if defined(__HIP_DEVICE_COMPILE__)
     asm volatile(C3D_TR(0, 16, 20) C3D_TR(1, 16, 21) C3D_TR(2, 17, 20) C3D_TR(3, 17, 21) C3D_TR(4, 18, 20)
@@ -174,7 +175,7 @@ __device__ __forceinline__ void tr_read4(const uint32_t (&a)[4], uint64_t (&v)[1
                  : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]),
                    "=&v"(v[7]), "=&v"(v[8]), "=&v"(v[9]), "=&v"(v[10]), "=&v"(v[11]), "=&v"(v[12]), "=&v"(v[13]),
                    "=&v"(v[14]), "=&v"(v[15])
-                 : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(0), "n"(4 * ROW), "n"(16 * ROW), "n"(20 * ROW)
+                 : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(K0 * ROW), "n"((K0 + 4) * ROW), "n"((K0 + 16) * ROW), "n"((K0 + 20) * ROW)
                  : "memory");
 #endif
 }
@@ -185,7 +186,7 @@ __device__ __forceinline__ void tr_read4(const uint32_t (&a)[4], uint64_t (&v)[1
 // contraction: lane l holds output row l % 32, contraction 8 (l / 32) .. + 7.
 template <bool TR, int ROWS, int NF>
 struct Fragments {
-    uint32_t off[TR ? NF : 2];
+    uint32_t off[TR ? NF : 4];
     __device__ __forceinline__ void init(int row0, int lane) {
         if constexpr (TR) {
             const int j = lane & 15, g = (lane >> 4) & 1, r = (lane >> 5) * 8 + (j >> 2);
@@ -197,10 +198,11 @@ struct Fragments {
         } else {
             const int r = lane & 31, hi = lane >> 5;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) off[kk] = (row0 + r) * kGemmRow + (((2 * kk + hi) ^ swz<kGemmBK>(r)) * 16);
+            for (int kk = 0; kk < 4; ++kk) off[kk] = (row0 + r) * kGemmRow + (((2 * kk + hi) ^ swz<kGemmBK>(r)) * 16);
         }
     }
-    // the fragments of one stage, both k-steps
+    // the fragments of k-steps KK0 and KK0 + 1 of a stage
+    template <int KK0>
     __device__ __forceinline__ void read(const char *lds, half8_t (&f)[2][NF]) const {
         if constexpr (TR) {
             static_assert(NF == 2 || NF == 4, "one assembly block per operand");
@@ -210,9 +212,9 @@ struct Fragments {
 #pragma unroll
             for (int i = 0; i < NF; ++i) a[i] = base + off[i];
             if constexpr (NF == 2)
-                tr_read2<ROWS * 2>(a, v);
+                tr_read2<ROWS * 2, KK0 * 16>(a, v);
             else
-                tr_read4<ROWS * 2>(a, v);
+                tr_read4<ROWS * 2, KK0 * 16>(a, v);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
@@ -225,7 +227,7 @@ struct Fragments {
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                 for (int i = 0; i < NF; ++i)
-                    f[kk][i] = *reinterpret_cast<const half8_t *>(lds + off[kk] + i * 32 * kGemmRow);
+                    f[kk][i] = *reinterpret_cast<const half8_t *>(lds + off[KK0 + kk] + i * 32 * kGemmRow);
         }
     }
 };

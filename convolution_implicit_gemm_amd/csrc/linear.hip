@@ -17,6 +17,16 @@ namespace c3d {
 
 namespace {
 
+// A workgroup's work unit.  Workgroups are dealt to the XCDs in turn; the whole
+// tiles and the pieces are each dealt out in contiguous ranges per XCD.
+__device__ __forceinline__ void gemm_my_unit(const GemmParams &p, int &m_tile, int &n_tile, int &it0, int &it1,
+                                             int &slot) {
+    const int b = blockIdx.x;
+    const int u = b < p.dp_tiles ? xcd_range(b, p.dp_tiles)
+                                 : p.dp_tiles + xcd_range(b - p.dp_tiles, p.sk_tiles * p.sk_pieces);
+    gemm_unit(p, u, m_tile, n_tile, it0, it1, slot);
+}
+
 // ---- ring kernel: 4 waves, a ring of NS stages, one barrier per stage.
 template <typename E, bool PT, bool QT, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(256) void gemm_ring_kernel(GemmParams p) {
@@ -29,12 +39,8 @@ __global__ __launch_bounds__(256) void gemm_ring_kernel(GemmParams p) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wmi = wave / (BN / WN), wni = wave % (BN / WN);
-
-    const int b = blockIdx.x;
-    const int u = b < p.dp_tiles ? xcd_range(b, p.dp_tiles)
-                                 : p.dp_tiles + xcd_range(b - p.dp_tiles, p.sk_tiles * p.sk_pieces);
     int mt, nt, it0, it1, slot;
-    gemm_unit(p, u, mt, nt, it0, it1, slot);
+    gemm_my_unit(p, mt, nt, it0, it1, slot);
     const int m0 = mt * BM, n0 = nt * BN;
     const int k0 = it0 * kGemmBK, kend = it1 * kGemmBK < p.K ? it1 * kGemmBK : p.K;
 
@@ -42,15 +48,11 @@ __global__ __launch_bounds__(256) void gemm_ring_kernel(GemmParams p) {
     Operand<QT, BM, NQ> oq;
     op.init(p.p, p.p_stride, n0, p.N, k0, kend, wave, WAVES, lane);
     oq.init(p.q, p.q_stride, m0, p.M, k0, kend, wave, WAVES, lane);
-    uint32_t soff = 0;
     int wbuf = 0;
     auto fire = [&]() {
         char *s = smem + wbuf * STAGE;
-        op.template load<0, NP>(s, wave, WAVES, soff);
-        oq.template load<0, NQ>(s + PB, wave, WAVES, soff);
-        op.advance();
-        oq.advance();
-        soff += kGemmRow;
+        op.load(s, wave, WAVES);
+        oq.load(s + PB, wave, WAVES);
         wbuf = wbuf + 1 == NS ? 0 : wbuf + 1;
     };
     Fragments<PT, BN, TN> fp;
@@ -70,15 +72,18 @@ __global__ __launch_bounds__(256) void gemm_ring_kernel(GemmParams p) {
         gemm_barrier();  // the stage has landed, and everyone is done with the one before it
         fire();
         const char *s = smem + rbuf * STAGE;
-        half8_t a[2][TN], bq[2][TM];
-        fp.read(s, a);
-        fq.read(s + PB, bq);
+        static_for<2>([&](auto hc) {
+            constexpr int KK0 = 2 * decltype(hc)::value;
+            half8_t a[2][TN], bq[2][TM];
+            fp.template read<KK0>(s, a);
+            fq.template read<KK0>(s + PB, bq);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int i = 0; i < TN; ++i)
+                for (int i = 0; i < TN; ++i)
 #pragma unroll
-                for (int j = 0; j < TM; ++j) acc[i][j] = mfma_32x32x16<E>(a[kk][i], bq[kk][j], acc[i][j]);
+                    for (int j = 0; j < TM; ++j) acc[i][j] = mfma_32x32x16<E>(a[kk][i], bq[kk][j], acc[i][j]);
+        });
         rbuf = rbuf + 1 == NS ? 0 : rbuf + 1;
     }
     gemm_wait_loads<0>();
@@ -92,33 +97,32 @@ __global__ __launch_bounds__(256) void gemm_ring_kernel(GemmParams p) {
 
 // ---- ping-pong kernel: 8 waves in two groups of 4, one wave of each on every
 // SIMD (waves w and w + 4 share one).  Group g owns half of the tile's columns
-// and alternates between a memory phase (all MFMA fragments of one stage from
+// and alternates between a memory phase (the MFMA fragments of two k-steps from
 // LDS into registers, its share of the loads of a later stage) and a compute
-// phase (that stage's MFMAs, at raised priority); the groups run one phase
-// apart with one workgroup barrier per phase, so that each SIMD's matrix core
-// is fed by one wave while the other reads LDS.
+// phase (those MFMAs, at raised priority); the groups run one phase apart with
+// one workgroup barrier per phase, so that each SIMD's matrix core is fed by
+// one wave while the other reads LDS.
 //
-// Stage s (32 of the contraction) is read by group g in phase 2s + g and its
-// buffer in the ring of NS is refilled with stage s + NS by loads issued from
-// phase 2s + 2 on, that is NS - 1 stages ahead of their use.  A wave waits for
-// its own loads of stage s + 1 before the barrier that ends phase 2s + 1.
-template <typename E, bool PT, bool QT, int BM, int BN, int NS>
+// Stage s (64 of the contraction) is read by group g in phases 4s + g (k-steps
+// 0-1) and 4s + 2 + g (k-steps 2-3).  LDS is a ring of five operand buffers
+// that hold, in turn, p(0), q(0), p(1), q(1), ...: while stage s is computed
+// the two buffers of stage s - 1 are refilled, with q(s + 1) from the first
+// memory phase and p(s + 2) from the second, so that a load has at least two
+// and a half phases (p: six) to land.  All but p(s + 2) have to have landed
+// before phase 4s + 4: both groups wait for their own in phase 4s + 3.
+template <typename E, bool PT, bool QT, int BM, int BN>
 __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p) {
     constexpr int WM = BM / 4, WN = BN / 2, TN = WN / 32, TM = WM / 32, WAVES = 8;
-    constexpr int PB = BN * kGemmRow, QB = BM * kGemmRow, STAGE = PB + QB;
-    constexpr int NP = PB / 1024 / WAVES, NQ = QB / 1024 / WAVES;
-    constexpr int LDS = NS * STAGE > BM * BN * 2 ? NS * STAGE : BM * BN * 2;
+    static_assert(BM == BN, "the ring's buffers hold either operand");
+    constexpr int BUF = BN * kGemmRow, NP = BUF / 1024 / WAVES, NQ = NP;
+    constexpr int LDS = 5 * BUF > BM * BN * 2 ? 5 * BUF : BM * BN * 2;
     static_assert(LDS <= 160 * 1024, "LDS is 160 KiB per CU");
     __shared__ __attribute__((aligned(1024))) char smem[LDS];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int grp = wave >> 2, wmi = wave & 3, wni = grp;
-
-    const int b = blockIdx.x;
-    const int u = b < p.dp_tiles ? xcd_range(b, p.dp_tiles)
-                                 : p.dp_tiles + xcd_range(b - p.dp_tiles, p.sk_tiles * p.sk_pieces);
     int mt, nt, it0, it1, slot;
-    gemm_unit(p, u, mt, nt, it0, it1, slot);
+    gemm_my_unit(p, mt, nt, it0, it1, slot);
     const int m0 = mt * BM, n0 = nt * BN;
     const int k0 = it0 * kGemmBK, kend = it1 * kGemmBK < p.K ? it1 * kGemmBK : p.K;
 
@@ -126,46 +130,23 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p) {
     Operand<QT, BM, NQ> oq;
     op.init(p.p, p.p_stride, n0, p.N, k0, kend, wave, WAVES, lane);
     oq.init(p.q, p.q_stride, m0, p.M, k0, kend, wave, WAVES, lane);
-    uint32_t soff = 0;
-    int wbuf = 0;
-    auto fire = [&]() {
-        char *s = smem + wbuf * STAGE;
-        op.template load<0, NP>(s, wave, WAVES, soff);
-        oq.template load<0, NQ>(s + PB, wave, WAVES, soff);
-        op.advance();
-        oq.advance();
-        soff += kGemmRow;
-        wbuf = wbuf + 1 == NS ? 0 : wbuf + 1;
-    };
     Fragments<PT, BN, TN> fp;
     Fragments<QT, BM, TM> fq;
     fp.init(wni * WN, lane);
     fq.init(wmi * WM, lane);
 
-    f32x16 acc[TN][TM];
     // loads past the contraction's end read zeros, so that every wave's load
     // count stays the same
-#pragma unroll
-    for (int s = 0; s < NS - 1; ++s) fire();
+    op.load(smem, wave, WAVES);
+    oq.load(smem + BUF, wave, WAVES);
+    op.load(smem + 2 * BUF, wave, WAVES);
+    f32x16 acc[TN][TM];
     gemm_init_acc<E, WM, WN>(p, acc, slot < 0 && p.bias, n0 + wni * WN, lane);
     gemm_wait_loads<0>();
     gemm_barrier();
     if (grp) gemm_barrier();  // group 1 runs one phase behind
     half8_t a[2][TN], bq[2][TM];
-    int rbuf = 0;
-    for (int it = it0; it < it1; ++it) {
-        const char *s = smem + rbuf * STAGE;
-        if constexpr (PT || QT) {  // the transposing reads wait for themselves
-            fire();
-            fq.read(s + PB, bq);
-            fp.read(s, a);
-        } else {
-            fp.read(s, a);
-            fq.read(s + PB, bq);
-            fire();
-        }
-        if (grp) gemm_wait_loads<(NS - 2) * (NP + NQ)>();
-        gemm_barrier();
+    auto compute = [&]() {
         __builtin_amdgcn_s_setprio(2);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
@@ -174,9 +155,38 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p) {
 #pragma unroll
                 for (int j = 0; j < TM; ++j) acc[i][j] = mfma_32x32x16<E>(a[kk][i], bq[kk][j], acc[i][j]);
         __builtin_amdgcn_s_setprio(0);
-        if (!grp) gemm_wait_loads<(NS - 2) * (NP + NQ)>();
+    };
+    int pbuf = 0;  // p(s); q(s) and the refills follow it in the ring
+    auto ring = [&](int d) {
+        const int i = pbuf + d;
+        return smem + (i >= 5 ? i - 5 : i) * BUF;
+    };
+    for (int it = it0; it < it1; ++it) {
+        const char *ps = ring(0), *qs = ring(1);
+        auto memory = [&](auto hc) {
+            constexpr int H = decltype(hc)::value;
+            auto refill = [&]() {
+                if constexpr (H == 0)
+                    oq.load(ring(3), wave, WAVES);
+                else
+                    op.load(ring(4), wave, WAVES);
+            };
+            if constexpr (PT || QT) refill();  // the transposing reads wait for themselves
+            fq.template read<2 * H>(qs, bq);
+            fp.template read<2 * H>(ps, a);
+            if constexpr (!PT && !QT) refill();
+        };
+        memory(std::integral_constant<int, 0>{});
+        gemm_barrier();
+        compute();
+        gemm_barrier();
+        memory(std::integral_constant<int, 1>{});
+        if (grp) gemm_wait_loads<NP>();
+        gemm_barrier();
+        compute();
+        if (!grp) gemm_wait_loads<NP>();
         if (!(grp && it + 1 == it1)) gemm_barrier();  // group 1's last would pair with nothing
-        rbuf = rbuf + 1 == NS ? 0 : rbuf + 1;
+        pbuf = pbuf + 2 >= 5 ? pbuf - 3 : pbuf + 2;
     }
     gemm_wait_loads<0>();
     if (slot >= 0) {
@@ -281,17 +291,17 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradParams p, int grou
 }
 
 const GemmTile kTiles[] = {
-    {"m256n256k32", 256, 256, kGemmBK, 512, 1, 1.0},
-    {"m128n128k32", 128, 128, kGemmBK, 256, 2, 0.62},
+    {"m256n256k64", 256, 256, kGemmBK, 512, 1, 1.0},
+    {"m128n128k64", 128, 128, kGemmBK, 256, 2, 0.62},
 };
 
 template <typename E, bool PT, bool QT>
 hipError_t launch_tile(const GemmParams &p, int tile, hipStream_t s) {
     const dim3 grid((unsigned)(p.dp_tiles + p.sk_tiles * p.sk_pieces));
     if (tile == 0)
-        hipLaunchKernelGGL((gemm_pp_kernel<E, PT, QT, 256, 256, 5>), grid, dim3(512), 0, s, p);
+        hipLaunchKernelGGL((gemm_pp_kernel<E, PT, QT, 256, 256>), grid, dim3(512), 0, s, p);
     else
-        hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 128, 128, 64, 64, 4>), grid, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 128, 128, 64, 64, 2>), grid, dim3(256), 0, s, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.sk_tiles) return e;
     const GemmTile &t = kTiles[tile];

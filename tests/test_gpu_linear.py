@@ -10,7 +10,7 @@ from token_helpers import (ACTS, DTYPES, U24, act64, assert_unmarked_only, asser
 
 pytestmark = pytest.mark.gpu
 
-TILES = [None, "m128n128k32", "m256n256k32"]
+TILES = [None, "m128n128k64", "m256n256k64"]
 
 
 def run_forward(m, n, k, act, dtype, bias, residual, keep, gap, seed, tile=None, x=None, w=None):
@@ -84,7 +84,7 @@ def test_forward_is_exact_on_small_integers(size, tile):
 
 def test_split_contraction_joins_all_pieces():
     # few tiles and a long contraction: the plan splits it, and each piece counts
-    plan, x, w, b, r, y, z = run_forward(256, 256, 16384, "gelu", "bf16", True, True, True, 8, 3, "m128n128k32")
+    plan, x, w, b, r, y, z = run_forward(256, 256, 16384, "gelu", "bf16", True, True, True, 8, 3, "m128n128k64")
     assert plan.info().split_pieces > 1
     yr, zr, mag = linear64(x, w, b, r, "gelu")
     zs, ys = linear_slack(16384, mag, zr, yr, "gelu")
