@@ -212,7 +212,7 @@ def _addr(t, what="tensor", elems=None, dtype=None):
         return t
     if not t.is_contiguous():
         raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is not contiguous (pass .contiguous())" % what)
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is on %s, not on a GPU" % (what, t.device))
     if dtype is not None and t.dtype != dtype:
         raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is %s, the plan expects %s" % (what, t.dtype, dtype))
@@ -239,7 +239,9 @@ def _conv_sizes(desc, chunk_t=None):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle of the current stream of the current device, without
+        # building a Stream object (2.8 us of a small call's host time)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -392,29 +394,32 @@ def _strided_addr(t, what, sizes, strides, dtype):
     (in elements, outermost first) from its first one, lie inside its storage."""
     if t is None or isinstance(t, int):
         return t
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is on %s, not on a GPU" % (what, t.device))
     if t.dtype != dtype:
         raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is %s, %s expected" % (what, t.dtype, dtype))
-    if any(n == 0 for n in sizes):
+    have = t.stride()
+    if have == strides and t.shape == sizes:
+        return t.data_ptr() or None  # a view laid out as the call reads it
+    if 0 in sizes:
         return t.data_ptr() or None
-    if t.dim() >= 2 and t.dim() == len(sizes):
-        # a view of the same shape has to be laid out as the call reads it
-        for n, have, want in zip(t.shape, t.stride(), strides):
-            if n > 1 and have != want:
+    if len(have) >= 2 and len(have) == len(sizes):
+        # a size of one may have any stride
+        for n, st, want in zip(t.shape, have, strides):
+            if n > 1 and st != want:
                 raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s has strides %s, the call reads %s"
-                                  % (what, tuple(t.stride()), tuple(strides)))
+                                  % (what, tuple(have), tuple(strides)))
     elif not t.is_contiguous():
         raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is not contiguous" % what)
     last = sum((n - 1) * st for n, st in zip(sizes, strides))
-    have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
-    if last >= have:
-        raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s holds %d elements, %d needed" % (what, have, last + 1))
+    room = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    if last >= room:
+        raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s holds %d elements, %d needed" % (what, room, last + 1))
     return t.data_ptr()
 
 
 def _rows_addr(t, what, rows, cols, stride, dtype):
-    return _strided_addr(t, what, (rows, cols), (stride or cols, 1), dtype)
+    return None if t is None else _strided_addr(t, what, (rows, cols), (stride or cols, 1), dtype)
 
 
 def _workspace_bytes(workspace, workspace_bytes, planned=0):
@@ -432,6 +437,8 @@ class LinearPlan:
         self.handle = handle
         self.workspace_bytes = workspace_bytes
         self.desc = desc
+        d = desc
+        self.sizes = (d.m, d.n, d.k, d.x_stride, d.y_stride, d.residual_stride, _elem_dtype(d.flags & CONV3D_F_BF16))
 
     def info(self) -> linear_plan_info:
         return linear_plan_query(self)
@@ -469,13 +476,12 @@ def linear_plan_destroy(plan: LinearPlan) -> None:
 def linear_forward(plan: LinearPlan, x, w, bias, residual, y, preact=None, workspace=None, workspace_bytes=None,
                    stream=None) -> None:
     """Enqueue y = act(x w^T + bias) + residual (and preact, the value before act) on ``stream``."""
-    d, dt = plan.desc, _elem_dtype(plan.desc.flags & CONV3D_F_BF16)
-    _check(load_library().linear_forward(
-        plan.handle, _rows_addr(x, "x", d.m, d.k, d.x_stride, dt), _addr(w, "w", d.n * d.k, dt),
-        _addr(bias, "bias", d.n, dt), _rows_addr(residual, "residual", d.m, d.n, d.residual_stride, dt),
-        _rows_addr(y, "y", d.m, d.n, d.y_stride, dt), _rows_addr(preact, "preact", d.m, d.n, 0, dt),
-        _addr(workspace, "workspace"), _workspace_bytes(workspace, workspace_bytes, plan.workspace_bytes),
-        _stream(stream)))
+    m, n, k, xs, ys, rs, dt = plan.sizes
+    _check((_lib or load_library()).linear_forward(
+        plan.handle, _rows_addr(x, "x", m, k, xs, dt), _addr(w, "w", n * k, dt), _addr(bias, "bias", n, dt),
+        _rows_addr(residual, "residual", m, n, rs, dt), _rows_addr(y, "y", m, n, ys, dt),
+        _rows_addr(preact, "preact", m, n, 0, dt), _addr(workspace, "workspace"),
+        _workspace_bytes(workspace, workspace_bytes, plan.workspace_bytes), _stream(stream)))
 
 
 def linear_backward_workspace(plan: LinearPlan) -> int:
@@ -485,13 +491,14 @@ def linear_backward_workspace(plan: LinearPlan) -> int:
 def linear_backward(plan: LinearPlan, dy, x, w, preact, dx, dw, dbias, workspace, workspace_bytes=None,
                     stream=None) -> None:
     """Enqueue the gradients dx, dw and dbias (each may be None) of one product on ``stream``."""
-    d, dt = plan.desc, _elem_dtype(plan.desc.flags & CONV3D_F_BF16)
-    _check(load_library().linear_backward(
-        plan.handle, _rows_addr(dy, "dy", d.m, d.n, d.y_stride, dt), _rows_addr(x, "x", d.m, d.k, d.x_stride, dt),
-        _addr(w, "w", d.n * d.k, dt), _rows_addr(preact, "preact", d.m, d.n, 0, dt),
-        _rows_addr(dx, "dx", d.m, d.k, d.x_stride, dt), _addr(dw, "dw", d.n * d.k, dt), _addr(dbias, "dbias", d.n, dt),
-        _addr(workspace, "workspace"),
-        _workspace_bytes(workspace, workspace_bytes, linear_backward_workspace(plan)), _stream(stream)))
+    m, n, k, xs, ys, _, dt = plan.sizes
+    if workspace_bytes is None and isinstance(workspace, int):
+        workspace_bytes = linear_backward_workspace(plan)
+    _check((_lib or load_library()).linear_backward(
+        plan.handle, _rows_addr(dy, "dy", m, n, ys, dt), _rows_addr(x, "x", m, k, xs, dt), _addr(w, "w", n * k, dt),
+        _rows_addr(preact, "preact", m, n, 0, dt), _rows_addr(dx, "dx", m, k, xs, dt), _addr(dw, "dw", n * k, dt),
+        _addr(dbias, "dbias", n, dt), _addr(workspace, "workspace"), _workspace_bytes(workspace, workspace_bytes),
+        _stream(stream)))
 
 
 def layernorm(x, gamma, beta, y, stats, rows, c, eps, x_stride=0, y_stride=0, stream=None, bf16=False) -> None:
@@ -520,13 +527,14 @@ def layernorm_backward(dy, x, gamma, stats, dres, dx, dgamma, dbeta, rows, c, wo
     dres, dgamma and dbeta may be None."""
     lib, dt = load_library(), _elem_dtype(bf16)
     import torch
+    if workspace_bytes is None and isinstance(workspace, int):
+        workspace_bytes = layernorm_backward_workspace(rows, c)
     fn = lib.layernorm_backward_bf16 if bf16 else lib.layernorm_backward
     _check(fn(_rows_addr(dy, "dy", rows, c, y_stride, dt), _rows_addr(x, "x", rows, c, x_stride, dt),
               _addr(gamma, "gamma", c, dt), _addr(stats, "stats", 2 * rows, torch.float32),
               _rows_addr(dres, "dres", rows, c, x_stride, dt), _rows_addr(dx, "dx", rows, c, x_stride, dt),
               _addr(dgamma, "dgamma", c, dt), _addr(dbeta, "dbeta", c, dt), rows, c, x_stride, y_stride,
-              _addr(workspace, "workspace"),
-              _workspace_bytes(workspace, workspace_bytes, layernorm_backward_workspace(rows, c)), _stream(stream)))
+              _addr(workspace, "workspace"), _workspace_bytes(workspace, workspace_bytes), _stream(stream)))
 
 
 def layernorm_backward_bf16(dy, x, gamma, stats, dres, dx, dgamma, dbeta, rows, c, workspace, x_stride=0, y_stride=0,
@@ -542,6 +550,20 @@ class RopePlan:
     def __init__(self, handle, desc):
         self.handle = handle
         self.desc = desc
+        d = desc
+        tokens = d.t * d.h * d.w
+
+        def layout(heads, stride):
+            stride = tuple(stride)
+            if not any(stride):
+                stride = (tokens * heads * d.head_dim, heads * d.head_dim, d.head_dim)
+            return (d.n, tokens, heads, d.head_dim), stride + (1,)
+
+        # (sizes, strides) of q, k, q_out and k_out
+        self.layouts = (layout(d.heads_q, d.q_stride), layout(d.heads_k, d.k_stride),
+                        layout(d.heads_q, d.q_out_stride), layout(d.heads_k, d.k_out_stride))
+        self.positions = d.n * tokens * 3 if d.flags & CONV3D_F_POSITIONS else 0
+        self.dtype = _elem_dtype(d.flags & CONV3D_F_BF16)
 
     def __del__(self):
         if self.handle and _lib is not None:
@@ -571,39 +593,28 @@ def rope3d_plan_destroy(plan: RopePlan) -> None:
         plan.handle = None
 
 
-def _rope_call(name, plan, q, k, q_out, k_out, positions, t_offset, stream, strides):
+def _rope_call(fn, plan, q, k, q_out, k_out, positions, t_offset, stream, layouts):
     import torch
-    d = plan.desc
-    tokens, dt = d.t * d.h * d.w, _elem_dtype(d.flags & CONV3D_F_BF16)
-
-    def addr(t, what, heads, stride):
-        stride = tuple(stride)
-        if not any(stride):
-            stride = (tokens * heads * d.head_dim, heads * d.head_dim, d.head_dim)
-        return _strided_addr(t, what, (d.n, tokens, heads, d.head_dim), stride + (1,), dt)
-
-    if d.heads_k == 0:
+    lq, lk, lqo, lko = layouts
+    dt = plan.dtype
+    if lk[0][2] == 0:
         k = k_out = None
-    if not d.flags & CONV3D_F_POSITIONS:
-        positions = None
-    _check(getattr(load_library(), name)(
-        plan.handle, addr(q, "q", d.heads_q, strides[0]), addr(k, "k", d.heads_k, strides[1]),
-        addr(q_out, "q_out", d.heads_q, strides[2]), addr(k_out, "k_out", d.heads_k, strides[3]),
-        _addr(positions, "positions", d.n * tokens * 3, torch.int32), t_offset, _stream(stream)))
+    given = positions if plan.positions else None
+    _check(fn(plan.handle, _strided_addr(q, "q", *lq, dt), _strided_addr(k, "k", *lk, dt),
+              _strided_addr(q_out, "q_out", *lqo, dt), _strided_addr(k_out, "k_out", *lko, dt),
+              _addr(given, "positions", plan.positions, torch.int32), t_offset, _stream(stream)))
 
 
 def rope3d_forward(plan: RopePlan, q, k, q_out, k_out, positions=None, t_offset=0, stream=None) -> None:
     """Enqueue the rotation of q into q_out and k into k_out on ``stream``."""
-    d = plan.desc
-    _rope_call("rope3d_forward", plan, q, k, q_out, k_out, positions, t_offset, stream,
-               (d.q_stride, d.k_stride, d.q_out_stride, d.k_out_stride))
+    _rope_call(load_library().rope3d_forward, plan, q, k, q_out, k_out, positions, t_offset, stream, plan.layouts)
 
 
 def rope3d_backward(plan: RopePlan, dq_out, dk_out, dq, dk, positions=None, t_offset=0, stream=None) -> None:
     """Enqueue the gradient of rope3d_forward (strides: those of the outputs, then of the inputs)."""
-    d = plan.desc
-    _rope_call("rope3d_backward", plan, dq_out, dk_out, dq, dk, positions, t_offset, stream,
-               (d.q_out_stride, d.k_out_stride, d.q_stride, d.k_stride))
+    lq, lk, lqo, lko = plan.layouts
+    _rope_call(load_library().rope3d_backward, plan, dq_out, dk_out, dq, dk, positions, t_offset, stream,
+               (lqo, lko, lq, lk))
 
 
 def conv3d_calibrate_scratch_bytes() -> int:

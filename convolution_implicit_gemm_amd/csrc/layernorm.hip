@@ -111,8 +111,9 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_kernel(LnParams p
 template <typename E, int NV, int WPR>
 __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGradParams p) {
     constexpr int TEAMS = ln_threads<WPR>() / 64 / WPR;
+    constexpr int SPAN = NV * WPR * 512;  // columns a team covers
     __shared__ float red[TEAMS * 2 * WPR];
-    __shared__ float join[TEAMS > 1 ? NV * WPR * 512 : 1];
+    __shared__ __attribute__((aligned(16))) float join[TEAMS > 1 ? TEAMS * SPAN : 4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int team = wave / WPR, wt = wave % WPR;
     const int first = (wt * 64 + lane) * 8;
@@ -124,31 +125,45 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGra
     for (int i = 0; i < NV; ++i) {
         const int c = first + i * WPR * 512;
         ga[i] = p.gamma && c < p.c ? load_vec<E>(p.gamma + c) : e16x8_t{};
+#pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (!p.gamma) ga[i][e] = from_f32<E>(1.0f);
             dg[i][e] = db[i][e] = 0.0f;
         }
     }
-    for (int64_t row0 = (int64_t)blockIdx.x * TEAMS; row0 < p.rows; row0 += (int64_t)gridDim.x * TEAMS) {
-        const int64_t row = row0 + team;
+    // The next row's loads are issued before the current row is worked on.
+    struct Row {
+        e16x8_t x[NV], dy[NV], dres[NV];
+        float2 st;
+    };
+    const int64_t step = (int64_t)gridDim.x * TEAMS;
+    auto fetch = [&](int64_t row, Row &r) {
         const bool live = row < p.rows;
-        const _Float16 *xr = p.x + row * p.x_stride, *gr = p.dy + row * p.y_stride;
-        const float2 st = live ? p.stats[row] : make_float2(0.0f, 0.0f);
-        e16x8_t xv[NV], gv[NV];
+        r.st = live ? p.stats[row] : make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = first + i * WPR * 512;
             const bool in = live && c < p.c;
-            xv[i] = in ? load_vec<E>(xr + c) : e16x8_t{};
-            gv[i] = in ? load_vec<E>(gr + c) : e16x8_t{};
+            r.x[i] = in ? load_vec<E>(p.x + row * p.x_stride + c) : e16x8_t{};
+            r.dy[i] = in ? load_vec<E>(p.dy + row * p.y_stride + c) : e16x8_t{};
+            r.dres[i] = in && p.dres ? load_vec<E>(p.dres + row * p.x_stride + c) : e16x8_t{};
         }
+    };
+    Row cur, next;
+    int64_t row = (int64_t)blockIdx.x * TEAMS + team;
+    const int64_t rounds = (p.rows - (int64_t)blockIdx.x * TEAMS + step - 1) / step;  // the same for all teams
+    fetch(row, cur);
+    for (int64_t k = 0; k < rounds; ++k, row += step) {
+        if (k + 1 < rounds) fetch(row + step, next);
         float s1 = 0.0f, s2 = 0.0f;
+        // columns past the end and rows past the end read zeros with zero
+        // statistics: they add nothing
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (live && first + i * WPR * 512 < p.c)
+            if (first + i * WPR * 512 < p.c)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float xh = (to_f32<E>(xv[i][e]) - st.x) * st.y, d = to_f32<E>(gv[i][e]);
+                    const float xh = (to_f32<E>(cur.x[i][e]) - cur.st.x) * cur.st.y, d = to_f32<E>(cur.dy[i][e]);
                     const float g = d * to_f32<E>(ga[i][e]);
                     s1 += g;
                     s2 = fmaf(g, xh, s2);
@@ -157,73 +172,90 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGra
                 }
         s1 = team_sum<WPR>(s1, slot, wt, 0) * inv_c;
         s2 = team_sum<WPR>(s2, slot, wt, 1) * inv_c;
-        if (!live) continue;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = first + i * WPR * 512;
-            if (c >= p.c) continue;
-            const e16x8_t rv = p.dres ? load_vec<E>(p.dres + row * p.x_stride + c) : e16x8_t{};
-            e16x8_t o;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float xh = (to_f32<E>(xv[i][e]) - st.x) * st.y;
-                const float g = to_f32<E>(gv[i][e]) * to_f32<E>(ga[i][e]);
-                o[e] = from_f32<E>(fmaf(st.y, g - s1 - xh * s2, to_f32<E>(rv[e])));
-            }
-            *reinterpret_cast<e16x8_t *>(p.dx + row * p.x_stride + c) = o;
-        }
-    }
-    if (!p.part) return;
-    float *out = p.part + (int64_t)blockIdx.x * 2 * p.c;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        if constexpr (TEAMS > 1) {  // add the teams in turn
-            for (int t = 0; t < TEAMS; ++t) {
-                __syncthreads();
-                if (team == t)
-#pragma unroll
-                    for (int i = 0; i < NV; ++i)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float *j = join + first + i * WPR * 512 + e;
-                            const float v = which ? db[i][e] : dg[i][e];
-                            *j = t == 0 ? v : *j + v;
-                        }
-            }
-            __syncthreads();
-            for (int c = threadIdx.x; c < p.c; c += ln_threads<WPR>()) out[which * p.c + c] = join[c];
-            __syncthreads();
-        } else {
+        if (row < p.rows)
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = first + i * WPR * 512;
-                if (c < p.c)
+                if (c >= p.c) continue;
+                e16x8_t o;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) out[which * p.c + c + e] = which ? db[i][e] : dg[i][e];
+                for (int e = 0; e < 8; ++e) {
+                    const float xh = (to_f32<E>(cur.x[i][e]) - cur.st.x) * cur.st.y;
+                    const float g = to_f32<E>(cur.dy[i][e]) * to_f32<E>(ga[i][e]);
+                    o[e] = from_f32<E>(fmaf(cur.st.y, g - s1 - xh * s2, to_f32<E>(cur.dres[i][e])));
+                }
+                *reinterpret_cast<e16x8_t *>(p.dx + row * p.x_stride + c) = o;
             }
+        cur = next;
+    }
+    if (!p.part) return;
+    float *out = p.part + (int64_t)blockIdx.x * 2 * p.c;
+    auto put = [&](float *to, const float (&v)[8]) {
+        *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    };
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = first + i * WPR * 512;
+            if constexpr (TEAMS > 1)
+                put(join + team * SPAN + c, which ? db[i] : dg[i]);
+            else if (c < p.c)
+                put(out + which * p.c + c, which ? db[i] : dg[i]);
+        }
+        if constexpr (TEAMS > 1) {  // add the teams in turn
+            __syncthreads();
+            for (int c = threadIdx.x * 4; c < p.c; c += ln_threads<WPR>() * 4) {
+                float4 t = *reinterpret_cast<const float4 *>(join + c);
+#pragma unroll
+                for (int k = 1; k < TEAMS; ++k) {
+                    const float4 u = *reinterpret_cast<const float4 *>(join + k * SPAN + c);
+                    t.x += u.x;
+                    t.y += u.y;
+                    t.z += u.z;
+                    t.w += u.w;
+                }
+                *reinterpret_cast<float4 *>(out + which * p.c + c) = t;
+            }
+            __syncthreads();
         }
     }
 }
 
-// Column sums of fp32 partials [rows][cols]: a block takes 16 columns, 16
-// threads per column add every 16th row, then the 16 sums in order.
+// Column sums of fp32 partials [rows][cols] (cols a multiple of 8): a block
+// takes 16 columns, 64 threads per 4 columns add every 64th row, then the 64
+// sums in order.
 template <typename E>
 __global__ __launch_bounds__(256) void column_sum_kernel(const float *part, int rows, int cols, _Float16 *out0,
                                                          _Float16 *out1, int split) {
-    __shared__ float s[16][17];
-    const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4;
-    const int c = blockIdx.x * 16 + tc;
-    float v = 0.0f;
-    if (c < cols)
-        for (int r = tr; r < rows; r += 16) v += part[(int64_t)r * cols + c];
-    s[tr][tc] = v;
+    __shared__ float s[64][17];
+    const int tc = threadIdx.x & 3, tr = threadIdx.x >> 2;
+    const int c = blockIdx.x * 16 + tc * 4;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < cols) {
+#pragma unroll 8
+        for (int r = tr; r < rows; r += 64) {
+            const float4 u = *reinterpret_cast<const float4 *>(part + (int64_t)r * cols + c);
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+        }
+    }
+    s[tr][tc * 4 + 0] = v.x;
+    s[tr][tc * 4 + 1] = v.y;
+    s[tr][tc * 4 + 2] = v.z;
+    s[tr][tc * 4 + 3] = v.w;
     __syncthreads();
-    if (tr == 0 && c < cols) {
-        float t = 0.0f;
+    const int col = threadIdx.x >> 4, q = threadIdx.x & 15;  // 16 threads per column, 4 sums each
+    float t = s[q * 4][col] + s[q * 4 + 1][col] + s[q * 4 + 2][col] + s[q * 4 + 3][col];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) t += s[i][tc];
-        _Float16 *o = c < split ? out0 : out1;
-        if (o) o[c < split ? c : c - split] = from_f32<E>(t);
+    for (int off = 8; off > 0; off >>= 1) t += __shfl_xor(t, off);
+    const int oc = blockIdx.x * 16 + col;
+    if (q == 0 && oc < cols) {
+        _Float16 *o = oc < split ? out0 : out1;
+        if (o) o[oc < split ? oc : oc - split] = from_f32<E>(t);
     }
 }
 
@@ -263,7 +295,8 @@ hipError_t launch_layernorm(const LnParams &p, hipStream_t s) {
 }
 
 int32_t ln_grad_blocks(int64_t rows, int32_t c) {
-    const int64_t want = (rows + ln_teams(c) - 1) / ln_teams(c);
+    // at least two rows per team: a block's partial costs about as much as a row
+    const int64_t want = (rows + 2 * ln_teams(c) - 1) / (2 * ln_teams(c));
     return (int32_t)(want < 512 ? want : 512);
 }
 

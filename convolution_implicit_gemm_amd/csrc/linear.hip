@@ -197,31 +197,30 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p) {
     gemm_store_tile<E, BM, BN, WM, WN, 512>(p, acc, smem, m0, n0, wmi, wni, lane);
 }
 
-// ---- the pieces of the split tiles, added in order, then the epilogue.  One
-// thread per 4 adjacent columns; blocks of the tile's fragment order.
-template <typename E, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p) {
-    constexpr int TN = WN / 32, TM = WM / 32, QUADS = BM * BN / 4;
-    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int st = (int)(idx / QUADS), qd = (int)(idx - (int64_t)st * QUADS);
-    if (st >= p.sk_tiles) return;
-    int mt, nt, it0, it1, slot;
-    gemm_unit(p, p.dp_tiles + st * p.sk_pieces, mt, nt, it0, it1, slot);
-    const int lane = qd & 63;
-    int r = qd >> 6;
-    const int g = r & 3;
-    r >>= 2;
-    const int j = r % TM;
-    r /= TM;
-    const int i = r % TN, wave = r / TN;
-    const int wmi = wave / (BN / WN), wni = wave % (BN / WN);
-    const int m = mt * BM + wmi * WM + j * 32 + (lane & 31);
-    const int n = nt * BN + wni * WN + i * 32 + 8 * g + 4 * (lane >> 5);
-    if (m >= p.M || n >= p.N) return;
-    const f32x4 *pp = reinterpret_cast<const f32x4 *>(p.partial) + (size_t)st * p.sk_pieces * QUADS + qd;
-    f32x4 v = pp[0];
-#pragma unroll 4
-    for (int k = 1; k < p.sk_pieces; ++k) v += pp[(size_t)k * QUADS];
+// ---- few rows (m <= 16): the product is the stream of w from HBM.  A block
+// takes 16 columns and splits the contraction over its WAVES waves; every lane
+// reads w's rows straight into the MFMA's A fragment (16x16x32: 16 columns, 64
+// contiguous bytes of each), several in flight, and the rows of x (which stay
+// in cache) into B.  The waves' sums meet in LDS, in wave order; one wave runs the
+// epilogue.  No LDS staging, no second launch.
+template <typename E>
+__device__ __forceinline__ f32x4 mfma_16x16x32(half8_t a, half8_t b, f32x4 c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (std::is_same_v<E, __bf16>)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
+                                                       c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+#else
+    (void)a;
+    (void)b;
+    return c;
+#endif
+}
+
+// The epilogue of 4 adjacent columns of one row (v: the full sums, without bias).
+template <typename E>
+__device__ __forceinline__ void gemm_finish_quad(const GemmParams &p, f32x4 v, int m, int n) {
     if (p.bias) {
         const half4_t bv = *reinterpret_cast<const half4_t *>(p.bias + n);
 #pragma unroll
@@ -248,6 +247,70 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p) {
     *reinterpret_cast<half4_t *>(p.y + (int64_t)m * p.y_stride + n) = h;
 }
 
+constexpr int kRowsWaves = 8, kRowsAhead = 8;
+template <typename E>
+__global__ __launch_bounds__(kRowsWaves * 64) void gemm_rows_kernel(GemmParams p) {
+    __shared__ f32x4 sums[kRowsWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r16 = lane & 15, kq = (lane >> 4) * 8;
+    const int n0 = blockIdx.x * 16;
+    // columns and rows past the end read the last one; their sums are dropped
+    const int nr = n0 + r16 < p.N ? n0 + r16 : p.N - 1, mr = r16 < p.M ? r16 : p.M - 1;
+    const _Float16 *wp = p.p + (int64_t)nr * p.p_stride + kq;
+    const _Float16 *xp = p.q + (int64_t)mr * p.q_stride + kq;
+    // this wave's steps of 32
+    const int steps = (p.K + 31) / 32;
+    const int s0 = steps * wave / kRowsWaves, s1 = steps * (wave + 1) / kRowsWaves;
+    f32x4 acc = {};
+    for (int s = s0; s < s1; s += kRowsAhead) {
+        half8_t a[kRowsAhead], b[kRowsAhead];
+#pragma unroll
+        for (int u = 0; u < kRowsAhead; ++u) {
+            const int k = (s + u) * 32;
+            const bool in = s + u < s1 && k + kq < p.K;
+            a[u] = in ? *reinterpret_cast<const half8_t *>(wp + k) : half8_t{};
+            b[u] = in ? *reinterpret_cast<const half8_t *>(xp + k) : half8_t{};
+        }
+#pragma unroll
+        for (int u = 0; u < kRowsAhead; ++u) acc = mfma_16x16x32<E>(a[u], b[u], acc);
+    }
+    sums[wave][lane] = acc;
+    __syncthreads();
+    const int n = n0 + 4 * (lane >> 4);
+    if (wave != 0 || r16 >= p.M || n >= p.N) return;
+#pragma unroll
+    for (int i = 1; i < kRowsWaves; ++i) acc += sums[i][lane];
+    gemm_finish_quad<E>(p, acc, r16, n);
+}
+
+// ---- the pieces of the split tiles, added in order, then the epilogue.  One
+// thread per 4 adjacent columns; blocks of the tile's fragment order.
+template <typename E, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p) {
+    constexpr int TN = WN / 32, TM = WM / 32, QUADS = BM * BN / 4;
+    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int st = (int)(idx / QUADS), qd = (int)(idx - (int64_t)st * QUADS);
+    if (st >= p.sk_tiles) return;
+    int mt, nt, it0, it1, slot;
+    gemm_unit(p, p.dp_tiles + st * p.sk_pieces, mt, nt, it0, it1, slot);
+    const int lane = qd & 63;
+    int r = qd >> 6;
+    const int g = r & 3;
+    r >>= 2;
+    const int j = r % TM;
+    r /= TM;
+    const int i = r % TN, wave = r / TN;
+    const int wmi = wave / (BN / WN), wni = wave % (BN / WN);
+    const int m = mt * BM + wmi * WM + j * 32 + (lane & 31);
+    const int n = nt * BN + wni * WN + i * 32 + 8 * g + 4 * (lane >> 5);
+    if (m >= p.M || n >= p.N) return;
+    const f32x4 *pp = reinterpret_cast<const f32x4 *>(p.partial) + (size_t)st * p.sk_pieces * QUADS + qd;
+    f32x4 v = pp[0];
+#pragma unroll 4
+    for (int k = 1; k < p.sk_pieces; ++k) v += pp[(size_t)k * QUADS];
+    gemm_finish_quad<E>(p, v, m, n);
+}
+
 // ---- dz = dy act'(z) and its column sums.  A block walks a strip of rows for
 // 256 groups of 8 columns (or, where there are fewer, several rows at once) and
 // writes the strip's fp32 sums.
@@ -259,6 +322,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradParams p, int grou
     float sum[8] = {};
     if (rl < rows_at_once && c < p.n) {
         const int64_t r0 = p.m * blockIdx.y / p.strips, r1 = p.m * (blockIdx.y + 1) / p.strips;
+#pragma unroll 4
         for (int64_t r = r0 + rl; r < r1; r += rows_at_once) {
             const half8_t d = *reinterpret_cast<const half8_t *>(p.dy + r * p.dy_stride + c);
             half8_t o;
@@ -293,6 +357,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradParams p, int grou
 const GemmTile kTiles[] = {
     {"m256n256k64", 256, 256, kGemmBK, 512, 1, 1.0},
     {"m128n128k64", 128, 128, kGemmBK, 256, 2, 0.62},
+    {"m16n16k32", 16, 16, 32, kRowsWaves * 64, 4, 0.0},  // few rows; no share in the cost model
 };
 
 template <typename E, bool PT, bool QT>
@@ -321,6 +386,14 @@ const GemmTile *gemm_tiles(int *count) {
 }
 
 hipError_t launch_gemm(const GemmParams &p, int tile, GemmLayout layout, hipStream_t s) {
+    if (tile == kGemmRowsTile) {
+        const dim3 grid((unsigned)((p.N + 15) / 16));
+        if (p.bf16)
+            hipLaunchKernelGGL((gemm_rows_kernel<__bf16>), grid, dim3(kRowsWaves * 64), 0, s, p);
+        else
+            hipLaunchKernelGGL((gemm_rows_kernel<_Float16>), grid, dim3(kRowsWaves * 64), 0, s, p);
+        return hipGetLastError();
+    }
     switch (layout) {
         case kGemmForward:
             return p.bf16 ? launch_tile<__bf16, false, false>(p, tile, s)

@@ -5,12 +5,14 @@
 // The gradient is the turn by the negative angle.
 //
 // A stream over HBM: each element is read and written once (in place, if the
-// caller wants), so the rest has to hide behind that.  A thread owns one group
-// of pairs of one token (8 adjacent elements, or 8 + 8 of the two halves) and
-// walks a range of the token's query and key heads with the same sines and
-// cosines, which it computes itself: whole turns are dropped from the angle in
-// 64 bits (positions of any size keep their accuracy), the rest goes through
-// fp32 sincospi.  No table, no extra launch, no extra traffic.
+// caller wants), so the rest has to hide behind that.  A block takes some
+// tokens: first its threads work out the sines and cosines of (token, pair), once
+// for all heads, into LDS; whole turns are dropped from the angle in 64 bits
+// (positions of any size keep their accuracy), the rest goes through fp32
+// sincospi.  Then they walk the tokens' heads in memory order, one task per
+// thread and step (a task: 8 adjacent elements, or 8 + 8 of the two halves), so
+// that a wave reads and writes whole runs of a token's row.  No table, no extra
+// launch, no extra traffic.
 #include "elem16.h"
 #include "token_internal.h"
 
@@ -19,93 +21,108 @@ namespace c3d {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBatch = 4;       // tasks of a thread whose loads are in flight at once
+constexpr int kRopeMaxTokens = 16;  // tokens of a block
 
 // HALVES: the pair is (p, p + pairs) instead of (2p, 2p + 1).
 template <typename E, bool HALVES>
-__global__ __launch_bounds__(kRopeThreads) void rope3d_kernel(RopeParams p, int tasks, int tokens_per_block,
-                                                              int heads_per_block) {
-    constexpr int NP = HALVES ? 8 : 4;  // pairs of a rotating task
-    const int slot = threadIdx.x / tasks, task = threadIdx.x - slot * tasks;
-    const int64_t idx = (int64_t)blockIdx.x * tokens_per_block + slot;  // flattened (sample, token)
-    if (slot >= tokens_per_block || idx >= p.tokens * p.n) return;
-    const int ns = (int)(idx / p.tokens);
-    const int64_t tok = idx - (int64_t)ns * p.tokens;
+__global__ __launch_bounds__(kRopeThreads) void rope3d_kernel(RopeParams p, int tasks, int tokens_per_block) {
+    extern __shared__ float2 turn[];  // [token][pair] (cos, sin)
+    const int64_t first = (int64_t)blockIdx.x * tokens_per_block;  // flattened (sample, token)
+    const int64_t left = p.tokens * p.n - first;
+    const int ntok = left < tokens_per_block ? (int)left : tokens_per_block;
 
-    // the task's elements: group e0 (and e1 = e0 + pairs), turned for pairs p0 .. p0 + NP - 1
-    const int turning = p.pairs / NP;  // tasks of whole groups of pairs
-    int e0, np, p0;
-    if (HALVES) {
-        const bool turn = task < turning;
-        e0 = turn ? task * 8 : 2 * p.pairs + (task - turning) * 8;
-        np = turn ? 8 : 0;
-        p0 = task * 8;
-    } else {
-        e0 = task * 8;
-        p0 = task * 4;
-        np = p.pairs - p0;
-        np = np < 0 ? 0 : (np > 4 ? 4 : np);
-    }
-    float cs[NP], sn[NP];
-    {
-        double pos[3];
+    for (int i = threadIdx.x; i < ntok * p.pairs; i += kRopeThreads) {
+        const int t = i / p.pairs, pr = i - t * p.pairs;
+        const int axis = pr < p.end_t ? 0 : pr < p.end_h ? 1 : 2;
+        const int64_t idx = first + t;
+        double pos;
         if (p.positions) {
-            const int32_t *pp = p.positions + idx * 3;
-            for (int a = 0; a < 3; ++a) pos[a] = (double)pp[a];
+            pos = (double)p.positions[idx * 3 + axis];
         } else {
+            const int64_t tok = idx % p.tokens;
             const int64_t hw = (int64_t)p.h * p.w;
-            const int64_t t = tok / hw;
-            const int r = (int)(tok - t * hw);
-            pos[0] = (double)(t + p.t_offset);
-            pos[1] = (double)(r / p.w);
-            pos[2] = (double)(r % p.w);
+            const int64_t frame = tok / hw;
+            const int r = (int)(tok - frame * hw);
+            pos = axis == 0 ? (double)(frame + p.t_offset) : (double)(axis == 1 ? r / p.w : r % p.w);
         }
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            cs[i] = 1.0f;
-            sn[i] = 0.0f;
-            if (i < np) {
-                const int pr = p0 + i;
-                double turns = (pr < p.end_t ? pos[0] : pr < p.end_h ? pos[1] : pos[2]) * p.turns[pr];
-                turns -= rint(turns);
-                sincospif(2.0f * (float)turns, &sn[i], &cs[i]);
-                if (p.inverse) sn[i] = -sn[i];
-            }
-        }
+        double turns = pos * p.turns[pr];
+        turns -= rint(turns);
+        float sn, cs;
+        sincospif(2.0f * (float)turns, &sn, &cs);
+        turn[i] = make_float2(cs, p.inverse ? -sn : sn);
     }
+    __syncthreads();
 
     const int heads = p.q.heads + p.k.heads;
-    const int h0 = blockIdx.y * heads_per_block;
-    const int h1 = h0 + heads_per_block < heads ? h0 + heads_per_block : heads;
-    for (int hh = h0; hh < h1; ++hh) {
+    const int per_token = heads * tasks, items = ntok * per_token;
+    const int turning = HALVES ? p.pairs / 8 : (p.pairs + 3) / 4;  // tasks that turn pairs
+    struct Item {
+        const _Float16 *in;
+        _Float16 *out;
+        const float2 *cs;
+        bool turns;
+        int np;
+    };
+    auto item = [&](int i) {
+        const int t = i / per_token, r = i - t * per_token;
+        const int hh = r / tasks, task = r - hh * tasks;
+        const int64_t idx = first + t;
+        const int64_t ns = idx / p.tokens, tok = idx - ns * p.tokens;
         const bool isq = hh < p.q.heads;
-        const RopeTensor &t = isq ? p.q : p.k;
+        const RopeTensor &x = isq ? p.q : p.k;
         const int head = isq ? hh : hh - p.q.heads;
-        const _Float16 *in = t.in + ns * t.in_stride[0] + tok * t.in_stride[1] + head * t.in_stride[2] + e0;
-        _Float16 *out = t.out + ns * t.out_stride[0] + tok * t.out_stride[1] + head * t.out_stride[2] + e0;
-        e16x8_t a = *reinterpret_cast<const e16x8_t *>(in);
-        if constexpr (HALVES) {
-            if (np) {
-                e16x8_t b = *reinterpret_cast<const e16x8_t *>(in + p.pairs);
-                e16x8_t oa, ob;
+        Item m;
+        m.turns = task < turning;
+        const int e0 = HALVES && !m.turns ? 2 * p.pairs + (task - turning) * 8 : task * 8;
+        m.in = x.in + ns * x.in_stride[0] + tok * x.in_stride[1] + head * x.in_stride[2] + e0;
+        m.out = x.out + ns * x.out_stride[0] + tok * x.out_stride[1] + head * x.out_stride[2] + e0;
+        const int p0 = task * (HALVES ? 8 : 4);
+        m.cs = turn + t * p.pairs + p0;
+        m.np = p.pairs - p0;
+        return m;
+    };
+    // The batch's loads go first: an output may be its input, so the compiler
+    // cannot move a load above an earlier store itself.
+    for (int base = threadIdx.x; base < items; base += kRopeThreads * kRopeBatch) {
+        Item m[kRopeBatch];
+        e16x8_t a[kRopeBatch], b[kRopeBatch];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float u = to_f32<E>(a[i]), v = to_f32<E>(b[i]);
-                    oa[i] = from_f32<E>(fmaf(u, cs[i], -v * sn[i]));
-                    ob[i] = from_f32<E>(fmaf(u, sn[i], v * cs[i]));
-                }
-                *reinterpret_cast<e16x8_t *>(out + p.pairs) = ob;
-                a = oa;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < np) {  // a pair that does not turn keeps its bits
-                    const float u = to_f32<E>(a[2 * i]), v = to_f32<E>(a[2 * i + 1]);
-                    a[2 * i] = from_f32<E>(fmaf(u, cs[i], -v * sn[i]));
-                    a[2 * i + 1] = from_f32<E>(fmaf(u, sn[i], v * cs[i]));
-                }
+        for (int k = 0; k < kRopeBatch; ++k) {
+            const int i = base + k * kRopeThreads;
+            if (i >= items) continue;
+            m[k] = item(i);
+            a[k] = *reinterpret_cast<const e16x8_t *>(m[k].in);
+            if (HALVES && m[k].turns) b[k] = *reinterpret_cast<const e16x8_t *>(m[k].in + p.pairs);
         }
-        *reinterpret_cast<e16x8_t *>(out) = a;
+#pragma unroll
+        for (int k = 0; k < kRopeBatch; ++k) {
+            if (base + k * kRopeThreads >= items) continue;
+            if (m[k].turns) {
+                if constexpr (HALVES) {
+                    e16x8_t oa, ob;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 c = m[k].cs[i];
+                        const float u = to_f32<E>(a[k][i]), v = to_f32<E>(b[k][i]);
+                        oa[i] = from_f32<E>(fmaf(u, c.x, -v * c.y));
+                        ob[i] = from_f32<E>(fmaf(u, c.y, v * c.x));
+                    }
+                    *reinterpret_cast<e16x8_t *>(m[k].out + p.pairs) = ob;
+                    a[k] = oa;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < m[k].np) {  // a pair that does not turn keeps its bits
+                            const float2 c = m[k].cs[i];
+                            const float u = to_f32<E>(a[k][2 * i]), v = to_f32<E>(a[k][2 * i + 1]);
+                            a[k][2 * i] = from_f32<E>(fmaf(u, c.x, -v * c.y));
+                            a[k][2 * i + 1] = from_f32<E>(fmaf(u, c.y, v * c.x));
+                        }
+                }
+            }
+            *reinterpret_cast<e16x8_t *>(m[k].out) = a[k];
+        }
     }
 }
 
@@ -113,13 +130,17 @@ __global__ __launch_bounds__(kRopeThreads) void rope3d_kernel(RopeParams p, int 
 
 hipError_t launch_rope3d(const RopeParams &p, hipStream_t s) {
     const int tasks = p.halves ? p.pairs / 8 + (p.head_dim - 2 * p.pairs) / 8 : p.head_dim / 8;
-    const int tpb = kRopeThreads / tasks;
-    const int64_t blocks = (p.tokens * p.n + tpb - 1) / tpb;
-    const int heads = p.q.heads + p.k.heads;
-    const int hpb = 8;
-    const dim3 grid((unsigned)blocks, (unsigned)((heads + hpb - 1) / hpb));
+    const int64_t total = p.tokens * p.n;
+    // one token per block where that leaves CUs idle otherwise, else enough
+    // tokens that a thread has a few batches
+    const int per_token = (p.q.heads + p.k.heads) * tasks;
+    int tpb = (4 * kRopeBatch * kRopeThreads + per_token - 1) / per_token;
+    if (tpb > kRopeMaxTokens) tpb = kRopeMaxTokens;
+    while (tpb > 1 && (total + tpb - 1) / tpb < 1024) --tpb;
+    const dim3 grid((unsigned)((total + tpb - 1) / tpb));
+    const size_t lds = (size_t)tpb * p.pairs * sizeof(float2);
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(kRopeThreads), 0, s, p, tasks, tpb, hpb);
+        hipLaunchKernelGGL(kernel, grid, dim3(kRopeThreads), lds, s, p, tasks, tpb);
         return hipGetLastError();
     };
     if (p.halves) return p.bf16 ? go(rope3d_kernel<__bf16, true>) : go(rope3d_kernel<_Float16, true>);

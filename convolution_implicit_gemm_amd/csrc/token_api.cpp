@@ -51,15 +51,23 @@ constexpr size_t kMaxPartial = (size_t)256 << 20;
 
 // Each CU runs whole waves of tiles; a last partial wave can be run as pieces
 // of the contraction instead, which costs writing and adding fp32 partials.
-GemmPlan plan_gemm(int64_t m, int n, int64_t k) {
+GemmPlan plan_gemm(int64_t m, int n, int64_t k, c3d::GemmLayout layout) {
     int count = 0;
     const c3d::GemmTile *tiles = c3d::gemm_tiles(&count);
     const char *force = getenv("CONV3D_LINEAR_TILE");
     GemmPlan best;
     double best_s = -1.0;
+    const bool rows_ok = layout == c3d::kGemmForward && m <= c3d::kGemmRowsMax;
+    if (rows_ok && (!force || strcmp(force, tiles[c3d::kGemmRowsTile].name) == 0)) {
+        best.tile = c3d::kGemmRowsTile;
+        best.m_tiles = 1;
+        best.n_tiles = best.dp = (n + 15) / 16;
+        return best;
+    }
     for (int pass = force ? 0 : 1; pass < 2 && best_s < 0.0; ++pass)
         for (int i = 0; i < count; ++i) {
             const c3d::GemmTile &t = tiles[i];
+            if (i == c3d::kGemmRowsTile) continue;
             if (pass == 0 && strcmp(force, t.name) != 0) continue;
             GemmPlan g;
             g.tile = i;
@@ -177,9 +185,9 @@ conv3d_status linear_plan(const linear_desc *d, linear_plan_t *out, size_t *work
     p->strips = c3d::act_grad_strips(d->m, d->n);
     p->off_col = p->off_part = p->back_bytes = 0;
     if (d->m > 0) {
-        p->fwd = plan_gemm(d->m, d->n, d->k);
-        p->dx = plan_gemm(d->m, d->k, d->n);
-        p->dw = plan_gemm(d->n, d->k, d->m);
+        p->fwd = plan_gemm(d->m, d->n, d->k, c3d::kGemmForward);
+        p->dx = plan_gemm(d->m, d->k, d->n, c3d::kGemmDx);
+        p->dw = plan_gemm(d->n, d->k, d->m, c3d::kGemmDw);
         const size_t dz = d->act != CONV3D_ACT_NONE ? align256((size_t)d->m * d->n * 2) : 0;
         const size_t part = p->dx.partial_bytes > p->dw.partial_bytes ? p->dx.partial_bytes : p->dw.partial_bytes;
         p->off_col = dz;

@@ -46,6 +46,8 @@ struct GemmTile {
     double rate;   // measured throughput per CU relative to the best tile
 };
 constexpr int kGemmMaxPieces = 32;
+// The kernel of few rows, an index into gemm_tiles: forward products of at most kGemmRowsMax rows.
+constexpr int kGemmRowsTile = 2, kGemmRowsMax = 16;
 const GemmTile *gemm_tiles(int *count);
 hipError_t launch_gemm(const GemmParams &p, int tile, GemmLayout layout, hipStream_t s);
 
