@@ -79,10 +79,17 @@ __device__ __forceinline__ void act_switch(int act, F &&f) {
 //   contraction contiguous (TR = false): ROWS rows of 128 bytes; 16-byte chunk
 //     c of row r sits at chunk c ^ swz<64>(r);
 //   transposed (TR = true): 64 rows (one per contraction index) of 2 ROWS
-//     bytes; chunk c of row r sits at chunk c ^ ((r & 3) << 2), so that the 4
-//     rows x 64 bytes that a half-wave's transposing reads take fill all banks.
+//     bytes; chunk c of row r sits at chunk c ^ tr_swz(r), so that the 4 rows x
+//     64 bytes that a half-wave's transposing reads take fill all banks.
 // Loads are 16 bytes per lane, 1 KiB per instruction, straight into LDS; the
 // swizzle is applied to the global side.
+
+// CH: 16-byte chunks of a row.  A row of 16 chunks spans all banks, one of 8
+// half of them; rows that repeat the same banks exchange their 64-byte pieces.
+template <int CH>
+__device__ __forceinline__ int tr_swz(int row) {
+    return CH >= 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
+}
 
 // One operand as a workgroup reads it: a moving buffer resource and the lane's
 // offsets for its NI load instructions per stage.
@@ -110,13 +117,13 @@ struct Operand {
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
                 const unsigned lin = (unsigned)((first + j * step) * 64 + lane);
-                const int r = (int)(lin / CH), c = (int)(lin % CH) ^ ((r & 3) << 2);
+                const int r = (int)(lin / CH), c = (int)(lin % CH) ^ tr_swz<(int)CH>(r);
                 voff[j] = c * 8 < ncols ? (uint32_t)(r * (int)stride + c * 8) * 2u : kOOB;
                 kc[j] = 0;
             }
         } else {
             base = m + (int64_t)row0 * stride + k0;
-            records = (uint32_t)((rows - 1) * (int)stride + left) * 2u;
+            records = (uint32_t)((rows - 1) * (int)stride + (left > 0 ? left : 0)) * 2u;
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
                 const int lin = (first + j * step) * 64 + lane;
@@ -126,8 +133,9 @@ struct Operand {
             }
         }
     }
-    // The current stage into `lds` (the operand's stage buffer), then on to the
-    // next; the contraction past its end reads as zeros.
+    // The current stage into `lds` (the operand's stage buffer), then on by STEP
+    // stages; the contraction past its end reads as zeros.
+    template <int STEP>
     __device__ __forceinline__ void load(char *lds, int first, int step) {
         if constexpr (TR) {
             // past the end: no record, so every offset is out of range
@@ -136,15 +144,15 @@ struct Operand {
             const buf_rsrc r = make_rsrc(base, (uint32_t)(rec < 0 || left <= 0 ? 0 : rec));
 #pragma unroll
             for (int j = 0; j < NI; ++j) dma16(r, lds + (first + j * step) * 1024, voff[j], 0u);
-            base += kGemmBK * stride;
+            base += STEP * kGemmBK * stride;
         } else {
             const buf_rsrc r = make_rsrc(base, records);
 #pragma unroll
             for (int j = 0; j < NI; ++j)
                 dma16(r, lds + (first + j * step) * 1024, kc[j] < left ? voff[j] : kOOB, soff);
-            soff += kGemmRow;
+            soff += STEP * kGemmRow;
         }
-        left -= kGemmBK;
+        left -= STEP * kGemmBK;
     }
 };
 
@@ -162,6 +170,15 @@ __device__ __forceinline__ void tr_read2(const uint32_t (&a)[2], uint64_t (&v)[8
                  : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]),
                    "=&v"(v[7])
                  : "v"(a[0]), "v"(a[1]), "n"(K0 * ROW), "n"((K0 + 4) * ROW), "n"((K0 + 16) * ROW), "n"((K0 + 20) * ROW)
+                 : "memory");
+#endif
+}
+template <int ROW, int K0>
+__device__ __forceinline__ void tr_read1(const uint32_t (&a)[1], uint64_t (&v)[4]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile(C3D_TR(0, 4, 5) C3D_TR(1, 4, 6) C3D_TR(2, 4, 7) C3D_TR(3, 4, 8) "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+                 : "v"(a[0]), "n"(K0 * ROW), "n"((K0 + 4) * ROW), "n"((K0 + 16) * ROW), "n"((K0 + 20) * ROW)
                  : "memory");
 #endif
 }
@@ -193,7 +210,7 @@ struct Fragments {
 #pragma unroll
             for (int i = 0; i < NF; ++i) {
                 const int chunk = ((row0 + i * 32 + 16 * g) >> 3) + ((j & 3) >> 1);
-                off[i] = r * ROWS * 2 + ((chunk ^ ((j >> 2) << 2)) << 4) + (j & 1) * 8;
+                off[i] = r * ROWS * 2 + ((chunk ^ tr_swz<ROWS / 8>(j >> 2)) << 4) + (j & 1) * 8;
             }
         } else {
             const int r = lane & 31, hi = lane >> 5;
@@ -205,13 +222,15 @@ struct Fragments {
     template <int KK0>
     __device__ __forceinline__ void read(const char *lds, half8_t (&f)[2][NF]) const {
         if constexpr (TR) {
-            static_assert(NF == 2 || NF == 4, "one assembly block per operand");
+            static_assert(NF == 1 || NF == 2 || NF == 4, "one assembly block per operand");
             const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)lds;
             uint32_t a[NF];
             uint64_t v[4 * NF];
 #pragma unroll
             for (int i = 0; i < NF; ++i) a[i] = base + off[i];
-            if constexpr (NF == 2)
+            if constexpr (NF == 1)
+                tr_read1<ROWS * 2, KK0 * 16>(a, v);
+            else if constexpr (NF == 2)
                 tr_read2<ROWS * 2, KK0 * 16>(a, v);
             else
                 tr_read4<ROWS * 2, KK0 * 16>(a, v);
@@ -386,7 +405,9 @@ __device__ __forceinline__ void gemm_store_partial(const GemmParams &p, const f3
 // Work unit u: a whole tile (slot < 0) or K-piece `slot` of a split tile, and
 // its range of stages.  Tiles are walked in groups of kGemmGroup rows of tiles,
 // down the rows first: the workgroups that an XCD runs at once (a contiguous
-// range of units) then share both operands' tiles in its L2.
+// range of units) then share both operands' tiles in its L2.  Pieces are walked
+// range of the contraction by range, so that an XCD reads its ranges of both
+// operands and not all of them.
 constexpr int kGemmGroup = 8;
 __device__ __forceinline__ void gemm_unit(const GemmParams &p, int u, int &m_tile, int &n_tile, int &it0, int &it1,
                                           int &slot) {
@@ -396,8 +417,8 @@ __device__ __forceinline__ void gemm_unit(const GemmParams &p, int u, int &m_til
     int tile = u;
     if (u >= p.dp_tiles) {
         slot = u - p.dp_tiles;
-        const int piece = slot % p.sk_pieces;
-        tile = p.dp_tiles + slot / p.sk_pieces;
+        const int piece = slot / p.sk_tiles;
+        tile = p.dp_tiles + slot % p.sk_tiles;
         it0 = (int)((int64_t)p.niter * piece / p.sk_pieces);
         it1 = (int)((int64_t)p.niter * (piece + 1) / p.sk_pieces);
     }

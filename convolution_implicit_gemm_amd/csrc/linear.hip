@@ -27,32 +27,38 @@ __device__ __forceinline__ void gemm_my_unit(const GemmParams &p, int &m_tile, i
     gemm_unit(p, u, m_tile, n_tile, it0, it1, slot);
 }
 
-// ---- ring kernel: 4 waves, a ring of NS stages, one barrier per stage.
-template <typename E, bool PT, bool QT, int BM, int BN, int WM, int WN, int NS>
-__global__ __launch_bounds__(256) void gemm_ring_kernel(GemmParams p) {
+// ---- ring kernel: KG groups of 4 waves, each with a ring of NS stages, one
+// barrier per stage.  The groups take the tile's stages in turn (a long
+// contraction over few tiles then needs no second launch to join its pieces);
+// their sums meet in LDS, in group order.
+template <typename E, bool PT, bool QT, int BM, int BN, int WM, int WN, int NS, int KG>
+__global__ __launch_bounds__(256 * KG) void gemm_ring_kernel(GemmParams p) {
     constexpr int TN = WN / 32, TM = WM / 32, WAVES = 4;
     constexpr int PB = BN * kGemmRow, QB = BM * kGemmRow, STAGE = PB + QB;
     constexpr int NP = PB / 1024 / WAVES, NQ = QB / 1024 / WAVES;
-    constexpr int LDS = NS * STAGE > BM * BN * 2 ? NS * STAGE : BM * BN * 2;
-    static_assert((BM / WM) * (BN / WN) == WAVES, "4 waves");
+    constexpr int LDS = KG * NS * STAGE;
+    static_assert((BM / WM) * (BN / WN) == WAVES, "4 waves per group");
+    static_assert(LDS >= BM * BN * 2 && LDS >= (KG - 1) * BM * BN * 4 && LDS <= 160 * 1024, "epilogue, sums, LDS");
     __shared__ __attribute__((aligned(1024))) char smem[LDS];
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
+    const int kg = KG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
     const int wmi = wave / (BN / WN), wni = wave % (BN / WN);
     int mt, nt, it0, it1, slot;
     gemm_my_unit(p, mt, nt, it0, it1, slot);
     const int m0 = mt * BM, n0 = nt * BN;
-    const int k0 = it0 * kGemmBK, kend = it1 * kGemmBK < p.K ? it1 * kGemmBK : p.K;
+    const int kend = it1 * kGemmBK < p.K ? it1 * kGemmBK : p.K;
+    char *ring = smem + kg * NS * STAGE;
 
     Operand<PT, BN, NP> op;
     Operand<QT, BM, NQ> oq;
-    op.init(p.p, p.p_stride, n0, p.N, k0, kend, wave, WAVES, lane);
-    oq.init(p.q, p.q_stride, m0, p.M, k0, kend, wave, WAVES, lane);
+    op.init(p.p, p.p_stride, n0, p.N, (it0 + kg) * kGemmBK, kend, wave, WAVES, lane);
+    oq.init(p.q, p.q_stride, m0, p.M, (it0 + kg) * kGemmBK, kend, wave, WAVES, lane);
     int wbuf = 0;
     auto fire = [&]() {
-        char *s = smem + wbuf * STAGE;
-        op.load(s, wave, WAVES);
-        oq.load(s + PB, wave, WAVES);
+        char *s = ring + wbuf * STAGE;
+        op.template load<KG>(s, wave, WAVES);
+        oq.template load<KG>(s + PB, wave, WAVES);
         wbuf = wbuf + 1 == NS ? 0 : wbuf + 1;
     };
     Fragments<PT, BN, TN> fp;
@@ -60,18 +66,18 @@ __global__ __launch_bounds__(256) void gemm_ring_kernel(GemmParams p) {
     fp.init(wni * WN, lane);
     fq.init(wmi * WM, lane);
 
-    f32x16 acc[TN][TM];
-    gemm_init_acc<E, WM, WN>(p, acc, slot < 0 && p.bias, n0 + wni * WN, lane);
     // stages past the end load zeros (their reads are out of range), so that
     // every wave's load count stays the same
+    f32x16 acc[TN][TM];
+    gemm_init_acc<E, WM, WN>(p, acc, slot < 0 && kg == 0 && p.bias, n0 + wni * WN, lane);
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s) fire();
     int rbuf = 0;
-    for (int it = it0; it < it1; ++it) {
+    for (int it = it0; it < it1; it += KG) {
         gemm_wait_loads<(NS - 2) * (NP + NQ)>();
         gemm_barrier();  // the stage has landed, and everyone is done with the one before it
         fire();
-        const char *s = smem + rbuf * STAGE;
+        const char *s = ring + rbuf * STAGE;
         static_for<2>([&](auto hc) {
             constexpr int KK0 = 2 * decltype(hc)::value;
             half8_t a[2][TN], bq[2][TM];
@@ -87,6 +93,40 @@ __global__ __launch_bounds__(256) void gemm_ring_kernel(GemmParams p) {
         rbuf = rbuf + 1 == NS ? 0 : rbuf + 1;
     }
     gemm_wait_loads<0>();
+    if constexpr (KG > 1) {
+        gemm_barrier();
+        constexpr int QUADS = BM * BN / 4;
+        f32x4 *sums = reinterpret_cast<f32x4 *>(smem);
+        auto at = [&](int g, int i, int j, int q) -> f32x4 & {
+            return sums[(g - 1) * QUADS + (((wave * TN + i) * TM + j) * 4 + q) * 64 + lane];
+        };
+        if (kg)
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        f32x4 v;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
+                        at(kg, i, j, q) = v;
+                    }
+        gemm_barrier();
+        if (kg) return;  // a wave that has ended counts as arrived at later barriers
+#pragma unroll
+        for (int g = 1; g < KG; ++g)
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 v = at(g, i, j, q);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+                    }
+    }
     if (slot >= 0) {
         gemm_store_partial<BM, BN, WM, WN>(p, acc, slot, wave, lane);
         return;
@@ -137,12 +177,12 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p) {
 
     // loads past the contraction's end read zeros, so that every wave's load
     // count stays the same
-    op.load(smem, wave, WAVES);
-    oq.load(smem + BUF, wave, WAVES);
-    op.load(smem + 2 * BUF, wave, WAVES);
+    op.template load<1>(smem, wave, WAVES);
+    oq.template load<1>(smem + BUF, wave, WAVES);
     f32x16 acc[TN][TM];
     gemm_init_acc<E, WM, WN>(p, acc, slot < 0 && p.bias, n0 + wni * WN, lane);
-    gemm_wait_loads<0>();
+    op.template load<1>(smem + 2 * BUF, wave, WAVES);
+    gemm_wait_loads<NP>();
     gemm_barrier();
     if (grp) gemm_barrier();  // group 1 runs one phase behind
     half8_t a[2][TN], bq[2][TM];
@@ -167,9 +207,9 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p) {
             constexpr int H = decltype(hc)::value;
             auto refill = [&]() {
                 if constexpr (H == 0)
-                    oq.load(ring(3), wave, WAVES);
+                    oq.template load<1>(ring(3), wave, WAVES);
                 else
-                    op.load(ring(4), wave, WAVES);
+                    op.template load<1>(ring(4), wave, WAVES);
             };
             if constexpr (PT || QT) refill();  // the transposing reads wait for themselves
             fq.template read<2 * H>(qs, bq);
@@ -288,11 +328,9 @@ __global__ __launch_bounds__(kRowsWaves * 64) void gemm_rows_kernel(GemmParams p
 template <typename E, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p) {
     constexpr int TN = WN / 32, TM = WM / 32, QUADS = BM * BN / 4;
-    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int st = (int)(idx / QUADS), qd = (int)(idx - (int64_t)st * QUADS);
-    if (st >= p.sk_tiles) return;
+    const int st = blockIdx.x / (QUADS / 256), qd = blockIdx.x % (QUADS / 256) * 256 + threadIdx.x;
     int mt, nt, it0, it1, slot;
-    gemm_unit(p, p.dp_tiles + st * p.sk_pieces, mt, nt, it0, it1, slot);
+    gemm_unit(p, p.dp_tiles + st, mt, nt, it0, it1, slot);
     const int lane = qd & 63;
     int r = qd >> 6;
     const int g = r & 3;
@@ -304,10 +342,11 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p) {
     const int m = mt * BM + wmi * WM + j * 32 + (lane & 31);
     const int n = nt * BN + wni * WN + i * 32 + 8 * g + 4 * (lane >> 5);
     if (m >= p.M || n >= p.N) return;
-    const f32x4 *pp = reinterpret_cast<const f32x4 *>(p.partial) + (size_t)st * p.sk_pieces * QUADS + qd;
+    const f32x4 *pp = reinterpret_cast<const f32x4 *>(p.partial) + (size_t)st * QUADS + qd;
+    const size_t piece = (size_t)p.sk_tiles * QUADS;
     f32x4 v = pp[0];
-#pragma unroll 4
-    for (int k = 1; k < p.sk_pieces; ++k) v += pp[(size_t)k * QUADS];
+#pragma unroll 8
+    for (int k = 1; k < p.sk_pieces; ++k) v += pp[k * piece];
     gemm_finish_quad<E>(p, v, m, n);
 }
 
@@ -354,27 +393,39 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradParams p, int grou
     }
 }
 
+// Times, in microseconds: of one step (a stage of 64 per group of waves) with
+// few workgroups on the card, for each layout; of one with per_cu workgroups on
+// every CU; and of what a workgroup adds before and after its steps.  Measured
+// over sizes from 200 x 704 x 704 to 8192^3.  (Four groups of waves look one
+// step ahead only: enough for operands in L2, not for the long streams of dw.)
 const GemmTile kTiles[] = {
-    {"m256n256k64", 256, 256, kGemmBK, 512, 1, 1.0},
-    {"m128n128k64", 128, 128, kGemmBK, 256, 2, 0.62},
-    {"m16n16k32", 16, 16, 32, kRowsWaves * 64, 4, 0.0},  // few rows; no share in the cost model
+    {"m256n256k64", 256, 256, kGemmBK, 512, 1, 1, {1.48, 1.48, 1.48}, 1.48, 5.5},
+    {"m128n128k64", 128, 128, kGemmBK, 256, 2, 1, {0.66, 0.7, 0.66}, 0.96, 2.5},
+    {"m64n64k64", 64, 64, kGemmBK, 256, 2, 1, {0.26, 0.3, 0.3}, 0.4, 2.0},
+    {"m64n64k64g4", 64, 64, kGemmBK, 1024, 1, 4, {0.42, 0.5, 1.3}, 0.88, 2.5},
+    {"m16n16k32", 16, 16, 32, kRowsWaves * 64, 4, 1, {0.0, 0.0, 0.0}, 0.0, 0.0},  // few rows; not in the cost model
 };
 
 template <typename E, bool PT, bool QT>
 hipError_t launch_tile(const GemmParams &p, int tile, hipStream_t s) {
-    const dim3 grid((unsigned)(p.dp_tiles + p.sk_tiles * p.sk_pieces));
-    if (tile == 0)
-        hipLaunchKernelGGL((gemm_pp_kernel<E, PT, QT, 256, 256>), grid, dim3(512), 0, s, p);
-    else
-        hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 128, 128, 64, 64, 2>), grid, dim3(256), 0, s, p);
+    const dim3 grid((unsigned)(p.dp_tiles + p.sk_tiles * p.sk_pieces)), block((unsigned)kTiles[tile].threads);
+    switch (tile) {
+        case 0: hipLaunchKernelGGL((gemm_pp_kernel<E, PT, QT, 256, 256>), grid, block, 0, s, p); break;
+        case 1:
+            hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 128, 128, 64, 64, 2, 1>), grid, block, 0, s, p);
+            break;
+        case 2: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 64, 64, 32, 32, 4, 1>), grid, block, 0, s, p); break;
+        default: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 64, 64, 32, 32, 2, 4>), grid, block, 0, s, p); break;
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.sk_tiles) return e;
     const GemmTile &t = kTiles[tile];
     const dim3 jb((unsigned)((int64_t)p.sk_tiles * (t.bm * t.bn / 4) / 256));
-    if (tile == 0)
-        hipLaunchKernelGGL((gemm_join_kernel<E, 256, 256, 64, 128>), jb, dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL((gemm_join_kernel<E, 128, 128, 64, 64>), jb, dim3(256), 0, s, p);
+    switch (tile) {
+        case 0: hipLaunchKernelGGL((gemm_join_kernel<E, 256, 256, 64, 128>), jb, dim3(256), 0, s, p); break;
+        case 1: hipLaunchKernelGGL((gemm_join_kernel<E, 128, 128, 64, 64>), jb, dim3(256), 0, s, p); break;
+        default: hipLaunchKernelGGL((gemm_join_kernel<E, 64, 64, 32, 32>), jb, dim3(256), 0, s, p); break;
+    }
     return hipGetLastError();
 }
 

@@ -25,22 +25,40 @@ constexpr int kRopeBatch = 4;       // tasks of a thread whose loads are in flig
 constexpr int kRopeMaxTokens = 16;  // tokens of a block
 
 // HALVES: the pair is (p, p + pairs) instead of (2p, 2p + 1).
+// a / b for 0 <= a < 2^22: the float quotient is off by at most one
+__device__ __forceinline__ int small_div(int a, int b, float rcp_b) {
+    int q = (int)((float)a * rcp_b);
+    const int r = a - q * b;
+    q += r >= b ? 1 : 0;
+    q -= r < 0 ? 1 : 0;
+    return q;
+}
+
 template <typename E, bool HALVES>
 __global__ __launch_bounds__(kRopeThreads) void rope3d_kernel(RopeParams p, int tasks, int tokens_per_block) {
     extern __shared__ float2 turn[];  // [token][pair] (cos, sin)
+    __shared__ int64_t place[kRopeMaxTokens][4];  // a token's offsets in q, q's output, k, k's output
     const int64_t first = (int64_t)blockIdx.x * tokens_per_block;  // flattened (sample, token)
     const int64_t left = p.tokens * p.n - first;
     const int ntok = left < tokens_per_block ? (int)left : tokens_per_block;
+    const int64_t ns0 = first / p.tokens, tok0 = first - ns0 * p.tokens;  // the first token's sample and index
 
+    if (threadIdx.x < ntok * 4) {
+        const int t = threadIdx.x >> 2, which = threadIdx.x & 3;
+        const int64_t over = tok0 + t, dn = over / p.tokens;
+        const RopeTensor &x = which < 2 ? p.q : p.k;
+        const int64_t *st = which & 1 ? x.out_stride : x.in_stride;
+        place[t][which] = (ns0 + dn) * st[0] + (over - dn * p.tokens) * st[1];
+    }
+    const float rcp_pairs = 1.0f / (float)p.pairs;
     for (int i = threadIdx.x; i < ntok * p.pairs; i += kRopeThreads) {
-        const int t = i / p.pairs, pr = i - t * p.pairs;
+        const int t = small_div(i, p.pairs, rcp_pairs), pr = i - t * p.pairs;
         const int axis = pr < p.end_t ? 0 : pr < p.end_h ? 1 : 2;
-        const int64_t idx = first + t;
         double pos;
         if (p.positions) {
-            pos = (double)p.positions[idx * 3 + axis];
+            pos = (double)p.positions[(first + t) * 3 + axis];
         } else {
-            const int64_t tok = idx % p.tokens;
+            const int64_t tok = (tok0 + t) % p.tokens;
             const int64_t hw = (int64_t)p.h * p.w;
             const int64_t frame = tok / hw;
             const int r = (int)(tok - frame * hw);
@@ -57,6 +75,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope3d_kernel(RopeParams p, int 
     const int heads = p.q.heads + p.k.heads;
     const int per_token = heads * tasks, items = ntok * per_token;
     const int turning = HALVES ? p.pairs / 8 : (p.pairs + 3) / 4;  // tasks that turn pairs
+    const float rcp_token = 1.0f / (float)per_token, rcp_tasks = 1.0f / (float)tasks;
     struct Item {
         const _Float16 *in;
         _Float16 *out;
@@ -65,18 +84,17 @@ __global__ __launch_bounds__(kRopeThreads) void rope3d_kernel(RopeParams p, int 
         int np;
     };
     auto item = [&](int i) {
-        const int t = i / per_token, r = i - t * per_token;
-        const int hh = r / tasks, task = r - hh * tasks;
-        const int64_t idx = first + t;
-        const int64_t ns = idx / p.tokens, tok = idx - ns * p.tokens;
+        const int t = small_div(i, per_token, rcp_token), r = i - t * per_token;
+        const int hh = small_div(r, tasks, rcp_tasks), task = r - hh * tasks;
         const bool isq = hh < p.q.heads;
-        const RopeTensor &x = isq ? p.q : p.k;
         const int head = isq ? hh : hh - p.q.heads;
         Item m;
         m.turns = task < turning;
         const int e0 = HALVES && !m.turns ? 2 * p.pairs + (task - turning) * 8 : task * 8;
-        m.in = x.in + ns * x.in_stride[0] + tok * x.in_stride[1] + head * x.in_stride[2] + e0;
-        m.out = x.out + ns * x.out_stride[0] + tok * x.out_stride[1] + head * x.out_stride[2] + e0;
+        m.in = (isq ? p.q.in : p.k.in) + place[t][isq ? 0 : 2] +
+               head * (isq ? p.q.in_stride[2] : p.k.in_stride[2]) + e0;
+        m.out = (isq ? p.q.out : p.k.out) + place[t][isq ? 1 : 3] +
+                head * (isq ? p.q.out_stride[2] : p.k.out_stride[2]) + e0;
         const int p0 = task * (HALVES ? 8 : 4);
         m.cs = turn + t * p.pairs + p0;
         m.np = p.pairs - p0;
@@ -136,6 +154,7 @@ hipError_t launch_rope3d(const RopeParams &p, hipStream_t s) {
     const int per_token = (p.q.heads + p.k.heads) * tasks;
     int tpb = (4 * kRopeBatch * kRopeThreads + per_token - 1) / per_token;
     if (tpb > kRopeMaxTokens) tpb = kRopeMaxTokens;
+    while (tpb > 1 && (int64_t)tpb * per_token >= 1 << 22) --tpb;  // small_div's range
     while (tpb > 1 && (total + tpb - 1) / tpb < 1024) --tpb;
     const dim3 grid((unsigned)((total + tpb - 1) / tpb));
     const size_t lds = (size_t)tpb * p.pairs * sizeof(float2);

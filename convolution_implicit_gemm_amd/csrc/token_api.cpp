@@ -44,13 +44,28 @@ struct GemmPlan {
     size_t partial_bytes = 0;
 };
 
-constexpr double kTileRate = 1300e12 / kCUs;  // flop/s of the best tile, per CU
-constexpr double kJoinBytesPerSec = 4.5e12;
-constexpr double kLaunchSeconds = 3e-6;
+constexpr double kJoinBytesPerUs = 4.5e6;
+constexpr double kJoinLaunchUs = 4.5;
 constexpr size_t kMaxPartial = (size_t)256 << 20;
 
-// Each CU runs whole waves of tiles; a last partial wave can be run as pieces
-// of the contraction instead, which costs writing and adding fp32 partials.
+// Time of `units` workgroups of `steps` steps each: rounds of as many as fit
+// the card.  The steps of a partial round run at the rate of the fullest CU and
+// at the card's share (L2 serves the operands of all of them).
+double rounds_us(const c3d::GemmTile &t, c3d::GemmLayout layout, int64_t units, double steps) {
+    const int64_t slots = (int64_t)kCUs * t.per_cu;
+    const int64_t full = units / slots, rem = units % slots;
+    double us = full * (steps * t.step_us_full + t.fixed_us);
+    if (rem) {
+        double step = rem > kCUs ? t.step_us_full : t.step_us_full * rem / slots;
+        if (step < t.step_us_few[layout]) step = t.step_us_few[layout];
+        us += steps * step + t.fixed_us;
+    }
+    return us;
+}
+
+// The kernel and decomposition with the least time by the measured rates.  A
+// last partial round of tiles can be run as pieces of the contraction instead,
+// which costs writing and adding fp32 partials in a second launch.
 GemmPlan plan_gemm(int64_t m, int n, int64_t k, c3d::GemmLayout layout) {
     int count = 0;
     const c3d::GemmTile *tiles = c3d::gemm_tiles(&count);
@@ -76,17 +91,16 @@ GemmPlan plan_gemm(int64_t m, int n, int64_t k, c3d::GemmLayout layout) {
             g.niter = (int)((k + t.bk - 1) / t.bk);
             const int64_t all = (int64_t)g.m_tiles * g.n_tiles;
             const int64_t slots = (int64_t)kCUs * t.per_cu;
-            const double iter_s = 2.0 * t.bm * t.bn * t.bk / (kTileRate * t.rate) * t.per_cu;
             g.dp = (int)all;
-            double sec = (double)((all + slots - 1) / slots) * g.niter * iter_s;
+            auto steps = [&](int pieces) { return (double)(((g.niter + pieces - 1) / pieces + t.groups - 1) / t.groups); };
+            double sec = rounds_us(t, layout, all, steps(1));
             const int64_t full = all / slots, rem = all % slots;
             GemmPlan pick = g;
             for (int pc = 2; rem && pc <= c3d::kGemmMaxPieces && pc * 4 <= g.niter; ++pc) {
                 const size_t bytes = (size_t)rem * pc * t.bm * t.bn * 4;
                 if (bytes > kMaxPartial) break;
-                const double s2 = ((double)full * g.niter +
-                                   (double)((rem * pc + slots - 1) / slots) * ((g.niter + pc - 1) / pc)) * iter_s +
-                                  2.0 * bytes / kJoinBytesPerSec + kLaunchSeconds;
+                const double s2 = rounds_us(t, layout, full * slots, steps(1)) + rounds_us(t, layout, rem * pc, steps(pc)) +
+                                  2.0 * bytes / kJoinBytesPerUs + kJoinLaunchUs;
                 if (s2 < sec * 0.97) {
                     sec = s2;
                     pick.dp = (int)(full * slots);
@@ -588,7 +602,7 @@ conv3d_status rope3d_plan(const rope3d_desc *d, rope3d_plan_t *out) {
                         2 * c3d::kRopeMaxPairs);
     if (d->pairing == ROPE3D_PAIR_HALVES && sum % 16)
         return api_fail(CONV3D_ERR_UNSUPPORTED, "ROPE3D_PAIR_HALVES needs dims that are a multiple of 16 together");
-    if (d->heads_q > 65536 || d->heads_k > 65536) return api_fail(CONV3D_ERR_UNSUPPORTED, "too many heads");
+    if (d->heads_q > 16384 || d->heads_k > 16384) return api_fail(CONV3D_ERR_UNSUPPORTED, "too many heads");
     double total = (double)d->n * d->t * d->h * d->w;
     if (total >= 2147483648.0 || (double)d->h * d->w >= 2147483648.0)
         return api_fail(CONV3D_ERR_UNSUPPORTED, "2^31 tokens or more");

@@ -37,17 +37,19 @@ struct GemmParams {
     float *partial;                // [sk_tiles * sk_pieces][tile_m * tile_n] fp32 (workspace)
 };
 
+
 enum GemmLayout { kGemmForward = 0, kGemmDx = 1, kGemmDw = 2 };  // (p, q): (k, k), (T, k), (T, T)
 
 struct GemmTile {
     const char *name;
     int bm, bn, bk, threads;
     int per_cu;    // workgroups that share a CU
-    double rate;   // measured throughput per CU relative to the best tile
+    int groups;    // groups of waves that take the stages in turn
+    double step_us_few[3], step_us_full, fixed_us;  // cost model (linear.hip)
 };
 constexpr int kGemmMaxPieces = 32;
 // The kernel of few rows, an index into gemm_tiles: forward products of at most kGemmRowsMax rows.
-constexpr int kGemmRowsTile = 2, kGemmRowsMax = 16;
+constexpr int kGemmRowsTile = 4, kGemmRowsMax = 16;
 const GemmTile *gemm_tiles(int *count);
 hipError_t launch_gemm(const GemmParams &p, int tile, GemmLayout layout, hipStream_t s);
 
