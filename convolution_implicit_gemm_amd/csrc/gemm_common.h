@@ -365,22 +365,105 @@ __device__ __forceinline__ void gemm_store_tile(const GemmParams &p, const f32x1
     store_rows<BM, BN, THREADS>(smem, p.y + (int64_t)m0 * p.y_stride + n0, p.y_stride, rows, cols);
 }
 
+// The bias of a lane's columns: element 4g + e of [i] is column col0 + 32 i + 8 g + 4 (lane / 32) + e.
+template <int TN>
+__device__ __forceinline__ void gemm_load_bias(const GemmParams &p, half4_t (&b)[TN][4], bool bias, int col0, int lane) {
+    const buf_rsrc rb = make_rsrc(bias ? p.bias : p.p, bias ? (uint32_t)p.N * 2u : 0u);
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int co = col0 + i * 32 + 8 * g + 4 * (lane >> 5);
+            b[i][g] = load8(rb, bias && co < p.N ? (uint32_t)co * 2u : kOOB);
+        }
+}
+
+// Epilogue of one wave's 64 x 128 part of a tile, through 8 KiB of LDS that no
+// other wave touches (no barrier), 64 columns at a time: rows of 128 bytes,
+// 16-byte chunk c of row v at chunk c ^ ((v >> 1) & 7), rows with bit 4 set
+// with the 8-byte halves of a chunk swapped, so that both the fragments' 8-byte
+// accesses (32 rows at one chunk) and the rows' 16-byte accesses spread over all
+// banks.  It leaves in whole cache lines.  row0, col0: the wave's first row and
+// column; rows, cols: how many of its 64 and 128 are inside the matrix (may be
+// none).
+template <typename E>
+__device__ __forceinline__ void gemm_store_wave(const GemmParams &p, const f32x16 (&acc)[4][2], char *lds, int row0,
+                                                int col0, int rows, int cols, int lane) {
+    if (rows <= 0 || cols <= 0) return;
+    const int rrow = lane & 31, rhi = lane >> 5;
+    const int vr = lane >> 3, vc = lane & 7;  // row accesses: 8 rows of 8 chunks per instruction
+    auto row_off = [&](int v, int c, int64_t stride, int h) {
+        return v < rows && h * 64 + c * 8 < cols ? (uint32_t)(v * (int)stride + h * 64 + c * 8) * 2u : kOOB;
+    };
+    auto fragments = [&](auto actc, auto resc, int h) {
+        constexpr int ACT = decltype(actc)::value;
+        constexpr bool RES = decltype(resc)::value;
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int v = j * 32 + rrow, c = ii * 4 + g;
+                    char *chunk = lds + v * 128 + ((c ^ ((v >> 1) & 7)) << 4);
+                    half4_t r = {}, o;
+                    if constexpr (RES) r = *reinterpret_cast<const half4_t *>(chunk + rhi * 8);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float z = h ? acc[2 + ii][j][4 * g + e] : acc[ii][j][4 * g + e];
+                        o[e] = from_f32<E>(RES ? act_f<ACT>(z) + to_f32<E>(r[e]) : act_f<ACT>(z));
+                    }
+                    *reinterpret_cast<half4_t *>(chunk + ((rhi ^ ((v >> 4) & 1)) << 3)) = o;
+                }
+    };
+    auto rows_out = [&](_Float16 *out, int64_t stride, int h) {
+        const buf_rsrc r = make_rsrc(out, (uint32_t)((rows - 1) * (int)stride + cols) * 2u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int v = 8 * k + vr;
+            half8_t t = *reinterpret_cast<const half8_t *>(lds + v * 128 + ((vc ^ ((v >> 1) & 7)) << 4));
+            if (k & 2) t = __builtin_shufflevector(t, t, 4, 5, 6, 7, 0, 1, 2, 3);  // v & 16
+            gemm_store16(r, row_off(v, vc, stride, h), t);
+        }
+    };
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (p.z) {
+            fragments(std::integral_constant<int, CONV3D_ACT_NONE>{}, std::false_type{}, h);
+            rows_out(p.z + (int64_t)row0 * p.N + col0, p.N, h);
+        }
+        if (p.res) {
+            const buf_rsrc r = make_rsrc(p.res + (int64_t)row0 * p.res_stride + col0,
+                                         (uint32_t)((rows - 1) * (int)p.res_stride + cols) * 2u);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the rows before have left the LDS
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int v = 8 * k + vr;
+                dma16(r, lds + k * 1024, row_off(v, vc ^ ((v >> 1) & 7), p.res_stride, h), 0u);
+            }
+            gemm_wait_loads<0>();
+            act_switch(p.act, [&](auto ac) { fragments(ac, std::true_type{}, h); });
+        } else {
+            act_switch(p.act, [&](auto ac) { fragments(ac, std::false_type{}, h); });
+        }
+        rows_out(p.y + (int64_t)row0 * p.y_stride + col0, p.y_stride, h);
+    }
+}
+
 // The bias of a lane's columns as the accumulators' start value.
 template <typename E, int WM, int WN>
 __device__ __forceinline__ void gemm_init_acc(const GemmParams &p, f32x16 (&acc)[WN / 32][WM / 32], bool bias, int col0,
                                               int lane) {
-    const buf_rsrc rb = make_rsrc(bias ? p.bias : p.p, bias ? (uint32_t)p.N * 2u : 0u);
+    half4_t b[WN / 32][4];
+    gemm_load_bias<WN / 32>(p, b, bias, col0, lane);
 #pragma unroll
     for (int i = 0; i < WN / 32; ++i)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int co = col0 + i * 32 + 8 * g + 4 * (lane >> 5);
-            const half4_t b = load8(rb, bias && co < p.N ? (uint32_t)co * 2u : kOOB);
+        for (int g = 0; g < 4; ++g)
 #pragma unroll
             for (int j = 0; j < WM / 32; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][4 * g + e] = to_f32<E>(b[e]);
-        }
+                for (int e = 0; e < 4; ++e) acc[i][j][4 * g + e] = to_f32<E>(b[i][g][e]);
 }
 
 // A K-piece's fp32 partial tile, in fragment order.

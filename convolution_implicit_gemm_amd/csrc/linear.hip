@@ -17,11 +17,10 @@ namespace c3d {
 
 namespace {
 
-// A workgroup's work unit.  Workgroups are dealt to the XCDs in turn; the whole
-// tiles and the pieces are each dealt out in contiguous ranges per XCD.
-__device__ __forceinline__ void gemm_my_unit(const GemmParams &p, int &m_tile, int &n_tile, int &it0, int &it1,
+// Work unit number b of the launch.  Workgroups are dealt to the XCDs in turn;
+// the whole tiles and the pieces are each dealt out in contiguous ranges per XCD.
+__device__ __forceinline__ void gemm_my_unit(const GemmParams &p, int b, int &m_tile, int &n_tile, int &it0, int &it1,
                                              int &slot) {
-    const int b = blockIdx.x;
     const int u = b < p.dp_tiles ? xcd_range(b, p.dp_tiles)
                                  : p.dp_tiles + xcd_range(b - p.dp_tiles, p.sk_tiles * p.sk_pieces);
     gemm_unit(p, u, m_tile, n_tile, it0, it1, slot);
@@ -45,7 +44,7 @@ __global__ __launch_bounds__(256 * KG) void gemm_ring_kernel(GemmParams p) {
     const int kg = KG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
     const int wmi = wave / (BN / WN), wni = wave % (BN / WN);
     int mt, nt, it0, it1, slot;
-    gemm_my_unit(p, mt, nt, it0, it1, slot);
+    gemm_my_unit(p, blockIdx.x, mt, nt, it0, it1, slot);
     const int m0 = mt * BM, n0 = nt * BN;
     const int kend = it1 * kGemmBK < p.K ? it1 * kGemmBK : p.K;
     char *ring = smem + kg * NS * STAGE;
@@ -150,91 +149,182 @@ __global__ __launch_bounds__(256 * KG) void gemm_ring_kernel(GemmParams p) {
 // memory phase and p(s + 2) from the second, so that a load has at least two
 // and a half phases (p: six) to land.  All but p(s + 2) have to have landed
 // before phase 4s + 4: both groups wait for their own in phase 4s + 3.
-template <typename E, bool PT, bool QT, int BM, int BN>
-__global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p) {
-    constexpr int WM = BM / 4, WN = BN / 2, TN = WN / 32, TM = WM / 32, WAVES = 8;
-    static_assert(BM == BN, "the ring's buffers hold either operand");
+//
+// A workgroup runs work units until none is left (one workgroup per CU), and
+// the ring runs on across them: the last stages of a unit load the first of the
+// next.  At its end the two buffers of the last stage are free and serve the
+// epilogue, 8 KiB per wave, so that its stores drain under the next unit's
+// stages.  (One workgroup per unit took 5.5 us per unit besides its stages, a
+// tenth of the time at a contraction of 2048.)
+template <typename E, bool PT, bool QT>
+__global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p0) {
+    constexpr int BM = 256, BN = 256, WM = BM / 4, WN = BN / 2, TN = WN / 32, TM = WM / 32, WAVES = 8;
     constexpr int BUF = BN * kGemmRow, NP = BUF / 1024 / WAVES, NQ = NP;
-    constexpr int LDS = 5 * BUF > BM * BN * 2 ? 5 * BUF : BM * BN * 2;
-    static_assert(LDS <= 160 * 1024, "LDS is 160 KiB per CU");
-    __shared__ __attribute__((aligned(1024))) char smem[LDS];
+    __shared__ __attribute__((aligned(1024))) char smem[5 * BUF];
+    static_assert(sizeof(smem) <= 160 * 1024, "LDS is 160 KiB per CU");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int grp = wave >> 2, wmi = wave & 3, wni = grp;
-    int mt, nt, it0, it1, slot;
-    gemm_my_unit(p, mt, nt, it0, it1, slot);
-    const int m0 = mt * BM, n0 = nt * BN;
-    const int k0 = it0 * kGemmBK, kend = it1 * kGemmBK < p.K ? it1 * kGemmBK : p.K;
+    // The lane and the parameters as the compiler cannot see through them: what
+    // the once-per-unit code needs is worked out and read again there instead of
+    // being kept in registers (and spilled) across the loop over stages.
+    auto opaque_lane = [&]() {
+        int l = lane;
+#if defined(__HIP_DEVICE_COMPILE__)
+        asm volatile("" : "+v"(l));
+#endif
+        return l;
+    };
+#if defined(__HIP_DEVICE_COMPILE__)
+    const uint64_t kaddr = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+#endif
+    auto params = [&]() -> GemmParams {
+#if defined(__HIP_DEVICE_COMPILE__)
+        uint64_t ka = kaddr;
+        asm volatile("" : "+s"(ka));
+        return *reinterpret_cast<const GemmParams __attribute__((address_space(4))) *>(ka);
+#else
+        return p0;
+#endif
+    };
+    struct Unit {
+        int mt, nt, it0, it1, slot;
+    };
+    auto unit_of = [&](const GemmParams &p, int u) {
+        Unit r;
+        gemm_my_unit(p, u, r.mt, r.nt, r.it0, r.it1, r.slot);
+        return r;
+    };
 
     Operand<PT, BN, NP> op;
     Operand<QT, BM, NQ> oq;
-    op.init(p.p, p.p_stride, n0, p.N, k0, kend, wave, WAVES, lane);
-    oq.init(p.q, p.q_stride, m0, p.M, k0, kend, wave, WAVES, lane);
+    auto aim_p = [&](const GemmParams &p, const Unit &u) {
+        const int kend = u.it1 * kGemmBK < p.K ? u.it1 * kGemmBK : p.K;
+        op.init(p.p, p.p_stride, u.nt * BN, p.N, u.it0 * kGemmBK, kend, wave, WAVES, opaque_lane());
+    };
+    auto aim_q = [&](const GemmParams &p, const Unit &u) {
+        const int kend = u.it1 * kGemmBK < p.K ? u.it1 * kGemmBK : p.K;
+        oq.init(p.q, p.q_stride, u.mt * BM, p.M, u.it0 * kGemmBK, kend, wave, WAVES, opaque_lane());
+    };
     Fragments<PT, BN, TN> fp;
     Fragments<QT, BM, TM> fq;
     fp.init(wni * WN, lane);
     fq.init(wmi * WM, lane);
 
-    // loads past the contraction's end read zeros, so that every wave's load
-    // count stays the same
+    int u = blockIdx.x;
+    Unit cur, next;
+    {
+        const GemmParams p = params();
+        cur = unit_of(p, u);
+        aim_p(p, cur);
+        aim_q(p, cur);
+    }
     op.template load<1>(smem, wave, WAVES);
     oq.template load<1>(smem + BUF, wave, WAVES);
-    f32x16 acc[TN][TM];
-    gemm_init_acc<E, WM, WN>(p, acc, slot < 0 && p.bias, n0 + wni * WN, lane);
     op.template load<1>(smem + 2 * BUF, wave, WAVES);
     gemm_wait_loads<NP>();
     gemm_barrier();
-    if (grp) gemm_barrier();  // group 1 runs one phase behind
-    half8_t a[2][TN], bq[2][TM];
-    auto compute = [&]() {
-        __builtin_amdgcn_s_setprio(2);
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int i = 0; i < TN; ++i)
-#pragma unroll
-                for (int j = 0; j < TM; ++j) acc[i][j] = mfma_32x32x16<E>(a[kk][i], bq[kk][j], acc[i][j]);
-        __builtin_amdgcn_s_setprio(0);
-    };
     int pbuf = 0;  // p(s); q(s) and the refills follow it in the ring
     auto ring = [&](int d) {
         const int i = pbuf + d;
         return smem + (i >= 5 ? i - 5 : i) * BUF;
     };
-    for (int it = it0; it < it1; ++it) {
-        const char *ps = ring(0), *qs = ring(1);
-        auto memory = [&](auto hc) {
-            constexpr int H = decltype(hc)::value;
-            auto refill = [&]() {
-                if constexpr (H == 0)
-                    oq.template load<1>(ring(3), wave, WAVES);
-                else
-                    op.template load<1>(ring(4), wave, WAVES);
-            };
-            if constexpr (PT || QT) refill();  // the transposing reads wait for themselves
-            fq.template read<2 * H>(qs, bq);
-            fp.template read<2 * H>(ps, a);
-            if constexpr (!PT && !QT) refill();
+    for (;;) {
+        f32x16 acc[TN][TM] = {};
+        half4_t bias[TN][4];
+        half8_t a[2][TN], bq[2][TM];
+        auto compute = [&]() {
+            __builtin_amdgcn_s_setprio(2);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int i = 0; i < TN; ++i)
+#pragma unroll
+                    for (int j = 0; j < TM; ++j) acc[i][j] = mfma_32x32x16<E>(a[kk][i], bq[kk][j], acc[i][j]);
+            __builtin_amdgcn_s_setprio(0);
         };
-        memory(std::integral_constant<int, 0>{});
-        gemm_barrier();
-        compute();
-        gemm_barrier();
-        memory(std::integral_constant<int, 1>{});
-        if (grp) gemm_wait_loads<NP>();
-        gemm_barrier();
-        compute();
-        if (!grp) gemm_wait_loads<NP>();
-        if (!(grp && it + 1 == it1)) gemm_barrier();  // group 1's last would pair with nothing
+        auto stage = [&](auto lastc) {
+            constexpr bool LAST = decltype(lastc)::value;
+            const char *ps = ring(0), *qs = ring(1);
+            auto memory = [&](auto hc) {
+                constexpr int H = decltype(hc)::value;
+                auto refill = [&]() {
+                    if constexpr (H == 0)
+                        oq.template load<1>(ring(3), wave, WAVES);
+                    else
+                        op.template load<1>(ring(4), wave, WAVES);
+                };
+                // the bias goes ahead of the stage's loads, so that the wait
+                // for those covers it
+                if constexpr (LAST && H == 0) {
+                    const GemmParams p = params();
+                    gemm_load_bias<TN>(p, bias, cur.slot < 0 && p.bias, cur.nt * BN + wni * WN, opaque_lane());
+                }
+                if constexpr (PT || QT) refill();  // the transposing reads wait for themselves
+                fq.template read<2 * H>(qs, bq);
+                fp.template read<2 * H>(ps, a);
+                if constexpr (!PT && !QT) refill();
+            };
+            memory(std::integral_constant<int, 0>{});
+            gemm_barrier();
+            compute();
+            gemm_barrier();
+            memory(std::integral_constant<int, 1>{});
+            if (grp) gemm_wait_loads<NP>();
+            gemm_barrier();
+            compute();
+            if (!grp) gemm_wait_loads<NP>();
+            if (!(LAST && grp)) gemm_barrier();  // group 1's last would pair with nothing
+            if constexpr (!LAST) pbuf = pbuf + 2 >= 5 ? pbuf - 3 : pbuf + 2;
+        };
+        if (grp) gemm_barrier();  // group 1 runs one phase behind
+        for (int it = cur.it0; it + 2 < cur.it1; ++it) stage(std::false_type{});
+        // two stages are left (there are at least two): p is loaded to its end
+        // and goes on to the next unit, then q; without one, both load zeros, so
+        // that every wave's load count stays the same
+        u += gridDim.x;
+        bool more;
+        {
+            const GemmParams p = params();
+            more = u < p.dp_tiles + p.sk_tiles * p.sk_pieces;
+            if (more) {
+                next = unit_of(p, u);
+                aim_p(p, next);
+            } else {
+                op.left = 0;
+            }
+        }
+        stage(std::false_type{});
+        if (more)
+            aim_q(params(), next);
+        else
+            oq.left = 0;
+        stage(std::true_type{});
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] += to_f32<E>(bias[i][e >> 2][e & 3]);
+        __builtin_amdgcn_sched_barrier(0);
+        // every wave is past its reads of the last stage (group 0 passed the
+        // barrier after them, group 1 made them)
+        {
+            const GemmParams p = params();
+            const int m0 = cur.mt * BM + wmi * WM, n0 = cur.nt * BN + wni * WN;  // this wave's part
+            if (cur.slot >= 0)
+                gemm_store_partial<BM, BN, WM, WN>(p, acc, cur.slot, wmi * 2 + wni, opaque_lane());
+            else
+                gemm_store_wave<E>(p, acc, ring(grp) + wmi * 8192, m0, n0, p.M - m0 < WM ? p.M - m0 : WM,
+                                   p.N - n0 < WN ? p.N - n0 : WN, opaque_lane());
+        }
+        if (!more) break;
         pbuf = pbuf + 2 >= 5 ? pbuf - 3 : pbuf + 2;
+        cur = next;
+        gemm_barrier();  // the epilogue's buffers are free again
     }
     gemm_wait_loads<0>();
-    if (slot >= 0) {
-        gemm_store_partial<BM, BN, WM, WN>(p, acc, slot, wmi * 2 + wni, lane);
-        return;
-    }
-    gemm_barrier();
-    gemm_store_tile<E, BM, BN, WM, WN, 512>(p, acc, smem, m0, n0, wmi, wni, lane);
 }
 
 // ---- few rows (m <= 16): the product is the stream of w from HBM.  A block
@@ -410,7 +500,13 @@ template <typename E, bool PT, bool QT>
 hipError_t launch_tile(const GemmParams &p, int tile, hipStream_t s) {
     const dim3 grid((unsigned)(p.dp_tiles + p.sk_tiles * p.sk_pieces)), block((unsigned)kTiles[tile].threads);
     switch (tile) {
-        case 0: hipLaunchKernelGGL((gemm_pp_kernel<E, PT, QT, 256, 256>), grid, block, 0, s, p); break;
+        case 0: {
+            GemmParams q = p;
+            if (q.niter < 2) q.niter = 2;  // a stage past the contraction's end is one of zeros
+            const dim3 cus(grid.x < (unsigned)kGemmCUs ? grid.x : (unsigned)kGemmCUs);
+            hipLaunchKernelGGL((gemm_pp_kernel<E, PT, QT>), cus, block, 0, s, q);
+            break;
+        }
         case 1:
             hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 128, 128, 64, 64, 2, 1>), grid, block, 0, s, p);
             break;

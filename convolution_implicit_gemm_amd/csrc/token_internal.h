@@ -47,6 +47,7 @@ struct GemmTile {
     int groups;    // groups of waves that take the stages in turn
     double step_us_few[3], step_us_full, fixed_us;  // cost model (linear.hip)
 };
+constexpr int kGemmCUs = 256;
 constexpr int kGemmMaxPieces = 32;
 // The kernel of few rows, an index into gemm_tiles: forward products of at most kGemmRowsMax rows.
 constexpr int kGemmRowsTile = 4, kGemmRowsMax = 16;
