@@ -39,7 +39,11 @@ __device__ __forceinline__ float act_f(float z) {
         float ex;
         return z * normal_cdf(z, ex);
     }
-    if constexpr (ACT == CONV3D_ACT_GELU_TANH) return z * sigmoid_f(2.0f * kGeluA * fmaf(kGeluB * z, z * z, z));
+    if constexpr (ACT == CONV3D_ACT_GELU_TANH) {
+        // z / (1 + 2^(z (k + kB z^2))), k = -2 log2(e) sqrt(2 / pi)
+        constexpr float k = -2.0f * kLog2e * kGeluA;
+        return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * fmaf(k * kGeluB, z * z, k)));
+    }
     return z;
 }
 // act'(z).  The arguments whose powers could overflow are bounded where the
@@ -491,7 +495,7 @@ __device__ __forceinline__ void gemm_store_partial(const GemmParams &p, const f3
 // range of units) then share both operands' tiles in its L2.  Pieces are walked
 // range of the contraction by range, so that an XCD reads its ranges of both
 // operands and not all of them.
-constexpr int kGemmGroup = 8;
+constexpr int kGemmGroup = 4;
 __device__ __forceinline__ void gemm_unit(const GemmParams &p, int u, int &m_tile, int &n_tile, int &it0, int &it1,
                                           int &slot) {
     it0 = 0;

@@ -44,7 +44,7 @@ struct GemmPlan {
     size_t partial_bytes = 0;
 };
 
-constexpr double kJoinBytesPerUs = 4.5e6;
+constexpr double kJoinBytesPerUs = 9e6;
 constexpr double kJoinLaunchUs = 4.5;
 constexpr size_t kMaxPartial = (size_t)256 << 20;
 
