@@ -15,8 +15,7 @@
 // columns' sums in registers, the block adds its teams through LDS and writes
 // one fp32 partial, and a second kernel adds the blocks in a fixed order (no
 // atomics: the result does not depend on the order blocks finish in).
-#include "elem16.h"
-#include "token_internal.h"
+#include "column_sum.h"
 
 namespace c3d {
 
@@ -223,40 +222,10 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGra
     }
 }
 
-// Column sums of fp32 partials [rows][cols] (cols a multiple of 8): a block
-// takes 16 columns, 64 threads per 4 columns add every 64th row, then the 64
-// sums in order.
 template <typename E>
-__global__ __launch_bounds__(256) void column_sum_kernel(const float *part, int rows, int cols, _Float16 *out0,
-                                                         _Float16 *out1, int split) {
-    __shared__ float s[64][17];
-    const int tc = threadIdx.x & 3, tr = threadIdx.x >> 2;
-    const int c = blockIdx.x * 16 + tc * 4;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (c < cols) {
-#pragma unroll 8
-        for (int r = tr; r < rows; r += 64) {
-            const float4 u = *reinterpret_cast<const float4 *>(part + (int64_t)r * cols + c);
-            v.x += u.x;
-            v.y += u.y;
-            v.z += u.z;
-            v.w += u.w;
-        }
-    }
-    s[tr][tc * 4 + 0] = v.x;
-    s[tr][tc * 4 + 1] = v.y;
-    s[tr][tc * 4 + 2] = v.z;
-    s[tr][tc * 4 + 3] = v.w;
-    __syncthreads();
-    const int col = threadIdx.x >> 4, q = threadIdx.x & 15;  // 16 threads per column, 4 sums each
-    float t = s[q * 4][col] + s[q * 4 + 1][col] + s[q * 4 + 2][col] + s[q * 4 + 3][col];
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) t += __shfl_xor(t, off);
-    const int oc = blockIdx.x * 16 + col;
-    if (q == 0 && oc < cols) {
-        _Float16 *o = oc < split ? out0 : out1;
-        if (o) o[oc < split ? oc : oc - split] = from_f32<E>(t);
-    }
+__global__ __launch_bounds__(256) void column_sum_kernel(ColumnSumParams p) {
+    __shared__ float lds[column_sum_lds(256)];
+    column_sum_block<E, 256>(p, blockIdx.x, lds);
 }
 
 __global__ __launch_bounds__(256) void zero_rows_kernel(_Float16 *y, int64_t rows, int width, int64_t stride) {
@@ -312,17 +281,16 @@ hipError_t launch_layernorm_grad(const LnGradParams &p, hipStream_t s) {
         return hipGetLastError();
     });
     if (e != hipSuccess || !p.part) return e;
-    return launch_column_sum(p.part, (int32_t)grid, 2 * p.c, p.dgamma, p.dbeta, 2, p.bf16, s);
+    const ColumnSumParams cs = {p.part, p.dgamma, p.dbeta, (int32_t)grid, 2 * p.c, p.c, p.bf16};
+    return launch_column_sum(cs, s);
 }
 
-hipError_t launch_column_sum(const float *part, int32_t rows, int32_t cols, _Float16 *out0, _Float16 *out1,
-                             int32_t parts, int32_t bf16, hipStream_t s) {
-    const int split = cols / parts;
-    const dim3 grid((unsigned)((cols + 15) / 16));
-    if (bf16)
-        hipLaunchKernelGGL((column_sum_kernel<__bf16>), grid, dim3(256), 0, s, part, rows, cols, out0, out1, split);
+hipError_t launch_column_sum(const ColumnSumParams &p, hipStream_t s) {
+    const dim3 grid((unsigned)((p.cols + 15) / 16));
+    if (p.bf16)
+        hipLaunchKernelGGL((column_sum_kernel<__bf16>), grid, dim3(256), 0, s, p);
     else
-        hipLaunchKernelGGL((column_sum_kernel<_Float16>), grid, dim3(256), 0, s, part, rows, cols, out0, out1, split);
+        hipLaunchKernelGGL((column_sum_kernel<_Float16>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 

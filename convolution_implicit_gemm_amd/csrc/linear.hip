@@ -11,6 +11,7 @@
 //
 // The MFMA's A operand is the output's columns, so a lane's accumulators hold 4
 // adjacent columns of one row.  Sums are fp32; y and z are rounded once.
+#include "column_sum.h"
 #include "gemm_common.h"
 
 namespace c3d {
@@ -30,21 +31,30 @@ __device__ __forceinline__ void gemm_my_unit(const GemmParams &p, int b, int &m_
 // barrier per stage.  The groups take the tile's stages in turn (a long
 // contraction over few tiles then needs no second launch to join its pieces);
 // their sums meet in LDS, in group order.
-template <typename E, bool PT, bool QT, int BM, int BN, int WM, int WN, int NS, int KG>
-__global__ __launch_bounds__(256 * KG) void gemm_ring_kernel(GemmParams p) {
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int KG_>
+struct RingTile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, KG = KG_;
+    static constexpr int THREADS = 256 * KG, STAGE = (BM + BN) * kGemmRow, LDS = KG * NS * STAGE;
+    static_assert((BM / WM) * (BN / WN) == 4, "4 waves per group");
+    static_assert(LDS >= BM * BN * 2 && LDS >= (KG - 1) * BM * BN * 4 && LDS <= 160 * 1024, "epilogue, sums, LDS");
+};
+using Ring128 = RingTile<128, 128, 64, 64, 2, 1>;
+using Ring64 = RingTile<64, 64, 32, 32, 4, 1>;
+using Ring64G4 = RingTile<64, 64, 32, 32, 2, 4>;
+
+// Work unit b of one product.
+template <typename E, bool PT, bool QT, typename T>
+__device__ __forceinline__ void gemm_ring_unit(const GemmParams &p, int b, char *smem) {
+    constexpr int BM = T::BM, BN = T::BN, WM = T::WM, WN = T::WN, NS = T::NS, KG = T::KG;
     constexpr int TN = WN / 32, TM = WM / 32, WAVES = 4;
     constexpr int PB = BN * kGemmRow, QB = BM * kGemmRow, STAGE = PB + QB;
     constexpr int NP = PB / 1024 / WAVES, NQ = QB / 1024 / WAVES;
-    constexpr int LDS = KG * NS * STAGE;
-    static_assert((BM / WM) * (BN / WN) == WAVES, "4 waves per group");
-    static_assert(LDS >= BM * BN * 2 && LDS >= (KG - 1) * BM * BN * 4 && LDS <= 160 * 1024, "epilogue, sums, LDS");
-    __shared__ __attribute__((aligned(1024))) char smem[LDS];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
     const int kg = KG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
     const int wmi = wave / (BN / WN), wni = wave % (BN / WN);
     int mt, nt, it0, it1, slot;
-    gemm_my_unit(p, blockIdx.x, mt, nt, it0, it1, slot);
+    gemm_my_unit(p, b, mt, nt, it0, it1, slot);
     const int m0 = mt * BM, n0 = nt * BN;
     const int kend = it1 * kGemmBK < p.K ? it1 * kGemmBK : p.K;
     char *ring = smem + kg * NS * STAGE;
@@ -132,6 +142,29 @@ __global__ __launch_bounds__(256 * KG) void gemm_ring_kernel(GemmParams p) {
     }
     gemm_barrier();
     gemm_store_tile<E, BM, BN, WM, WN, 256>(p, acc, smem, m0, n0, wmi, wni, lane);
+}
+
+template <typename E, bool PT, bool QT, typename T>
+__global__ __launch_bounds__(T::THREADS) void gemm_ring_kernel(GemmParams p) {
+    __shared__ __attribute__((aligned(1024))) char smem[T::LDS];
+    gemm_ring_unit<E, PT, QT, T>(p, blockIdx.x, smem);
+}
+
+// Both gradients' products and the columns' sums behind dbias in one launch:
+// blocks [0, x_units) dx, [x_units, x_units + w_units) dw, then the sums.  Where
+// neither product fills the card they share it, and a small backward pass is
+// three launches.
+template <typename E, typename T>
+__global__ __launch_bounds__(T::THREADS) void gemm_pair_kernel(GemmParams px, GemmParams pw, ColumnSumParams cs,
+                                                               int x_units, int w_units) {
+    __shared__ __attribute__((aligned(1024))) char smem[T::LDS];
+    const int b = blockIdx.x;
+    if (b < x_units)
+        gemm_ring_unit<E, true, false, T>(px, b, smem);
+    else if (b < x_units + w_units)
+        gemm_ring_unit<E, true, true, T>(pw, b - x_units, smem);
+    else
+        column_sum_block<E, T::THREADS>(cs, b - x_units - w_units, reinterpret_cast<float *>(smem));
 }
 
 // ---- ping-pong kernel: 8 waves in two groups of 4, one wave of each on every
@@ -416,9 +449,9 @@ __global__ __launch_bounds__(kRowsWaves * 64) void gemm_rows_kernel(GemmParams p
 // ---- the pieces of the split tiles, added in order, then the epilogue.  One
 // thread per 4 adjacent columns; blocks of the tile's fragment order.
 template <typename E, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p) {
+__device__ __forceinline__ void gemm_join_block(const GemmParams &p, int b) {
     constexpr int TN = WN / 32, TM = WM / 32, QUADS = BM * BN / 4;
-    const int st = blockIdx.x / (QUADS / 256), qd = blockIdx.x % (QUADS / 256) * 256 + threadIdx.x;
+    const int st = b / (QUADS / 256), qd = b % (QUADS / 256) * 256 + threadIdx.x;
     int mt, nt, it0, it1, slot;
     gemm_unit(p, p.dp_tiles + st, mt, nt, it0, it1, slot);
     const int lane = qd & 63;
@@ -438,6 +471,16 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p) {
 #pragma unroll 8
     for (int k = 1; k < p.sk_pieces; ++k) v += pp[k * piece];
     gemm_finish_quad<E>(p, v, m, n);
+}
+
+// Blocks [0, x_blocks) join the first product's tiles, the others the second's.
+template <typename E, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p, GemmParams p2, int x_blocks) {
+    const int b = blockIdx.x;
+    if (b < x_blocks)
+        gemm_join_block<E, BM, BN, WM, WN>(p, b);
+    else
+        gemm_join_block<E, BM, BN, WM, WN>(p2, b - x_blocks);
 }
 
 // ---- dz = dy act'(z) and its column sums.  A block walks a strip of rows for
@@ -492,13 +535,34 @@ const GemmTile kTiles[] = {
     {"m256n256k64", 256, 256, kGemmBK, 512, 1, 1, {1.48, 1.48, 1.48}, 1.48, 5.5},
     {"m128n128k64", 128, 128, kGemmBK, 256, 2, 1, {0.66, 0.7, 0.66}, 0.96, 2.5},
     {"m64n64k64", 64, 64, kGemmBK, 256, 2, 1, {0.26, 0.3, 0.3}, 0.4, 2.0},
-    {"m64n64k64g4", 64, 64, kGemmBK, 1024, 1, 4, {0.42, 0.5, 1.3}, 0.88, 2.5},
+    {"m64n64k64g4", 64, 64, kGemmBK, 1024, 1, 4, {0.42, 0.9, 1.3}, 0.88, 2.5},
     {"m16n16k32", 16, 16, 32, kRowsWaves * 64, 4, 1, {0.0, 0.0, 0.0}, 0.0, 0.0},  // few rows; not in the cost model
 };
 
+unsigned units_of(const GemmParams &p) { return (unsigned)(p.dp_tiles + p.sk_tiles * p.sk_pieces); }
+
+unsigned join_blocks(const GemmParams &p, int tile) {
+    return (unsigned)((int64_t)p.sk_tiles * (kTiles[tile].bm * kTiles[tile].bn / 4) / 256);
+}
+
+// The split tiles of p (and of p2, or null).
+template <typename E>
+hipError_t launch_join(const GemmParams &p, const GemmParams *p2, int tile, hipStream_t s) {
+    const unsigned jx = join_blocks(p, tile), jw = p2 ? join_blocks(*p2, tile) : 0;
+    if (jx + jw == 0) return hipSuccess;
+    const GemmParams &q = p2 ? *p2 : p;
+    const dim3 grid(jx + jw);
+    switch (tile) {
+        case 0: hipLaunchKernelGGL((gemm_join_kernel<E, 256, 256, 64, 128>), grid, dim3(256), 0, s, p, q, (int)jx); break;
+        case 1: hipLaunchKernelGGL((gemm_join_kernel<E, 128, 128, 64, 64>), grid, dim3(256), 0, s, p, q, (int)jx); break;
+        default: hipLaunchKernelGGL((gemm_join_kernel<E, 64, 64, 32, 32>), grid, dim3(256), 0, s, p, q, (int)jx); break;
+    }
+    return hipGetLastError();
+}
+
 template <typename E, bool PT, bool QT>
 hipError_t launch_tile(const GemmParams &p, int tile, hipStream_t s) {
-    const dim3 grid((unsigned)(p.dp_tiles + p.sk_tiles * p.sk_pieces)), block((unsigned)kTiles[tile].threads);
+    const dim3 grid(units_of(p)), block((unsigned)kTiles[tile].threads);
     switch (tile) {
         case 0: {
             GemmParams q = p;
@@ -507,22 +571,27 @@ hipError_t launch_tile(const GemmParams &p, int tile, hipStream_t s) {
             hipLaunchKernelGGL((gemm_pp_kernel<E, PT, QT>), cus, block, 0, s, q);
             break;
         }
-        case 1:
-            hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 128, 128, 64, 64, 2, 1>), grid, block, 0, s, p);
-            break;
-        case 2: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 64, 64, 32, 32, 4, 1>), grid, block, 0, s, p); break;
-        default: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, 64, 64, 32, 32, 2, 4>), grid, block, 0, s, p); break;
+        case 1: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, Ring128>), grid, block, 0, s, p); break;
+        case 2: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, Ring64>), grid, block, 0, s, p); break;
+        default: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, Ring64G4>), grid, block, 0, s, p); break;
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !p.sk_tiles) return e;
-    const GemmTile &t = kTiles[tile];
-    const dim3 jb((unsigned)((int64_t)p.sk_tiles * (t.bm * t.bn / 4) / 256));
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : launch_join<E>(p, nullptr, tile, s);
+}
+
+template <typename E>
+hipError_t launch_pair(const GemmParams &px, const GemmParams &pw, int tile, const ColumnSumParams &cs,
+                       hipStream_t s) {
+    const int xu = (int)units_of(px), wu = (int)units_of(pw);
+    const dim3 grid((unsigned)(xu + wu + (cs.out0 ? (cs.cols + 15) / 16 : 0))), block((unsigned)kTiles[tile].threads);
     switch (tile) {
-        case 0: hipLaunchKernelGGL((gemm_join_kernel<E, 256, 256, 64, 128>), jb, dim3(256), 0, s, p); break;
-        case 1: hipLaunchKernelGGL((gemm_join_kernel<E, 128, 128, 64, 64>), jb, dim3(256), 0, s, p); break;
-        default: hipLaunchKernelGGL((gemm_join_kernel<E, 64, 64, 32, 32>), jb, dim3(256), 0, s, p); break;
+        case 1: hipLaunchKernelGGL((gemm_pair_kernel<E, Ring128>), grid, block, 0, s, px, pw, cs, xu, wu); break;
+        case 2: hipLaunchKernelGGL((gemm_pair_kernel<E, Ring64>), grid, block, 0, s, px, pw, cs, xu, wu); break;
+        case 3: hipLaunchKernelGGL((gemm_pair_kernel<E, Ring64G4>), grid, block, 0, s, px, pw, cs, xu, wu); break;
+        default: return hipErrorInvalidValue;
     }
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : launch_join<E>(px, &pw, tile, s);
 }
 
 }  // namespace
@@ -551,6 +620,11 @@ hipError_t launch_gemm(const GemmParams &p, int tile, GemmLayout layout, hipStre
         default:
             return p.bf16 ? launch_tile<__bf16, true, true>(p, tile, s) : launch_tile<_Float16, true, true>(p, tile, s);
     }
+}
+
+hipError_t launch_gemm_pair(const GemmParams &dx, const GemmParams &dw, int tile, const ColumnSumParams &cs,
+                            hipStream_t s) {
+    return dx.bf16 ? launch_pair<__bf16>(dx, dw, tile, cs, s) : launch_pair<_Float16>(dx, dw, tile, cs, s);
 }
 
 namespace {

@@ -46,6 +46,7 @@ struct GemmPlan {
 
 constexpr double kJoinBytesPerUs = 9e6;
 constexpr double kJoinLaunchUs = 4.5;
+constexpr double kPairGain = 1.1;  // what sharing the card gains beyond plan_pair's times
 constexpr size_t kMaxPartial = (size_t)256 << 20;
 
 // Time of `units` workgroups of `steps` steps each: rounds of as many as fit
@@ -63,27 +64,37 @@ double rounds_us(const c3d::GemmTile &t, c3d::GemmLayout layout, int64_t units, 
     return us;
 }
 
+// CONV3D_LINEAR_TILE: a kernel's name, or its name + "+pair", which also makes
+// a backward pass run dx and dw in one launch of it.
+struct Forced {
+    const char *v = getenv("CONV3D_LINEAR_TILE");
+    const size_t len = v ? strcspn(v, "+") : 0;
+    bool is(const char *name) const { return v && strlen(name) == len && strncmp(v, name, len) == 0; }
+    bool pair() const { return v && strcmp(v + len, "+pair") == 0; }
+};
+
 // The kernel and decomposition with the least time by the measured rates.  A
 // last partial round of tiles can be run as pieces of the contraction instead,
 // which costs writing and adding fp32 partials in a second launch.
-GemmPlan plan_gemm(int64_t m, int n, int64_t k, c3d::GemmLayout layout) {
+GemmPlan plan_gemm(int64_t m, int n, int64_t k, c3d::GemmLayout layout, double *us) {
     int count = 0;
     const c3d::GemmTile *tiles = c3d::gemm_tiles(&count);
-    const char *force = getenv("CONV3D_LINEAR_TILE");
+    const Forced force;
     GemmPlan best;
     double best_s = -1.0;
     const bool rows_ok = layout == c3d::kGemmForward && m <= c3d::kGemmRowsMax;
-    if (rows_ok && (!force || strcmp(force, tiles[c3d::kGemmRowsTile].name) == 0)) {
+    *us = 0.0;
+    if (rows_ok && (!force.v || force.is(tiles[c3d::kGemmRowsTile].name))) {
         best.tile = c3d::kGemmRowsTile;
         best.m_tiles = 1;
         best.n_tiles = best.dp = (n + 15) / 16;
         return best;
     }
-    for (int pass = force ? 0 : 1; pass < 2 && best_s < 0.0; ++pass)
+    for (int pass = force.v ? 0 : 1; pass < 2 && best_s < 0.0; ++pass)
         for (int i = 0; i < count; ++i) {
             const c3d::GemmTile &t = tiles[i];
             if (i == c3d::kGemmRowsTile) continue;
-            if (pass == 0 && strcmp(force, t.name) != 0) continue;
+            if (pass == 0 && !force.is(t.name)) continue;
             GemmPlan g;
             g.tile = i;
             g.m_tiles = (int)((m + t.bm - 1) / t.bm);
@@ -114,6 +125,71 @@ GemmPlan plan_gemm(int64_t m, int n, int64_t k, c3d::GemmLayout layout) {
                 best = pick;
             }
         }
+    *us = best_s;
+    return best;
+}
+
+// Tiles of one product, all split into `pieces` (1: none).
+GemmPlan even_split(int tile, const c3d::GemmTile &t, int64_t m, int n, int64_t k, int pieces) {
+    GemmPlan g;
+    g.tile = tile;
+    g.m_tiles = (int)((m + t.bm - 1) / t.bm);
+    g.n_tiles = (n + t.bn - 1) / t.bn;
+    g.niter = (int)((k + t.bk - 1) / t.bk);
+    const int all = g.m_tiles * g.n_tiles;
+    if (pieces > 1) {
+        g.sk = all;
+        g.pieces = pieces;
+        g.partial_bytes = (size_t)all * pieces * t.bm * t.bn * 4;
+    } else {
+        g.dp = all;
+    }
+    return g;
+}
+
+// dx and dw in one launch, sharing the card: the tile and the pieces of each
+// with the least time, and that time.  Units that fit the card at once take as
+// long as the longest, at the rate of all of them; more take the sum of their
+// steps at the full card's rate.
+double plan_pair(int64_t m, int n, int k, GemmPlan *dx, GemmPlan *dw) {
+    int count = 0;
+    const c3d::GemmTile *tiles = c3d::gemm_tiles(&count);
+    const Forced force;
+    double best = -1.0;
+    for (int i = c3d::kGemmPairFirst; i <= c3d::kGemmPairLast; ++i) {
+        const c3d::GemmTile &t = tiles[i];
+        if (force.v && !force.is(t.name)) continue;
+        const int64_t slots = (int64_t)kCUs * t.per_cu;
+        auto steps = [&](const GemmPlan &g) {
+            const int per = g.pieces ? (g.niter + g.pieces - 1) / g.pieces : g.niter;
+            return (double)((per + t.groups - 1) / t.groups);
+        };
+        auto units = [](const GemmPlan &g) { return (int64_t)g.dp + (int64_t)g.sk * g.pieces; };
+        for (int px = 1; px <= 8; ++px)
+            for (int pw = 1; pw <= c3d::kGemmMaxPieces; ++pw) {
+                const GemmPlan x = even_split(i, t, m, k, n, px), w = even_split(i, t, n, k, m, pw);
+                if ((px > 1 && px * 4 > x.niter) || (pw > 1 && pw * 4 > w.niter)) continue;
+                const size_t bytes = x.partial_bytes + w.partial_bytes;
+                if (bytes > kMaxPartial) continue;
+                const int64_t all = units(x) + units(w);
+                auto time_of = [&](const GemmPlan &g, c3d::GemmLayout l) {
+                    double step = t.step_us_full * all / slots;
+                    if (step > t.step_us_full) step = t.step_us_full;
+                    if (step < t.step_us_few[l]) step = t.step_us_few[l];
+                    return steps(g) * step + t.fixed_us;
+                };
+                const double tx = time_of(x, c3d::kGemmDx), tw = time_of(w, c3d::kGemmDw);
+                double us = tx > tw ? tx : tw;
+                const double sum = (units(x) * tx + units(w) * tw) / slots;
+                if (all > slots) us = sum + 0.5 * us;
+                if (bytes) us += 2.0 * bytes / kJoinBytesPerUs + kJoinLaunchUs;
+                if (best < 0.0 || us < best) {
+                    best = us;
+                    *dx = x;
+                    *dw = w;
+                }
+            }
+    }
     return best;
 }
 
@@ -166,6 +242,8 @@ struct linear_plan_s {
     linear_desc d;
     int64_t xs, ys, rs;
     GemmPlan fwd, dx, dw;
+    GemmPlan pair_dx, pair_dw;  // dx and dw in one launch, when both are asked for
+    bool pair;
     int strips;               // partial sums of dbias
     size_t off_col, off_part; // backward workspace: [dz][column sums][partial tiles]
     size_t back_bytes;
@@ -199,11 +277,19 @@ conv3d_status linear_plan(const linear_desc *d, linear_plan_t *out, size_t *work
     p->strips = c3d::act_grad_strips(d->m, d->n);
     p->off_col = p->off_part = p->back_bytes = 0;
     if (d->m > 0) {
-        p->fwd = plan_gemm(d->m, d->n, d->k, c3d::kGemmForward);
-        p->dx = plan_gemm(d->m, d->k, d->n, c3d::kGemmDx);
-        p->dw = plan_gemm(d->n, d->k, d->m, c3d::kGemmDw);
+        double us_f, us_x, us_w;
+        p->fwd = plan_gemm(d->m, d->n, d->k, c3d::kGemmForward, &us_f);
+        p->dx = plan_gemm(d->m, d->k, d->n, c3d::kGemmDx, &us_x);
+        p->dw = plan_gemm(d->n, d->k, d->m, c3d::kGemmDw, &us_w);
+        const Forced force;
+        const double us_pair = plan_pair(d->m, d->n, d->k, &p->pair_dx, &p->pair_dw);
+        // one launch less, and neither product's tail leaves the card idle
+        p->pair = us_pair >= 0.0 &&
+                  (force.v ? force.pair() : us_pair < kPairGain * (us_x + us_w) + kJoinLaunchUs);
         const size_t dz = d->act != CONV3D_ACT_NONE ? align256((size_t)d->m * d->n * 2) : 0;
-        const size_t part = p->dx.partial_bytes > p->dw.partial_bytes ? p->dx.partial_bytes : p->dw.partial_bytes;
+        size_t part = p->dx.partial_bytes > p->dw.partial_bytes ? p->dx.partial_bytes : p->dw.partial_bytes;
+        const size_t both = p->pair ? p->pair_dx.partial_bytes + p->pair_dw.partial_bytes : 0;
+        if (both > part) part = both;
         p->off_col = dz;
         p->off_part = dz + align256((size_t)p->strips * d->n * 4);
         p->back_bytes = p->off_part + part;
@@ -318,6 +404,7 @@ conv3d_status linear_backward(linear_plan_t p, const void *dy, const void *x, co
     char *ws = static_cast<char *>(workspace);
     const _Float16 *dz = in16(dy);
     int64_t dz_stride = p->ys;
+    c3d::ColumnSumParams cs = {};
     if (act || dbias) {
         c3d::ActGradParams a = {};
         a.dy = in16(dy);
@@ -331,34 +418,43 @@ conv3d_status linear_backward(linear_plan_t p, const void *dy, const void *x, co
         a.bf16 = bf16;
         a.strips = p->strips;
         e = c3d::launch_act_grad(a, s);
-        if (e == hipSuccess && dbias)
-            e = c3d::launch_column_sum(a.colpart, p->strips, d.n, out16(dbias), nullptr, 1, bf16, s);
+        cs.part = a.colpart;
+        cs.out0 = out16(dbias);
+        cs.rows = p->strips;
+        cs.cols = cs.split = d.n;
+        cs.bf16 = bf16;
         if (act) {
             dz = a.dz;
             dz_stride = d.n;
         }
     }
-    if (e == hipSuccess && dx) {
-        c3d::GemmParams q = {};
-        fill(q, p->dx, d.m, d.k, d.n, bf16, ws + p->off_part);
-        q.p = in16(w);
-        q.p_stride = d.k;
-        q.q = dz;
-        q.q_stride = dz_stride;
-        q.y = out16(dx);
-        q.y_stride = p->xs;
-        e = c3d::launch_gemm(q, p->dx.tile, c3d::kGemmDx, s);
+    const bool pair = dx && dw && p->pair;
+    if (e == hipSuccess && dbias && !pair) e = c3d::launch_column_sum(cs, s);
+    c3d::GemmParams qx = {}, qw = {};
+    char *part = ws + p->off_part;
+    if (dx) {
+        fill(qx, pair ? p->pair_dx : p->dx, d.m, d.k, d.n, bf16, part);
+        qx.p = in16(w);
+        qx.p_stride = d.k;
+        qx.q = dz;
+        qx.q_stride = dz_stride;
+        qx.y = out16(dx);
+        qx.y_stride = p->xs;
     }
-    if (e == hipSuccess && dw) {
-        c3d::GemmParams q = {};
-        fill(q, p->dw, d.n, d.k, d.m, bf16, ws + p->off_part);
-        q.p = in16(x);
-        q.p_stride = p->xs;
-        q.q = dz;
-        q.q_stride = dz_stride;
-        q.y = out16(dw);
-        q.y_stride = d.k;
-        e = c3d::launch_gemm(q, p->dw.tile, c3d::kGemmDw, s);
+    if (dw) {
+        fill(qw, pair ? p->pair_dw : p->dw, d.n, d.k, d.m, bf16, pair ? part + p->pair_dx.partial_bytes : part);
+        qw.p = in16(x);
+        qw.p_stride = p->xs;
+        qw.q = dz;
+        qw.q_stride = dz_stride;
+        qw.y = out16(dw);
+        qw.y_stride = d.k;
+    }
+    if (pair) {
+        if (e == hipSuccess) e = c3d::launch_gemm_pair(qx, qw, p->pair_dx.tile, cs, s);
+    } else {
+        if (e == hipSuccess && dx) e = c3d::launch_gemm(qx, p->dx.tile, c3d::kGemmDx, s);
+        if (e == hipSuccess && dw) e = c3d::launch_gemm(qw, p->dw.tile, c3d::kGemmDw, s);
     }
     return launched(e, "linear_backward");
 }

@@ -53,6 +53,12 @@ constexpr int kGemmMaxPieces = 32;
 constexpr int kGemmRowsTile = 4, kGemmRowsMax = 16;
 const GemmTile *gemm_tiles(int *count);
 hipError_t launch_gemm(const GemmParams &p, int tile, GemmLayout layout, hipStream_t s);
+// dx, dw and the column sums (cs.out0 null: none) in one launch, with one tile
+// of kGemmPairFirst .. kGemmPairLast for both.
+constexpr int kGemmPairFirst = 1, kGemmPairLast = 3;
+struct ColumnSumParams;
+hipError_t launch_gemm_pair(const GemmParams &dx, const GemmParams &dw, int tile, const ColumnSumParams &cs,
+                            hipStream_t s);
 
 // dz = dy * act'(z) (dz may be null: no activation) and the column sums of dz
 // as `strips` fp32 partials [strips][n] (colpart may be null).
@@ -66,11 +72,16 @@ struct ActGradParams {
 };
 int32_t act_grad_strips(int64_t m, int32_t n);
 hipError_t launch_act_grad(const ActGradParams &p, hipStream_t s);
-// out[c] = sum over rows of part[rows][cols], rounded to the element type; the
-// columns are split into `parts` equal outputs (any of them may be null).
-hipError_t launch_column_sum(const float *part, int32_t rows, int32_t cols, _Float16 *out0, _Float16 *out1,
-                             int32_t parts, int32_t bf16, hipStream_t s);
-// Zeros into n 16-byte groups' worth of bytes (a multiple of 2), with rows of `width` elements.
+// The sums over the rows of part [rows][cols] (cols a multiple of 8), rounded to
+// the element type: columns below split into out0, the others into out1 (either
+// may be null).
+struct ColumnSumParams {
+    const float *part;
+    _Float16 *out0, *out1;
+    int32_t rows, cols, split, bf16;
+};
+hipError_t launch_column_sum(const ColumnSumParams &p, hipStream_t s);
+// Zeros into rows of `width` elements, `stride` apart.
 hipError_t launch_zero_rows(_Float16 *y, int64_t rows, int32_t width, int64_t stride, hipStream_t s);
 
 // ---- layernorm

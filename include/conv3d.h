@@ -342,7 +342,8 @@ typedef struct {
  * Products of few rows, or with few tiles, split the contraction over several
  * workgroups, which leave fp32 partials in the workspace that a second small
  * kernel adds in a fixed order.  The environment variable
- * CONV3D_LINEAR_TILE=<name> forces a kernel.
+ * CONV3D_LINEAR_TILE=<name> forces a kernel (where it can run the product), and
+ * <name>+pair also the backward pass's two products into one launch of it.
  */
 conv3d_status linear_plan(const linear_desc *d, linear_plan_t *out, size_t *workspace_bytes);
 conv3d_status linear_plan_query(linear_plan_t p, linear_plan_info *info);

@@ -174,6 +174,13 @@ def check_backward(m, n, k, act, dtype, gap=0, seed=1, tile=None):
         assert_within(got, ref, s, what)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("tile", ["m128n128k64+pair", "m64n64k64+pair", "m64n64k64g4+pair"])
+@pytest.mark.parametrize("size", [(1, 8, 8), (70, 200, 40), (300, 520, 264), (2000, 776, 520), (5000, 72, 72)], ids=str)
+def test_backward_in_one_launch(size, tile, dtype):
+    check_backward(*size, act="silu", dtype=dtype, gap=8, seed=4, tile=tile)
+
+
 BACK_SIZES = [(1, 8, 8), (1, 264, 1032), (7, 72, 40), (31, 520, 136), (33, 136, 264), (64, 2056, 72), (129, 264, 392),
               (257, 72, 520), (1001, 264, 136), (2049, 392, 264)]
 
