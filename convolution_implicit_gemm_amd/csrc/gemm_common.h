@@ -255,6 +255,17 @@ struct Fragments {
     }
 };
 
+// 2-byte buffer load; out-of-range loads read zero.
+__device__ __forceinline__ _Float16 load2(buf_rsrc r, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_bit_cast(_Float16, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+#else
+    (void)r;
+    (void)off;
+    return (_Float16)0.0f;
+#endif
+}
+
 // 16-byte buffer store; out-of-range stores are dropped.
 __device__ __forceinline__ void gemm_store16(buf_rsrc r, uint32_t off, half8_t v) {
 #if defined(__HIP_DEVICE_COMPILE__)

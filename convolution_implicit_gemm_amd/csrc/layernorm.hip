@@ -21,6 +21,8 @@ namespace c3d {
 
 namespace {
 
+constexpr int64_t kLnWideRows = 512;
+
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
@@ -130,7 +132,9 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGra
             dg[i][e] = db[i][e] = 0.0f;
         }
     }
-    // The next row's loads are issued before the current row is worked on.
+    // The next row's loads are issued before the current row is worked on (a
+    // block of 16 waves has no registers to spare for that).
+    constexpr bool AHEAD = WPR < 16;
     struct Row {
         e16x8_t x[NV], dy[NV], dres[NV];
         float2 st;
@@ -151,9 +155,12 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGra
     Row cur, next;
     int64_t row = (int64_t)blockIdx.x * TEAMS + team;
     const int64_t rounds = (p.rows - (int64_t)blockIdx.x * TEAMS + step - 1) / step;  // the same for all teams
-    fetch(row, cur);
+    if (AHEAD) fetch(row, cur);
     for (int64_t k = 0; k < rounds; ++k, row += step) {
-        if (k + 1 < rounds) fetch(row + step, next);
+        if (!AHEAD)
+            fetch(row, cur);
+        else if (k + 1 < rounds)
+            fetch(row + step, next);
         float s1 = 0.0f, s2 = 0.0f;
         // columns past the end and rows past the end read zeros with zero
         // statistics: they add nothing
@@ -185,7 +192,7 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGra
                 }
                 *reinterpret_cast<e16x8_t *>(p.dx + row * p.x_stride + c) = o;
             }
-        cur = next;
+        if (AHEAD) cur = next;
     }
     if (!p.part) return;
     float *out = p.part + (int64_t)blockIdx.x * 2 * p.c;
@@ -234,26 +241,30 @@ __global__ __launch_bounds__(256) void zero_rows_kernel(_Float16 *y, int64_t row
         y[i / width * stride + i % width] = (_Float16)0.0f;
 }
 
-// (vectors per lane, waves per row) of a channel count.
+// (vectors per lane, waves per row) of a channel count.  `wide`: one row per
+// block of four waves also where a wave could hold it.
 template <typename F>
-hipError_t ln_dispatch(int c, F &&f) {
+hipError_t ln_dispatch(int c, bool wide, F &&f) {
     using std::integral_constant;
     if (c <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    if (wide && c <= 2048) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
     if (c <= 1024) return f(integral_constant<int, 2>{}, integral_constant<int, 1>{});
     if (c <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
     if (c <= 4096) return f(integral_constant<int, 2>{}, integral_constant<int, 4>{});
-    if (c <= 8192) return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+    if (c <= 8192) return f(integral_constant<int, 2>{}, integral_constant<int, 8>{});
     return f(integral_constant<int, 2>{}, integral_constant<int, 16>{});
 }
 
-int ln_teams(int c) { return c <= 2048 ? 4 : 1; }
+// Few rows: a row's latency counts, not the stream's rate.
+bool ln_wide(int64_t rows) { return rows <= kLnWideRows; }
+int ln_teams(int64_t rows, int c) { return c <= (ln_wide(rows) ? 512 : 2048) ? 4 : 1; }
 
 }  // namespace
 
 hipError_t launch_layernorm(const LnParams &p, hipStream_t s) {
-    const int64_t want = (p.rows + ln_teams(p.c) - 1) / ln_teams(p.c);
+    const int64_t want = (p.rows + ln_teams(p.rows, p.c) - 1) / ln_teams(p.rows, p.c);
     const unsigned grid = (unsigned)(want < 65536 ? want : 65536);
-    return ln_dispatch(p.c, [&](auto nv, auto wpr) {
+    return ln_dispatch(p.c, ln_wide(p.rows), [&](auto nv, auto wpr) {
         constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
         if (p.bf16)
             hipLaunchKernelGGL((layernorm_kernel<__bf16, NV, WPR>), dim3(grid), dim3(ln_threads<WPR>()), 0, s, p);
@@ -264,14 +275,18 @@ hipError_t launch_layernorm(const LnParams &p, hipStream_t s) {
 }
 
 int32_t ln_grad_blocks(int64_t rows, int32_t c) {
-    // at least two rows per team: a block's partial costs about as much as a row
-    const int64_t want = (rows + 2 * ln_teams(c) - 1) / (2 * ln_teams(c));
-    return (int32_t)(want < 512 ? want : 512);
+    // two rows per team and more: a block's partial is written and read again, as
+    // much traffic as two or three rows.  Up to four, while 256 blocks are left.
+    const int64_t passes = (rows + ln_teams(rows, c) - 1) / ln_teams(rows, c);
+    int64_t rounds = (passes + 255) / 256;
+    if (rounds > 4) rounds = (passes + 511) / 512 < 4 ? 4 : (passes + 511) / 512;
+    if (rounds < 2 && passes > 1) rounds = 2;
+    return (int32_t)((passes + rounds - 1) / rounds);
 }
 
 hipError_t launch_layernorm_grad(const LnGradParams &p, hipStream_t s) {
     const unsigned grid = (unsigned)ln_grad_blocks(p.rows, p.c);
-    hipError_t e = ln_dispatch(p.c, [&](auto nv, auto wpr) {
+    hipError_t e = ln_dispatch(p.c, ln_wide(p.rows), [&](auto nv, auto wpr) {
         constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
         if (p.bf16)
             hipLaunchKernelGGL((layernorm_grad_kernel<__bf16, NV, WPR>), dim3(grid), dim3(ln_threads<WPR>()), 0, s, p);

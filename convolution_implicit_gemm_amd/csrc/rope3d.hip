@@ -34,11 +34,11 @@ __device__ __forceinline__ int small_div(int a, int b, float rcp_b) {
     return q;
 }
 
+// The block's tokens from `first` on.  turn: [token][pair] (cos, sin); place: a
+// token's offsets in q, q's output, k, k's output.
 template <typename E, bool HALVES>
-__global__ __launch_bounds__(kRopeThreads) void rope3d_kernel(RopeParams p, int tasks, int tokens_per_block) {
-    extern __shared__ float2 turn[];  // [token][pair] (cos, sin)
-    __shared__ int64_t place[kRopeMaxTokens][4];  // a token's offsets in q, q's output, k, k's output
-    const int64_t first = (int64_t)blockIdx.x * tokens_per_block;  // flattened (sample, token)
+__device__ __forceinline__ void rope3d_tokens(const RopeParams &p, int64_t first, int tasks, int tokens_per_block,
+                                              float2 *turn, int64_t (*place)[4]) {
     const int64_t left = p.tokens * p.n - first;
     const int ntok = left < tokens_per_block ? (int)left : tokens_per_block;
     const int64_t ns0 = first / p.tokens, tok0 = first - ns0 * p.tokens;  // the first token's sample and index
@@ -144,6 +144,17 @@ __global__ __launch_bounds__(kRopeThreads) void rope3d_kernel(RopeParams p, int 
     }
 }
 
+template <typename E, bool HALVES>
+__global__ __launch_bounds__(kRopeThreads) void rope3d_kernel(RopeParams p, int tasks, int tokens_per_block) {
+    extern __shared__ float2 turn[];
+    __shared__ int64_t place[kRopeMaxTokens][4];
+    const int64_t all = p.tokens * p.n, step = (int64_t)gridDim.x * tokens_per_block;
+    for (int64_t first = (int64_t)blockIdx.x * tokens_per_block; first < all; first += step) {
+        rope3d_tokens<E, HALVES>(p, first, tasks, tokens_per_block, turn, place);
+        __syncthreads();  // the next tokens' sines overwrite these
+    }
+}
+
 }  // namespace
 
 hipError_t launch_rope3d(const RopeParams &p, hipStream_t s) {
@@ -156,7 +167,8 @@ hipError_t launch_rope3d(const RopeParams &p, hipStream_t s) {
     if (tpb > kRopeMaxTokens) tpb = kRopeMaxTokens;
     while (tpb > 1 && (int64_t)tpb * per_token >= 1 << 22) --tpb;  // small_div's range
     while (tpb > 1 && (total + tpb - 1) / tpb < 1024) --tpb;
-    const dim3 grid((unsigned)((total + tpb - 1) / tpb));
+    const int64_t blocks = (total + tpb - 1) / tpb;
+    const dim3 grid((unsigned)(blocks < 1 << 22 ? blocks : 1 << 22));  // a launch holds fewer than 2^32 threads
     const size_t lds = (size_t)tpb * p.pairs * sizeof(float2);
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(kRopeThreads), lds, s, p, tasks, tpb);

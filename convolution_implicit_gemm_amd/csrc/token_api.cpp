@@ -73,6 +73,12 @@ struct Forced {
     bool pair() const { return v && strcmp(v + len, "+pair") == 0; }
 };
 
+// Launches hold fewer than 2^32 threads; the first tile's kernel launches at
+// most one workgroup per CU and only counts its units.
+bool runnable(int tile, const c3d::GemmTile &t, int64_t units) {
+    return tile == 0 ? units < (int64_t)1 << 30 : units * t.threads < (int64_t)1 << 31;
+}
+
 // The kernel and decomposition with the least time by the measured rates.  A
 // last partial round of tiles can be run as pieces of the contraction instead,
 // which costs writing and adding fp32 partials in a second launch.
@@ -102,6 +108,7 @@ GemmPlan plan_gemm(int64_t m, int n, int64_t k, c3d::GemmLayout layout, double *
             g.niter = (int)((k + t.bk - 1) / t.bk);
             const int64_t all = (int64_t)g.m_tiles * g.n_tiles;
             const int64_t slots = (int64_t)kCUs * t.per_cu;
+            if (!runnable(i, t, all)) continue;
             g.dp = (int)all;
             auto steps = [&](int pieces) { return (double)(((g.niter + pieces - 1) / pieces + t.groups - 1) / t.groups); };
             double sec = rounds_us(t, layout, all, steps(1));
@@ -159,6 +166,10 @@ double plan_pair(int64_t m, int n, int k, GemmPlan *dx, GemmPlan *dw) {
     for (int i = c3d::kGemmPairFirst; i <= c3d::kGemmPairLast; ++i) {
         const c3d::GemmTile &t = tiles[i];
         if (force.v && !force.is(t.name)) continue;
+        auto tiles_of = [&](int64_t rows, int64_t cols) {
+            return ((rows + t.bm - 1) / t.bm) * ((cols + t.bn - 1) / t.bn);
+        };
+        if (!runnable(i, t, (tiles_of(m, k) + tiles_of(n, k)) * 2)) continue;
         const int64_t slots = (int64_t)kCUs * t.per_cu;
         auto steps = [&](const GemmPlan &g) {
             const int per = g.pieces ? (g.niter + g.pieces - 1) / g.pieces : g.niter;

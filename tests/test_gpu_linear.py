@@ -82,6 +82,24 @@ def test_forward_is_exact_on_small_integers(size, tile):
     assert torch.equal(y.double(), ref)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("m,tile", [(3, None), (300, "m128n128k64"), (300, "m256n256k64"), (300, "m64n64k64g4")])
+def test_bias_alone_comes_through_exactly(m, tile, dtype):
+    # x = 0: y is the bias bit for bit, subnormal and infinite values too
+    dt = DTYPES[dtype]
+    n, k = 264, 72
+    b = normal(gen(2), (n,), dt)
+    b[:8] = torch.tensor([6e-8, -6e-8, 3e-5, -5.9e-5, float("inf"), -float("inf"), 65504.0, 0.0]).to(dt)
+    x, w = torch.zeros((m, k), dtype=dt, device="cuda:0"), normal(gen(3), (n, k), dt)
+    with env_var("CONV3D_LINEAR_TILE", tile):
+        plan = c3d.linear_plan(c3d.make_linear_desc(m, n, k, 0, c3d.CONV3D_F_BIAS |
+                                                    (c3d.CONV3D_F_BF16 if dtype == "bf16" else 0)))
+    y = torch.empty((m, n), dtype=dt, device="cuda:0")
+    c3d.linear_forward(plan, x, w, b, None, y, None, scratch(plan.workspace_bytes))
+    torch.cuda.synchronize()
+    assert torch.equal(y, b.expand(m, n))
+
+
 def test_split_contraction_joins_all_pieces():
     # few tiles and a long contraction: the plan splits it, and each piece counts
     plan, x, w, b, r, y, z = run_forward(256, 256, 16384, "gelu", "bf16", True, True, True, 8, 3, "m128n128k64")
