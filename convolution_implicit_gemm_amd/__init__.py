@@ -221,9 +221,30 @@ def _addr(t, what="tensor", elems=None, dtype=None):
     return t.data_ptr()
 
 
-def _elem_dtype(bf16):
+# What calls need of torch, bound at the first one that needs it (importing this
+# module does not import torch).
+_F16 = _BF16 = _F32 = _I32 = _raw_stream = _current_device = None
+
+
+def _bind_torch():
+    global _F16, _BF16, _F32, _I32
     import torch
-    return torch.bfloat16 if bf16 else torch.float16
+    _F16, _BF16, _F32, _I32 = torch.float16, torch.bfloat16, torch.float32, torch.int32
+
+
+def _bind_streams():
+    # the raw handle of the current stream, without building a Stream object
+    # (2.8 us of a small call's host time)
+    global _raw_stream, _current_device
+    import torch
+    torch.cuda.current_device()  # initialises the device
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _elem_dtype(bf16):
+    if _F16 is None:
+        _bind_torch()
+    return _BF16 if bf16 else _F16
 
 
 def _conv_sizes(desc, chunk_t=None):
@@ -238,10 +259,9 @@ def _conv_sizes(desc, chunk_t=None):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        # the raw handle of the current stream of the current device, without
-        # building a Stream object (2.8 us of a small call's host time)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _raw_stream is None:
+            _bind_streams()
+        return _raw_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -504,11 +524,10 @@ def linear_backward(plan: LinearPlan, dy, x, w, preact, dx, dw, dbias, workspace
 def layernorm(x, gamma, beta, y, stats, rows, c, eps, x_stride=0, y_stride=0, stream=None, bf16=False) -> None:
     """Enqueue y = LayerNorm(x) over the c channels of each row on ``stream``;
     gamma, beta and stats (fp32 [rows][2]: mean, 1 / sqrt(var + eps)) may be None."""
-    lib, dt = load_library(), _elem_dtype(bf16)
-    import torch
+    lib, dt = _lib or load_library(), _elem_dtype(bf16)
     fn = lib.layernorm_bf16 if bf16 else lib.layernorm
     _check(fn(_rows_addr(x, "x", rows, c, x_stride, dt), _addr(gamma, "gamma", c, dt), _addr(beta, "beta", c, dt),
-              _rows_addr(y, "y", rows, c, y_stride, dt), _addr(stats, "stats", 2 * rows, torch.float32), rows, c,
+              _rows_addr(y, "y", rows, c, y_stride, dt), _addr(stats, "stats", 2 * rows, _F32), rows, c,
               x_stride, y_stride, float(eps), _stream(stream)))
 
 
@@ -525,13 +544,12 @@ def layernorm_backward(dy, x, gamma, stats, dres, dx, dgamma, dbeta, rows, c, wo
                        workspace_bytes=None, stream=None, bf16=False) -> None:
     """Enqueue dx (+ dres), dgamma and dbeta of layernorm on ``stream``; gamma,
     dres, dgamma and dbeta may be None."""
-    lib, dt = load_library(), _elem_dtype(bf16)
-    import torch
+    lib, dt = _lib or load_library(), _elem_dtype(bf16)
     if workspace_bytes is None and isinstance(workspace, int):
         workspace_bytes = layernorm_backward_workspace(rows, c)
     fn = lib.layernorm_backward_bf16 if bf16 else lib.layernorm_backward
     _check(fn(_rows_addr(dy, "dy", rows, c, y_stride, dt), _rows_addr(x, "x", rows, c, x_stride, dt),
-              _addr(gamma, "gamma", c, dt), _addr(stats, "stats", 2 * rows, torch.float32),
+              _addr(gamma, "gamma", c, dt), _addr(stats, "stats", 2 * rows, _F32),
               _rows_addr(dres, "dres", rows, c, x_stride, dt), _rows_addr(dx, "dx", rows, c, x_stride, dt),
               _addr(dgamma, "dgamma", c, dt), _addr(dbeta, "dbeta", c, dt), rows, c, x_stride, y_stride,
               _addr(workspace, "workspace"), _workspace_bytes(workspace, workspace_bytes), _stream(stream)))
@@ -594,7 +612,6 @@ def rope3d_plan_destroy(plan: RopePlan) -> None:
 
 
 def _rope_call(fn, plan, q, k, q_out, k_out, positions, t_offset, stream, layouts):
-    import torch
     lq, lk, lqo, lko = layouts
     dt = plan.dtype
     if lk[0][2] == 0:
@@ -602,18 +619,18 @@ def _rope_call(fn, plan, q, k, q_out, k_out, positions, t_offset, stream, layout
     given = positions if plan.positions else None
     _check(fn(plan.handle, _strided_addr(q, "q", *lq, dt), _strided_addr(k, "k", *lk, dt),
               _strided_addr(q_out, "q_out", *lqo, dt), _strided_addr(k_out, "k_out", *lko, dt),
-              _addr(given, "positions", plan.positions, torch.int32), t_offset, _stream(stream)))
+              _addr(given, "positions", plan.positions, _I32), t_offset, _stream(stream)))
 
 
 def rope3d_forward(plan: RopePlan, q, k, q_out, k_out, positions=None, t_offset=0, stream=None) -> None:
     """Enqueue the rotation of q into q_out and k into k_out on ``stream``."""
-    _rope_call(load_library().rope3d_forward, plan, q, k, q_out, k_out, positions, t_offset, stream, plan.layouts)
+    _rope_call((_lib or load_library()).rope3d_forward, plan, q, k, q_out, k_out, positions, t_offset, stream, plan.layouts)
 
 
 def rope3d_backward(plan: RopePlan, dq_out, dk_out, dq, dk, positions=None, t_offset=0, stream=None) -> None:
     """Enqueue the gradient of rope3d_forward (strides: those of the outputs, then of the inputs)."""
     lq, lk, lqo, lko = plan.layouts
-    _rope_call(load_library().rope3d_backward, plan, dq_out, dk_out, dq, dk, positions, t_offset, stream,
+    _rope_call((_lib or load_library()).rope3d_backward, plan, dq_out, dk_out, dq, dk, positions, t_offset, stream,
                (lqo, lko, lq, lk))
 
 
