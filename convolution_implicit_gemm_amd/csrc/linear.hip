@@ -41,6 +41,7 @@ struct RingTile {
 using Ring128 = RingTile<128, 128, 64, 64, 2, 1>;
 using Ring64 = RingTile<64, 64, 32, 32, 4, 1>;
 using Ring64G4 = RingTile<64, 64, 32, 32, 2, 4>;
+using Ring128G2 = RingTile<128, 128, 64, 64, 2, 2>;
 
 // Work unit b of one product.
 template <typename E, bool PT, bool QT, typename T>
@@ -546,6 +547,7 @@ const GemmTile kTiles[] = {
     {"m128n128k64", 128, 128, kGemmBK, 256, 2, 1, {0.66, 0.7, 0.66}, 0.96, 2.5},
     {"m64n64k64", 64, 64, kGemmBK, 256, 2, 1, {0.26, 0.3, 0.3}, 0.4, 2.0},
     {"m64n64k64g4", 64, 64, kGemmBK, 1024, 1, 4, {0.42, 0.9, 1.3}, 0.88, 2.5},
+    {"m128n128k64g2", 128, 128, kGemmBK, 512, 1, 2, {0.7, 0.75, 0.8}, 0.95, 3.0},
     {"m16n16k32", 16, 16, 32, kRowsWaves * 64, 4, 1, {0.0, 0.0, 0.0}, 0.0, 0.0},  // few rows; not in the cost model
 };
 
@@ -564,7 +566,8 @@ hipError_t launch_join(const GemmParams &p, const GemmParams *p2, int tile, hipS
     const dim3 grid(jx + jw);
     switch (tile) {
         case 0: hipLaunchKernelGGL((gemm_join_kernel<E, 256, 256, 64, 128>), grid, dim3(256), 0, s, p, q, (int)jx); break;
-        case 1: hipLaunchKernelGGL((gemm_join_kernel<E, 128, 128, 64, 64>), grid, dim3(256), 0, s, p, q, (int)jx); break;
+        case 1:
+        case 4: hipLaunchKernelGGL((gemm_join_kernel<E, 128, 128, 64, 64>), grid, dim3(256), 0, s, p, q, (int)jx); break;
         default: hipLaunchKernelGGL((gemm_join_kernel<E, 64, 64, 32, 32>), grid, dim3(256), 0, s, p, q, (int)jx); break;
     }
     return hipGetLastError();
@@ -583,7 +586,8 @@ hipError_t launch_tile(const GemmParams &p, int tile, hipStream_t s) {
         }
         case 1: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, Ring128>), grid, block, 0, s, p); break;
         case 2: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, Ring64>), grid, block, 0, s, p); break;
-        default: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, Ring64G4>), grid, block, 0, s, p); break;
+        case 3: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, Ring64G4>), grid, block, 0, s, p); break;
+        default: hipLaunchKernelGGL((gemm_ring_kernel<E, PT, QT, Ring128G2>), grid, block, 0, s, p); break;
     }
     const hipError_t e = hipGetLastError();
     return e != hipSuccess ? e : launch_join<E>(p, nullptr, tile, s);

@@ -50,14 +50,14 @@ constexpr double kPairGain = 1.1;  // what sharing the card gains beyond plan_pa
 constexpr size_t kMaxPartial = (size_t)256 << 20;
 
 // Time of `units` workgroups of `steps` steps each: rounds of as many as fit
-// the card.  The steps of a partial round run at the rate of the fullest CU and
-// at the card's share (L2 serves the operands of all of them).
+// the card.  The steps of a partial round are as much faster as it is smaller
+// (L2 serves the operands of all of them), down to the time of a few.
 double rounds_us(const c3d::GemmTile &t, c3d::GemmLayout layout, int64_t units, double steps) {
     const int64_t slots = (int64_t)kCUs * t.per_cu;
     const int64_t full = units / slots, rem = units % slots;
     double us = full * (steps * t.step_us_full + t.fixed_us);
     if (rem) {
-        double step = rem > kCUs ? t.step_us_full : t.step_us_full * rem / slots;
+        double step = t.step_us_full * rem / slots;
         if (step < t.step_us_few[layout]) step = t.step_us_few[layout];
         us += steps * step + t.fixed_us;
     }

@@ -50,7 +50,7 @@ struct GemmTile {
 constexpr int kGemmCUs = 256;
 constexpr int kGemmMaxPieces = 32;
 // The kernel of few rows, an index into gemm_tiles: forward products of at most kGemmRowsMax rows.
-constexpr int kGemmRowsTile = 4, kGemmRowsMax = 16;
+constexpr int kGemmRowsTile = 5, kGemmRowsMax = 16;
 const GemmTile *gemm_tiles(int *count);
 hipError_t launch_gemm(const GemmParams &p, int tile, GemmLayout layout, hipStream_t s);
 // dx, dw and the column sums (cs.out0 null: none) in one launch, with one tile

@@ -10,7 +10,7 @@ from token_helpers import (ACTS, DTYPES, U24, act64, assert_unmarked_only, asser
 
 pytestmark = pytest.mark.gpu
 
-TILES = [None, "m128n128k64", "m256n256k64", "m64n64k64", "m64n64k64g4"]
+TILES = [None, "m128n128k64", "m256n256k64", "m64n64k64", "m64n64k64g4", "m128n128k64g2"]
 
 
 def run_forward(m, n, k, act, dtype, bias, residual, keep, gap, seed, tile=None, x=None, w=None):
