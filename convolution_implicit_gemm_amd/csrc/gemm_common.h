@@ -11,58 +11,58 @@ namespace c3d {
 constexpr int kGemmBK = 64;                 // contraction per stage
 constexpr int kGemmRow = kGemmBK * 2;       // bytes of one LDS row, contraction contiguous
 
-// z -> act(z), fp32.  GELU (erf form) through Abramowitz and Stegun 7.1.26,
-// erf(x) = 1 - (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x),
-// absolute error 1.5e-7; the tanh form as z * sigmoid(2u).
+// z -> act(z) and act'(z), fp32, two transcendental instructions each.
+// GELU (erf form) through Abramowitz and Stegun 7.1.26, erf(x) = 1 - (a1 t + ...
+// + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), absolute error 1.5e-7; the tanh
+// form as z * sigmoid(2u), u = sqrt(2 / pi) (z + 0.044715 z^3).
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGeluA = 0.797884560802865356f, kGeluB = 0.044715f;
 
 __device__ __forceinline__ float sigmoid_f(float v) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * v));
 }
-// (Phi(z), exp(-z^2 / 2)) of the standard normal distribution
-__device__ __forceinline__ float normal_cdf(float z, float &ex) {
-    const float x = fabsf(z) * 0.707106781186547524f;
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
-    ex = __builtin_amdgcn_exp2f(-kLog2e * x * x);
-    float q = fmaf(t, 1.061405429f, -1.453152027f);
-    q = fmaf(t, q, 1.421413741f);
-    q = fmaf(t, q, -0.284496736f);
-    q = fmaf(t, q, 0.254829592f);
-    const float tail = 0.5f * q * t * ex;  // Phi(-|z|)
-    return z < 0.0f ? tail : 1.0f - tail;
+// sigmoid(2u) of the tanh form: 1 / (1 + 2^(z (k + k B z^2)))
+__device__ __forceinline__ float sigmoid_2u(float z) {
+    constexpr float k = -2.0f * kLog2e * kGeluA;
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * fmaf(k * kGeluB, z * z, k)));
+}
+// Phi(-|z|) of the standard normal distribution; ex: exp(-z^2 / 2)
+__device__ __forceinline__ float normal_tail(float z, float &ex) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.707106781186547524f, fabsf(z), 1.0f));
+    ex = __builtin_amdgcn_exp2f(z * (-0.5f * kLog2e * z));
+    float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    q = fmaf(t, q, 0.5f * 1.421413741f);
+    q = fmaf(t, q, 0.5f * -0.284496736f);
+    q = fmaf(t, q, 0.5f * 0.254829592f);
+    return q * t * ex;
 }
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
     if constexpr (ACT == CONV3D_ACT_SILU) return z * sigmoid_f(z);
     if constexpr (ACT == CONV3D_ACT_GELU) {
         float ex;
-        return z * normal_cdf(z, ex);
+        return fmaf(-fabsf(z), normal_tail(z, ex), fmaxf(z, 0.0f));  // z Phi(z) for either sign
     }
-    if constexpr (ACT == CONV3D_ACT_GELU_TANH) {
-        // z / (1 + 2^(z (k + kB z^2))), k = -2 log2(e) sqrt(2 / pi)
-        constexpr float k = -2.0f * kLog2e * kGeluA;
-        return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * fmaf(k * kGeluB, z * z, k)));
-    }
+    if constexpr (ACT == CONV3D_ACT_GELU_TANH) return z * sigmoid_2u(z);
     return z;
 }
-// act'(z).  The arguments whose powers could overflow are bounded where the
-// derivative is 0 or 1 to the last bit anyway.
+// The arguments whose powers could overflow are bounded where the derivative is
+// 0 or 1 to the last bit anyway.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == CONV3D_ACT_NONE) return 1.0f;
-    z = fminf(fmaxf(z, -1e4f), 1e4f);
+    z = z > 1e4f ? 1e4f : z < -1e4f ? -1e4f : z;  // a NaN stays one
     if constexpr (ACT == CONV3D_ACT_SILU) {
         const float s = sigmoid_f(z);
         return s * fmaf(z, 1.0f - s, 1.0f);
     }
     if constexpr (ACT == CONV3D_ACT_GELU) {
         float ex;
-        const float cdf = normal_cdf(z, ex);
-        return fmaf(z * 0.398942280401432678f, ex, cdf);
+        const float tail = normal_tail(z, ex);
+        return fmaf(z * 0.398942280401432678f, ex, z < 0.0f ? tail : 1.0f - tail);
     }
-    const float s = sigmoid_f(2.0f * kGeluA * fmaf(kGeluB * z, z * z, z));
-    return s * fmaf(z * (1.0f - s), 2.0f * kGeluA * fmaf(3.0f * kGeluB * z, z, 1.0f), 1.0f);
+    const float s = sigmoid_2u(z);
+    return s * fmaf(z * (1.0f - s), fmaf(6.0f * kGeluA * kGeluB * z, z, 2.0f * kGeluA), 1.0f);
 }
 
 // Calls f(std::integral_constant<int, ACT>) for the activation chosen at run time.
@@ -299,34 +299,36 @@ __device__ __forceinline__ int tile_chunk(int v, int c) {
     return v * BN * 2 + ((c ^ (v & (BN / 8 - 1))) << 4);
 }
 
-// Tile rows between LDS and global memory in whole rows, 16 bytes per lane.
+// Tile rows between LDS and global memory in whole rows, 16 bytes per lane: a
+// thread takes one chunk of every RP-th row.  Rows past the matrix lie past the
+// records; a column past it is out of range itself.
 template <int BM, int BN, int THREADS>
 __device__ __forceinline__ void store_rows(const char *smem, _Float16 *out, int64_t stride, int rows, int cols) {
-    constexpr int CH = BN / 8;
+    constexpr int CH = BN / 8, RP = THREADS / CH;
+    static_assert(RP % CH == 0, "a thread's rows share one swizzle");
     const buf_rsrc r = make_rsrc(out, (uint32_t)((rows - 1) * (int)stride + cols) * 2u);
+    const int v0 = (int)threadIdx.x / CH, c = (int)threadIdx.x % CH;
+    const uint32_t off = c * 8 < cols ? (uint32_t)(v0 * (int)stride + c * 8) * 2u : kOOB;
+    const char *at = smem + tile_chunk<BN>(v0, c);
 #pragma unroll
-    for (int k = 0; k < BM * CH / THREADS; ++k) {
-        const int lin = k * THREADS + threadIdx.x;
-        const int v = lin / CH, c = lin % CH;
-        half8_t h = *reinterpret_cast<const half8_t *>(smem + tile_chunk<BN>(v, c));
-        if (v & 16) h = __builtin_shufflevector(h, h, 4, 5, 6, 7, 0, 1, 2, 3);
-        gemm_store16(r, v < rows && c * 8 < cols ? (uint32_t)(v * (int)stride + c * 8) * 2u : kOOB, h);
+    for (int k = 0; k < BM / RP; ++k) {
+        half8_t h = *reinterpret_cast<const half8_t *>(at + k * RP * BN * 2);
+        if ((v0 + k * RP) & 16) h = __builtin_shufflevector(h, h, 4, 5, 6, 7, 0, 1, 2, 3);
+        gemm_store16(r, off + (uint32_t)(k * RP * 2) * (uint32_t)stride, h);
     }
 }
 // The residual's rows into the same places.  The 8-byte halves are not swapped
 // (they arrive as they are); the fragments read them so.
 template <int BM, int BN, int THREADS>
 __device__ __forceinline__ void load_rows(char *smem, const _Float16 *in, int64_t stride, int rows, int cols) {
-    constexpr int CH = BN / 8;
+    constexpr int CH = BN / 8, RP = THREADS / CH;
     const buf_rsrc r = make_rsrc(in, (uint32_t)((rows - 1) * (int)stride + cols) * 2u);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int v0 = (int)threadIdx.x / CH, c = ((int)threadIdx.x % CH) ^ (v0 & (CH - 1));
+    const uint32_t off = c * 8 < cols ? (uint32_t)(v0 * (int)stride + c * 8) * 2u : kOOB;
 #pragma unroll
-    for (int k = 0; k < BM * CH / THREADS; ++k) {
-        const int lin = k * THREADS + threadIdx.x;
-        const int v = lin / CH, c = (lin % CH) ^ (v & (CH - 1));
-        dma16(r, smem + (k * THREADS + wave * 64) * 16,
-              v < rows && c * 8 < cols ? (uint32_t)(v * (int)stride + c * 8) * 2u : kOOB, 0u);
-    }
+    for (int k = 0; k < BM / RP; ++k)
+        dma16(r, smem + (k * THREADS + wave * 64) * 16, off + (uint32_t)(k * RP * 2) * (uint32_t)stride, 0u);
 }
 
 // Epilogue of a whole tile: z = acc (the bias is in it), stored when asked
@@ -407,9 +409,13 @@ __device__ __forceinline__ void gemm_store_wave(const GemmParams &p, const f32x1
     if (rows <= 0 || cols <= 0) return;
     const int rrow = lane & 31, rhi = lane >> 5;
     const int vr = lane >> 3, vc = lane & 7;  // row accesses: 8 rows of 8 chunks per instruction
-    auto row_off = [&](int v, int c, int64_t stride, int h) {
-        return v < rows && h * 64 + c * 8 < cols ? (uint32_t)(v * (int)stride + h * 64 + c * 8) * 2u : kOOB;
+    // Byte offset of the lane's chunk c in rows vr, vr + 8, ... of columns
+    // [64 h, 64 h + 64): rows past the matrix lie past the records, a column past
+    // it is out of range itself (and stays so with a multiple of the stride on top).
+    auto first_off = [&](int c, int64_t stride, int h) {
+        return h * 64 + c * 8 < cols ? (uint32_t)(vr * (int)stride + h * 64 + c * 8) * 2u : kOOB;
     };
+    const int key = (vr >> 1) & 3;  // ((8 k + vr) >> 1) & 7 is key, with bit 2 set for odd k
     auto fragments = [&](auto actc, auto resc, int h) {
         constexpr int ACT = decltype(actc)::value;
         constexpr bool RES = decltype(resc)::value;
@@ -433,12 +439,13 @@ __device__ __forceinline__ void gemm_store_wave(const GemmParams &p, const f32x1
     };
     auto rows_out = [&](_Float16 *out, int64_t stride, int h) {
         const buf_rsrc r = make_rsrc(out, (uint32_t)((rows - 1) * (int)stride + cols) * 2u);
+        const uint32_t off = first_off(vc, stride, h);
+        const char *at[2] = {lds + vr * 128 + ((vc ^ key) << 4), lds + vr * 128 + ((vc ^ key ^ 4) << 4)};
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int v = 8 * k + vr;
-            half8_t t = *reinterpret_cast<const half8_t *>(lds + v * 128 + ((vc ^ ((v >> 1) & 7)) << 4));
-            if (k & 2) t = __builtin_shufflevector(t, t, 4, 5, 6, 7, 0, 1, 2, 3);  // v & 16
-            gemm_store16(r, row_off(v, vc, stride, h), t);
+            half8_t t = *reinterpret_cast<const half8_t *>(at[k & 1] + k * 1024);
+            if (k & 2) t = __builtin_shufflevector(t, t, 4, 5, 6, 7, 0, 1, 2, 3);  // row & 16
+            gemm_store16(r, off + (uint32_t)(k * 16) * (uint32_t)stride, t);
         }
     };
 #pragma unroll
@@ -451,11 +458,10 @@ __device__ __forceinline__ void gemm_store_wave(const GemmParams &p, const f32x1
             const buf_rsrc r = make_rsrc(p.res + (int64_t)row0 * p.res_stride + col0,
                                          (uint32_t)((rows - 1) * (int)p.res_stride + cols) * 2u);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the rows before have left the LDS
+            const uint32_t off[2] = {first_off(vc ^ key, p.res_stride, h), first_off(vc ^ key ^ 4, p.res_stride, h)};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int v = 8 * k + vr;
-                dma16(r, lds + k * 1024, row_off(v, vc ^ ((v >> 1) & 7), p.res_stride, h), 0u);
-            }
+            for (int k = 0; k < 8; ++k)
+                dma16(r, lds + k * 1024, off[k & 1] + (uint32_t)(k * 16) * (uint32_t)p.res_stride, 0u);
             gemm_wait_loads<0>();
             act_switch(p.act, [&](auto ac) { fragments(ac, std::true_type{}, h); });
         } else {

@@ -176,8 +176,8 @@ double plan_pair(int64_t m, int n, int k, GemmPlan *dx, GemmPlan *dw) {
             return (double)((per + t.groups - 1) / t.groups);
         };
         auto units = [](const GemmPlan &g) { return (int64_t)g.dp + (int64_t)g.sk * g.pieces; };
-        for (int px = 1; px <= 8; ++px)
-            for (int pw = 1; pw <= c3d::kGemmMaxPieces; ++pw) {
+        for (int px : {1, 2, 3, 4, 6, 8})
+            for (int pw : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
                 const GemmPlan x = even_split(i, t, m, k, n, px), w = even_split(i, t, n, k, m, pw);
                 if ((px > 1 && px * 4 > x.niter) || (pw > 1 && pw * 4 > w.niter)) continue;
                 const size_t bytes = x.partial_bytes + w.partial_bytes;

@@ -122,6 +122,27 @@ def test_infinite_and_nan_rows_stay_in_their_rows(m):
     assert bool(torch.isfinite(y[2:]).all())
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_nan_preactivations_stay_nan(act):
+    m, n, k = 40, 72, 64
+    g = gen(4)
+    dt = torch.float16
+    z, dy, x, w = normal(g, (m, n), dt), normal(g, (m, n), dt), normal(g, (m, k), dt), normal(g, (n, k), dt)
+    z[3, 5] = float("nan")
+    plan = c3d.linear_plan(c3d.make_linear_desc(m, n, k, ACTS[act]))
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty((n,), dtype=dt, device="cuda:0")
+    c3d.linear_backward(plan, dy, x, w, z, dx, dw, db, scratch(c3d.linear_backward_workspace(plan)))
+    torch.cuda.synchronize()
+    assert torch.isnan(dx).nonzero()[:, 0].unique().tolist() == [3] and bool(torch.isnan(dx[3]).all())
+    assert torch.isnan(dw).nonzero()[:, 0].unique().tolist() == [5] and bool(torch.isnan(dw[5]).all())
+    assert torch.isnan(db).nonzero().flatten().tolist() == [5]
+    x[2, 0] = float("nan")
+    y = torch.empty((m, n), dtype=dt, device="cuda:0")
+    c3d.linear_forward(plan, x, w, None, None, y, None, scratch(plan.workspace_bytes))
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(y[2]).all()) and not bool(torch.isnan(y[:2]).any()) and not bool(torch.isnan(y[3:]).any())
+
+
 def test_large_preactivations_saturate():
     # silu and the gelus tend to z and to 0; their derivatives to 1 and 0
     vals = torch.tensor([3e4, -3e4, 65504.0, -65504.0, 200.0, -200.0, 12.0, -12.0], device="cuda:0")
