@@ -46,12 +46,12 @@ __device__ __forceinline__ float act_f(float z) {
     if constexpr (ACT == CONV3D_ACT_GELU_TANH) return z * sigmoid_2u(z);
     return z;
 }
-// The arguments whose powers could overflow are bounded where the derivative is
-// 0 or 1 to the last bit anyway.
+// (Finite z of any size: the exponentials reach 0 or infinity before a product
+// with z overflows, except for the tanh form's z^2, whose z is bounded where the
+// derivative is 0 or 1 to the last bit.  A NaN comes through.)
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == CONV3D_ACT_NONE) return 1.0f;
-    z = z > 1e4f ? 1e4f : z < -1e4f ? -1e4f : z;  // a NaN stays one
     if constexpr (ACT == CONV3D_ACT_SILU) {
         const float s = sigmoid_f(z);
         return s * fmaf(z, 1.0f - s, 1.0f);
@@ -62,7 +62,12 @@ __device__ __forceinline__ float act_slope(float z) {
         return fmaf(z * 0.398942280401432678f, ex, z < 0.0f ? tail : 1.0f - tail);
     }
     const float s = sigmoid_2u(z);
-    return s * fmaf(z * (1.0f - s), fmaf(6.0f * kGeluA * kGeluB * z, z, 2.0f * kGeluA), 1.0f);
+#if defined(__HIP_DEVICE_COMPILE__)
+    const float b = __builtin_amdgcn_fmed3f(z, -1e4f, 1e4f);
+#else
+    const float b = z;
+#endif
+    return s * fmaf(b * (1.0f - s), fmaf(6.0f * kGeluA * kGeluB * b, b, 2.0f * kGeluA), 1.0f);
 }
 
 // Calls f(std::integral_constant<int, ACT>) for the activation chosen at run time.
