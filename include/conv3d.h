@@ -290,7 +290,9 @@ conv3d_status groupnorm_silu_noalloc(const void *x, const void *gamma, const voi
  * rows, a multiple of 8, 0 for contiguous rows; at most 2^20).  Sizes of zero
  * rows are valid: such a call enqueues nothing but the zeros of weight
  * gradients.  Like every entry point, they take the caller's stream, allocate
- * nothing and can be captured in a HIP graph.
+ * nothing and can be captured in a HIP graph.  Where a call's tensors must not
+ * overlap, a tensor counts as everything from its first element to its last, the
+ * gaps between its rows included.
  */
 
 /* Activations of linear.  GELU is z * Phi(z) with the normal distribution's
