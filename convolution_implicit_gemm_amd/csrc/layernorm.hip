@@ -23,10 +23,24 @@ namespace {
 
 constexpr int64_t kLnWideRows = 512;
 
+// Sum over the wave, the same in every lane: shifted adds within rows of 16
+// lanes, then the rows' last lanes into the next rows, all in vector
+// registers (a shuffle through LDS per step doubles a small row's latency).
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+#if defined(__HIP_DEVICE_COMPILE__)
+#define C3D_DPP_ADD(ctrl, rows)                                                                                    \
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, rows, 0xf, false))
+    C3D_DPP_ADD(0x111, 0xf);  // row_shr:1
+    C3D_DPP_ADD(0x112, 0xf);  // row_shr:2
+    C3D_DPP_ADD(0x114, 0xf);  // row_shr:4
+    C3D_DPP_ADD(0x118, 0xf);  // row_shr:8: lane 15 of each row holds the row's sum
+    C3D_DPP_ADD(0x142, 0xa);  // row_bcast:15 into rows 1 and 3
+    C3D_DPP_ADD(0x143, 0xc);  // row_bcast:31 into rows 2 and 3: lane 63 holds the sum
+#undef C3D_DPP_ADD
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+#else
     return v;
+#endif
 }
 
 // Sum over the WPR waves of a row's team.  slot: this team's 2 x WPR floats of
