@@ -15,6 +15,10 @@
 // columns' sums in registers, the block adds its teams through LDS and writes
 // one fp32 partial, and a second kernel adds the blocks in a fixed order (no
 // atomics: the result does not depend on the order blocks finish in).
+//
+// Measured, bf16: 36864 x 2048 forward 54-57 us, 5.3-5.6 TB/s (a copy runs at 5.0);
+// its gradient with a residual's 120 us, 5.0 TB/s.  Few rows are bound by latency: 1
+// x 1024 2.4 us, the gradient of 1543 x 1032 11 us in two launches.
 #include "column_sum.h"
 
 namespace c3d {
@@ -269,7 +273,8 @@ hipError_t ln_dispatch(int c, bool wide, F &&f) {
     return f(integral_constant<int, 2>{}, integral_constant<int, 16>{});
 }
 
-// Few rows: a row's latency counts, not the stream's rate.
+// Few rows: a row's latency counts, not the stream's rate.  (200 x 1032: forward
+// 3.9 -> 3.2 us, gradient 9.6 -> 7.0; 36864 x 1024: gradient 44 -> 85 us.)
 bool ln_wide(int64_t rows) { return rows <= kLnWideRows; }
 int ln_teams(int64_t rows, int c) { return c <= (ln_wide(rows) ? 512 : 2048) ? 4 : 1; }
 

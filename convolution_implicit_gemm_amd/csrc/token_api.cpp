@@ -64,6 +64,16 @@ double rounds_us(const c3d::GemmTile &t, c3d::GemmLayout layout, int64_t units, 
     return us;
 }
 
+// The kernel of few rows: every workgroup streams its 16 columns of w at what one
+// CU draws, 32 bytes per nanosecond, less for the rows of x read beside them
+// (measured over n and k from 256 to 16384, m = 1, 4, 16), and all of them at
+// 6.4 TB/s.
+double rows_us(int64_t m, int n, int64_t k) {
+    const double rounds = n > 16 * kCUs ? n / (16.0 * kCUs) : 1.0;
+    const double draw = rounds * (double)k * 1e-3 * (1.0 + 0.041 * m), stream = 2.0 * n * k / 6.4e6;
+    return 2.3 + (draw > stream ? draw : stream);
+}
+
 // CONV3D_LINEAR_TILE: a kernel's name, or its name + "+pair", which also makes
 // a backward pass run dx and dw in one launch of it.
 struct Forced {
@@ -88,15 +98,19 @@ GemmPlan plan_gemm(int64_t m, int n, int64_t k, c3d::GemmLayout layout, double *
     const Forced force;
     GemmPlan best;
     double best_s = -1.0;
-    const bool rows_ok = layout == c3d::kGemmForward && m <= c3d::kGemmRowsMax;
-    *us = 0.0;
-    if (rows_ok && (!force.v || force.is(tiles[c3d::kGemmRowsTile].name))) {
+    if (layout == c3d::kGemmForward && m <= c3d::kGemmRowsMax &&
+        (!force.v || force.is(tiles[c3d::kGemmRowsTile].name))) {
         best.tile = c3d::kGemmRowsTile;
         best.m_tiles = 1;
         best.n_tiles = best.dp = (n + 15) / 16;
-        return best;
+        best_s = rows_us(m, n, k);
+        if (force.v) {
+            *us = best_s;
+            return best;
+        }
     }
-    for (int pass = force.v ? 0 : 1; pass < 2 && best_s < 0.0; ++pass)
+    bool found = false;
+    for (int pass = force.v ? 0 : 1; pass < 2 && !found; ++pass)
         for (int i = 0; i < count; ++i) {
             const c3d::GemmTile &t = tiles[i];
             if (i == c3d::kGemmRowsTile) continue;
@@ -127,6 +141,10 @@ GemmPlan plan_gemm(int64_t m, int n, int64_t k, c3d::GemmLayout layout, double *
                     pick.partial_bytes = bytes;
                 }
             }
+            found = true;
+            // both operands and the output once, as fast as the tiles stream them
+            const double stream = 2.0 + 2.0 * ((double)m * k + (double)n * k + (double)m * n) / 6.0e6;
+            if (sec < stream) sec = stream;
             if (best_s < 0.0 || sec < best_s) {
                 best_s = sec;
                 best = pick;
@@ -292,6 +310,11 @@ conv3d_status linear_plan(const linear_desc *d, linear_plan_t *out, size_t *work
         p->fwd = plan_gemm(d->m, d->n, d->k, c3d::kGemmForward, &us_f);
         p->dx = plan_gemm(d->m, d->k, d->n, c3d::kGemmDx, &us_x);
         p->dw = plan_gemm(d->n, d->k, d->m, c3d::kGemmDw, &us_w);
+        for (const GemmPlan *g : {&p->fwd, &p->dx, &p->dw})
+            if (g->dp + g->sk == 0) {
+                delete p;
+                return api_fail(CONV3D_ERR_UNSUPPORTED, "the product has too many tiles");
+            }
         const Forced force;
         const double us_pair = plan_pair(d->m, d->n, d->k, &p->pair_dx, &p->pair_dw);
         // one launch less, and neither product's tail leaves the card idle
