@@ -552,18 +552,21 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradParams p, int grou
     }
 }
 
-// Times, in microseconds: of one step (a stage of 64 per group of waves) with
-// few workgroups on the card, for each layout; of one with per_cu workgroups on
-// every CU; and of what a workgroup adds before and after its steps.  Measured
-// over sizes from 200 x 704 x 704 to 8192^3.  (Four groups of waves look one
-// step ahead only: enough for operands in L2, not for the long streams of dw.)
+// The cost model, in microseconds and for each layout: a step (a stage of 64 per
+// group of waves) with few workgroups on the card and operands in L2, a step with
+// per_cu workgroups on every CU, the share that operands outside the L2s add to
+// the first, what the launch costs, and what each round of workgroups adds
+// before and after its steps.  Fitted to the times of 4500 products of 300 random
+// sizes (1..36864 rows, 64..8192 columns) with each kernel in turn: within 10%
+// rms, and on 150 other sizes the kernel it picks takes 1.1% longer than the
+// fastest on average, 10% at the 95th percentile.
 const GemmTile kTiles[] = {
-    {"m256n256k64", 256, 256, kGemmBK, 512, 1, 1, {1.48, 1.48, 1.48}, 1.48, 5.5},
-    {"m128n128k64", 128, 128, kGemmBK, 256, 2, 1, {0.66, 0.7, 0.66}, 0.96, 2.5},
-    {"m64n64k64", 64, 64, kGemmBK, 256, 2, 1, {0.26, 0.3, 0.3}, 0.4, 2.5},
-    {"m64n64k64g4", 64, 64, kGemmBK, 1024, 1, 4, {0.42, 0.9, 1.3}, 0.88, 4.3},
-    {"m128n128k64g2", 128, 128, kGemmBK, 512, 1, 2, {0.7, 0.75, 0.8}, 0.95, 3.0},
-    {"m16n16k32", 16, 16, 32, kRowsWaves * 64, 4, 1, {0.0, 0.0, 0.0}, 0.0, 0.0},  // few rows: rows_us
+    {"m256n256k64", 256, 256, kGemmBK, 512, 1, 1, {0.53, 0.61, 0.77}, {1.59, 1.62, 1.30}, 1.0, 0.0, 6.9},
+    {"m128n128k64", 128, 128, kGemmBK, 256, 2, 1, {0.41, 0.47, 0.52}, {1.27, 1.16, 1.19}, 0.65, 1.5, 2.8},
+    {"m64n64k64", 64, 64, kGemmBK, 256, 2, 1, {0.16, 0.21, 0.23}, {0.47, 0.49, 0.56}, 1.2, 2.1, 1.7},
+    {"m64n64k64g4", 64, 64, kGemmBK, 1024, 1, 4, {0.49, 0.54, 0.69}, {1.05, 1.21, 1.31}, 0.95, 2.3, 2.3},
+    {"m128n128k64g2", 128, 128, kGemmBK, 512, 1, 2, {0.69, 0.80, 0.84}, {1.34, 1.30, 1.24}, 0.33, 1.7, 3.4},
+    {"m16n16k32", 16, 16, 32, kRowsWaves * 64, 4, 1, {}, {}, 0.0, 0.0, 0.0},  // few rows: rows_us
 };
 
 unsigned units_of(const GemmParams &p) { return (unsigned)(p.dp_tiles + p.sk_tiles * p.sk_pieces); }

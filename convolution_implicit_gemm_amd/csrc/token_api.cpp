@@ -46,23 +46,38 @@ struct GemmPlan {
 
 constexpr double kJoinBytesPerUs = 9e6;
 constexpr double kJoinLaunchUs = 4.5;
-constexpr double kPairGain = 1.1;  // what sharing the card gains beyond plan_pair's times
+// One launch of dx and dw is taken up to this much above the sum of their own
+// best estimates, which are the more optimistic ones: over 300 sizes the slower
+// way is then taken at a mean loss of 0.6%, at 1.0 of 1.8%.
+constexpr double kPairMargin = 1.2;
+constexpr double kL2Bytes = 32e6;  // all eight
 constexpr size_t kMaxPartial = (size_t)256 << 20;
 
-// Time of `units` workgroups of `steps` steps each: rounds of as many as fit
-// the card.  The steps of a partial round are as much faster as it is smaller
-// (L2 serves the operands of all of them), down to the time of a few.
-double rounds_us(const c3d::GemmTile &t, c3d::GemmLayout layout, int64_t units, double steps) {
-    const int64_t slots = (int64_t)kCUs * t.per_cu;
-    const int64_t full = units / slots, rem = units % slots;
-    double us = full * (steps * t.step_us_full + t.fixed_us);
-    if (rem) {
-        double step = t.step_us_full * rem / slots;
-        if (step < t.step_us_few[layout]) step = t.step_us_few[layout];
-        us += steps * step + t.fixed_us;
+// What steps of a product cost in a tile's kernel.  `missed` is how much of its
+// operands the L2s (4 MB on each of the 8 dies) cannot hold.
+struct TileCost {
+    const c3d::GemmTile &t;
+    double few, full;
+    int64_t slots;
+    TileCost(const c3d::GemmTile &tile, c3d::GemmLayout l, double operand_bytes) : t(tile) {
+        full = t.step_us_full[l];
+        slots = (int64_t)kCUs * t.per_cu;
+        const double missed = operand_bytes < kL2Bytes ? operand_bytes / kL2Bytes : 1.0;
+        few = t.step_us_few[l] * (1.0 + t.cold * missed);
+        if (few > full) few = full;
     }
-    return us;
-}
+    // Steps of a card with `units` workgroups on it: as much faster as they are
+    // fewer (the L2s serve the operands of all of them), down to the time of a few.
+    double step(int64_t units) const {
+        const double s = units < slots ? full * units / slots : full;
+        return s > few ? s : few;
+    }
+    // `units` workgroups of `steps` steps each: rounds of as many as fit the card.
+    double rounds(int64_t units, double steps) const {
+        const int64_t rem = units % slots;
+        return units / slots * (steps * full + t.round_us) + (rem ? steps * step(rem) + t.round_us : 0.0);
+    }
+};
 
 // The kernel of few rows: every workgroup streams its 16 columns of w at what one
 // CU draws, 32 bytes per nanosecond, less for the rows of x read beside them
@@ -125,14 +140,15 @@ GemmPlan plan_gemm(int64_t m, int n, int64_t k, c3d::GemmLayout layout, double *
             if (!runnable(i, t, all)) continue;
             g.dp = (int)all;
             auto steps = [&](int pieces) { return (double)(((g.niter + pieces - 1) / pieces + t.groups - 1) / t.groups); };
-            double sec = rounds_us(t, layout, all, steps(1));
+            const TileCost cost(t, layout, 2.0 * ((double)m * k + (double)n * k));
+            double sec = t.launch_us + cost.rounds(all, steps(1));
             const int64_t full = all / slots, rem = all % slots;
             GemmPlan pick = g;
             for (int pc = 2; rem && pc <= c3d::kGemmMaxPieces && pc * 4 <= g.niter; ++pc) {
                 const size_t bytes = (size_t)rem * pc * t.bm * t.bn * 4;
                 if (bytes > kMaxPartial) break;
-                const double s2 = rounds_us(t, layout, full * slots, steps(1)) + rounds_us(t, layout, rem * pc, steps(pc)) +
-                                  2.0 * bytes / kJoinBytesPerUs + kJoinLaunchUs;
+                const double s2 = t.launch_us + cost.rounds(full * slots, steps(1)) +
+                                  cost.rounds(rem * pc, steps(pc)) + 2.0 * bytes / kJoinBytesPerUs + kJoinLaunchUs;
                 if (s2 < sec * 0.97) {
                     sec = s2;
                     pick.dp = (int)(full * slots);
@@ -175,7 +191,8 @@ GemmPlan even_split(int tile, const c3d::GemmTile &t, int64_t m, int n, int64_t 
 // dx and dw in one launch, sharing the card: the tile and the pieces of each
 // with the least time, and that time.  Units that fit the card at once take as
 // long as the longest, at the rate of all of them; more take the sum of their
-// steps at the full card's rate.
+// steps at the full card's rate and a part of the longest, when the card drains.
+// (Fitted with the tiles' rates: within 10% rms of 900 pairs' times.)
 double plan_pair(int64_t m, int n, int k, GemmPlan *dx, GemmPlan *dw) {
     int count = 0;
     const c3d::GemmTile *tiles = c3d::gemm_tiles(&count);
@@ -188,7 +205,9 @@ double plan_pair(int64_t m, int n, int k, GemmPlan *dx, GemmPlan *dw) {
             return ((rows + t.bm - 1) / t.bm) * ((cols + t.bn - 1) / t.bn);
         };
         if (!runnable(i, t, (tiles_of(m, k) + tiles_of(n, k)) * 2)) continue;
-        const int64_t slots = (int64_t)kCUs * t.per_cu;
+        const double operands = 2.0 * ((double)m * k + (double)n * k + (double)m * n);
+        const TileCost cost_x(t, c3d::kGemmDx, operands), cost_w(t, c3d::kGemmDw, operands);
+        const int64_t slots = cost_x.slots;
         auto steps = [&](const GemmPlan &g) {
             const int per = g.pieces ? (g.niter + g.pieces - 1) / g.pieces : g.niter;
             return (double)((per + t.groups - 1) / t.groups);
@@ -201,16 +220,12 @@ double plan_pair(int64_t m, int n, int k, GemmPlan *dx, GemmPlan *dw) {
                 const size_t bytes = x.partial_bytes + w.partial_bytes;
                 if (bytes > kMaxPartial) continue;
                 const int64_t all = units(x) + units(w);
-                auto time_of = [&](const GemmPlan &g, c3d::GemmLayout l) {
-                    double step = t.step_us_full * all / slots;
-                    if (step > t.step_us_full) step = t.step_us_full;
-                    if (step < t.step_us_few[l]) step = t.step_us_few[l];
-                    return steps(g) * step + t.fixed_us;
-                };
-                const double tx = time_of(x, c3d::kGemmDx), tw = time_of(w, c3d::kGemmDw);
+                const double tx = steps(x) * cost_x.step(all) + t.round_us;
+                const double tw = steps(w) * cost_w.step(all) + t.round_us;
                 double us = tx > tw ? tx : tw;
                 const double sum = (units(x) * tx + units(w) * tw) / slots;
-                if (all > slots) us = sum + 0.5 * us;
+                if (all > slots) us = sum + 0.3 * us;
+                us += t.launch_us;
                 if (bytes) us += 2.0 * bytes / kJoinBytesPerUs + kJoinLaunchUs;
                 if (best < 0.0 || us < best) {
                     best = us;
@@ -319,7 +334,7 @@ conv3d_status linear_plan(const linear_desc *d, linear_plan_t *out, size_t *work
         const double us_pair = plan_pair(d->m, d->n, d->k, &p->pair_dx, &p->pair_dw);
         // one launch less, and neither product's tail leaves the card idle
         p->pair = us_pair >= 0.0 &&
-                  (force.v ? force.pair() : us_pair < kPairGain * (us_x + us_w) + kJoinLaunchUs);
+                  (force.v ? force.pair() : us_pair < kPairMargin * (us_x + us_w));
         const size_t dz = d->act != CONV3D_ACT_NONE ? align256((size_t)d->m * d->n * 2) : 0;
         size_t part = p->dx.partial_bytes > p->dw.partial_bytes ? p->dx.partial_bytes : p->dw.partial_bytes;
         const size_t both = p->pair ? p->pair_dx.partial_bytes + p->pair_dw.partial_bytes : 0;

@@ -45,7 +45,7 @@ struct GemmTile {
     int bm, bn, bk, threads;
     int per_cu;    // workgroups that share a CU
     int groups;    // groups of waves that take the stages in turn
-    double step_us_few[3], step_us_full, fixed_us;  // cost model (linear.hip)
+    double step_us_few[3], step_us_full[3], cold, launch_us, round_us;  // cost model (linear.hip)
 };
 constexpr int kGemmCUs = 256;
 constexpr int kGemmMaxPieces = 32;
