@@ -201,7 +201,8 @@ __device__ __forceinline__ void tr_read4(const uint32_t (&a)[4], uint64_t (&v)[1
                  : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]),
                    "=&v"(v[7]), "=&v"(v[8]), "=&v"(v[9]), "=&v"(v[10]), "=&v"(v[11]), "=&v"(v[12]), "=&v"(v[13]),
                    "=&v"(v[14]), "=&v"(v[15])
-                 : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(K0 * ROW), "n"((K0 + 4) * ROW), "n"((K0 + 16) * ROW), "n"((K0 + 20) * ROW)
+                 : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(K0 * ROW), "n"((K0 + 4) * ROW),
+                   "n"((K0 + 16) * ROW), "n"((K0 + 20) * ROW)
                  : "memory");
 #endif
 }
@@ -362,7 +363,8 @@ __device__ __forceinline__ void gemm_store_tile(const GemmParams &p, const f32x1
                     if constexpr (RES) {
                         const half4_t r = *reinterpret_cast<const half4_t *>(chunk + rhi * 8);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) h[e] = from_f32<E>(act_f<ACT>(acc[i][j][4 * g + e]) + to_f32<E>(r[e]));
+                        for (int e = 0; e < 4; ++e)
+                            h[e] = from_f32<E>(act_f<ACT>(acc[i][j][4 * g + e]) + to_f32<E>(r[e]));
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) h[e] = from_f32<E>(act_f<ACT>(acc[i][j][4 * g + e]));
@@ -389,7 +391,8 @@ __device__ __forceinline__ void gemm_store_tile(const GemmParams &p, const f32x1
 
 // The bias of a lane's columns: element 4g + e of [i] is column col0 + 32 i + 8 g + 4 (lane / 32) + e.
 template <int TN>
-__device__ __forceinline__ void gemm_load_bias(const GemmParams &p, half4_t (&b)[TN][4], bool bias, int col0, int lane) {
+__device__ __forceinline__ void gemm_load_bias(const GemmParams &p, half4_t (&b)[TN][4], bool bias, int col0,
+                                               int lane) {
     const buf_rsrc rb = make_rsrc(bias ? p.bias : p.p, bias ? (uint32_t)p.N * 2u : 0u);
 #pragma unroll
     for (int i = 0; i < TN; ++i)

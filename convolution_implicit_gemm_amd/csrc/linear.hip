@@ -582,11 +582,12 @@ hipError_t launch_join(const GemmParams &p, const GemmParams *p2, int tile, hipS
     if (jx + jw == 0) return hipSuccess;
     const GemmParams &q = p2 ? *p2 : p;
     const dim3 grid(jx + jw);
+    const auto go = [&](auto *kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, p, q, (int)jx); };
     switch (tile) {
-        case 0: hipLaunchKernelGGL((gemm_join_kernel<E, 256, 256, 64, 128>), grid, dim3(256), 0, s, p, q, (int)jx); break;
+        case 0: go(gemm_join_kernel<E, 256, 256, 64, 128>); break;
         case 1:
-        case 4: hipLaunchKernelGGL((gemm_join_kernel<E, 128, 128, 64, 64>), grid, dim3(256), 0, s, p, q, (int)jx); break;
-        default: hipLaunchKernelGGL((gemm_join_kernel<E, 64, 64, 32, 32>), grid, dim3(256), 0, s, p, q, (int)jx); break;
+        case 4: go(gemm_join_kernel<E, 128, 128, 64, 64>); break;
+        default: go(gemm_join_kernel<E, 64, 64, 32, 32>); break;
     }
     return hipGetLastError();
 }

@@ -139,7 +139,9 @@ GemmPlan plan_gemm(int64_t m, int n, int64_t k, c3d::GemmLayout layout, double *
             const int64_t slots = (int64_t)kCUs * t.per_cu;
             if (!runnable(i, t, all)) continue;
             g.dp = (int)all;
-            auto steps = [&](int pieces) { return (double)(((g.niter + pieces - 1) / pieces + t.groups - 1) / t.groups); };
+            auto steps = [&](int pieces) {
+                return (double)(((g.niter + pieces - 1) / pieces + t.groups - 1) / t.groups);
+            };
             const TileCost cost(t, layout, 2.0 * ((double)m * k + (double)n * k));
             double sec = t.launch_us + cost.rounds(all, steps(1));
             const int64_t full = all / slots, rem = all % slots;
