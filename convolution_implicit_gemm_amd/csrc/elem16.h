@@ -47,4 +47,11 @@ __device__ __forceinline__ e32x16_t mfma_32x32x16(e16x8_t a, e16x8_t b, e32x16_t
 #endif
 }
 
+// Workgroups are dealt to the XCDs in turn; XCD x takes the x-th contiguous
+// range of the units [first, first + count).
+__device__ __forceinline__ int xcd_range(int b, int count) {
+    const int per = count >> 3, rem = count & 7, x = b & 7;
+    return x * per + (x < rem ? x : rem) + (b >> 3);
+}
+
 }  // namespace c3d

@@ -541,11 +541,5 @@ __device__ __forceinline__ void gemm_unit(const GemmParams &p, int u, int &m_til
     m_tile = g0 + r % rows;
     n_tile = r / rows;
 }
-// Workgroups are dealt to the XCDs in turn; XCD x takes the x-th contiguous
-// range of the units [first, first + count).
-__device__ __forceinline__ int xcd_range(int b, int count) {
-    const int per = count >> 3, rem = count & 7, x = b & 7;
-    return x * per + (x < rem ? x : rem) + (b >> 3);
-}
 
 }  // namespace c3d

@@ -14,18 +14,21 @@
 // The weights' gradients: every team walks rows blockwise and keeps its
 // columns' sums in registers, the block adds its teams through LDS and writes
 // one fp32 partial, and a second kernel adds the blocks in a fixed order (no
-// atomics: the result does not depend on the order blocks finish in).
+// atomics: the result does not depend on the order blocks finish in).  Up to
+// 2048 rows other blocks of the same launch take 16 columns each and walk all
+// rows, whose statistics are known, instead: dy and x are read twice, from L2,
+// but nothing has to be joined.
 //
 // Measured, bf16: 36864 x 2048 forward 54-57 us, 5.3-5.6 TB/s (a copy runs at 5.0);
 // its gradient with a residual's 120 us, 5.0 TB/s.  Few rows are bound by latency: 1
-// x 1024 2.4 us, the gradient of 1543 x 1032 11 us in two launches.
+// x 1024 2.4 us, the gradients of 1543 x 1032 5.1 us.
 #include "column_sum.h"
 
 namespace c3d {
 
 namespace {
 
-constexpr int64_t kLnWideRows = 512;
+constexpr int64_t kLnWideRows = 512, kLnColumnRows = 2048;
 
 // Sum over the wave, the same in every lane: shifted adds within rows of 16
 // lanes, then the rows' last lanes into the next rows, all in vector
@@ -127,19 +130,20 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_kernel(LnParams p
     }
 }
 
-template <typename E, int NV, int WPR>
-__global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGradParams p) {
+// dx of the rows that workgroup `block` of `blocks` walks and, with SUMS, its
+// partial of the weights' gradients.
+template <typename E, int NV, int WPR, bool SUMS>
+__device__ __forceinline__ void ln_grad_rows(const LnGradParams &p, int block, int blocks, float *join) {
     constexpr int TEAMS = ln_threads<WPR>() / 64 / WPR;
     constexpr int SPAN = NV * WPR * 512;  // columns a team covers
     __shared__ float red[TEAMS * 2 * WPR];
-    __shared__ __attribute__((aligned(16))) float join[TEAMS > 1 ? TEAMS * SPAN : 4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int team = wave / WPR, wt = wave % WPR;
     const int first = (wt * 64 + lane) * 8;
     float *slot = red + team * 2 * WPR;
     const float inv_c = 1.0f / (float)p.c;
     e16x8_t ga[NV];
-    float dg[NV][8], db[NV][8];
+    float dg[SUMS ? NV : 1][8], db[SUMS ? NV : 1][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = first + i * WPR * 512;
@@ -147,7 +151,7 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGra
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (!p.gamma) ga[i][e] = from_f32<E>(1.0f);
-            dg[i][e] = db[i][e] = 0.0f;
+            if constexpr (SUMS) dg[i][e] = db[i][e] = 0.0f;
         }
     }
     // The next row's loads are issued before the current row is worked on (a
@@ -157,7 +161,7 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGra
         e16x8_t x[NV], dy[NV], dres[NV];
         float2 st;
     };
-    const int64_t step = (int64_t)gridDim.x * TEAMS;
+    const int64_t step = (int64_t)blocks * TEAMS;
     auto fetch = [&](int64_t row, Row &r) {
         const bool live = row < p.rows;
         r.st = live ? p.stats[row] : make_float2(0.0f, 0.0f);
@@ -171,8 +175,8 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGra
         }
     };
     Row cur, next;
-    int64_t row = (int64_t)blockIdx.x * TEAMS + team;
-    const int64_t rounds = (p.rows - (int64_t)blockIdx.x * TEAMS + step - 1) / step;  // the same for all teams
+    int64_t row = (int64_t)block * TEAMS + team;
+    const int64_t rounds = (p.rows - (int64_t)block * TEAMS + step - 1) / step;  // the same for all teams
     if (AHEAD) fetch(row, cur);
     for (int64_t k = 0; k < rounds; ++k, row += step) {
         if (!AHEAD)
@@ -191,8 +195,10 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGra
                     const float g = d * to_f32<E>(ga[i][e]);
                     s1 += g;
                     s2 = fmaf(g, xh, s2);
-                    dg[i][e] = fmaf(d, xh, dg[i][e]);
-                    db[i][e] += d;
+                    if constexpr (SUMS) {
+                        dg[i][e] = fmaf(d, xh, dg[i][e]);
+                        db[i][e] += d;
+                    }
                 }
         s1 = team_sum<WPR>(s1, slot, wt, 0) * inv_c;
         s2 = team_sum<WPR>(s2, slot, wt, 1) * inv_c;
@@ -212,39 +218,104 @@ __global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGra
             }
         if (AHEAD) cur = next;
     }
-    if (!p.part) return;
-    float *out = p.part + (int64_t)blockIdx.x * 2 * p.c;
-    auto put = [&](float *to, const float (&v)[8]) {
-        *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    };
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = first + i * WPR * 512;
-            if constexpr (TEAMS > 1)
-                put(join + team * SPAN + c, which ? db[i] : dg[i]);
-            else if (c < p.c)
-                put(out + which * p.c + c, which ? db[i] : dg[i]);
-        }
-        if constexpr (TEAMS > 1) {  // add the teams in turn
-            __syncthreads();
-            for (int c = threadIdx.x * 4; c < p.c; c += ln_threads<WPR>() * 4) {
-                float4 t = *reinterpret_cast<const float4 *>(join + c);
-#pragma unroll
-                for (int k = 1; k < TEAMS; ++k) {
-                    const float4 u = *reinterpret_cast<const float4 *>(join + k * SPAN + c);
-                    t.x += u.x;
-                    t.y += u.y;
-                    t.z += u.z;
-                    t.w += u.w;
-                }
-                *reinterpret_cast<float4 *>(out + which * p.c + c) = t;
+    if constexpr (SUMS) {
+        float *out = p.part + (int64_t)block * 2 * p.c;
+        auto put = [&](float *to, const float (&v)[8]) {
+            *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        };
+    #pragma unroll
+        for (int which = 0; which < 2; ++which) {
+    #pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = first + i * WPR * 512;
+                if constexpr (TEAMS > 1)
+                    put(join + team * SPAN + c, which ? db[i] : dg[i]);
+                else if (c < p.c)
+                    put(out + which * p.c + c, which ? db[i] : dg[i]);
             }
-            __syncthreads();
+            if constexpr (TEAMS > 1) {  // add the teams in turn
+                __syncthreads();
+                for (int c = threadIdx.x * 4; c < p.c; c += ln_threads<WPR>() * 4) {
+                    float4 t = *reinterpret_cast<const float4 *>(join + c);
+    #pragma unroll
+                    for (int k = 1; k < TEAMS; ++k) {
+                        const float4 u = *reinterpret_cast<const float4 *>(join + k * SPAN + c);
+                        t.x += u.x;
+                        t.y += u.y;
+                        t.z += u.z;
+                        t.w += u.w;
+                    }
+                    *reinterpret_cast<float4 *>(out + which * p.c + c) = t;
+                }
+                __syncthreads();
+            }
         }
     }
+}
+
+// dgamma and dbeta of 16 columns, straight from dy, x and the rows' statistics:
+// two threads per row, THREADS / 2 rows at once, their sums through LDS in a
+// fixed order.  Bound by the latency of a thread's rows.  The column blocks that
+// share cache lines run on one XCD (dealt out in turn: 1543 x 1032 8.1 us, so
+// 5.1); 8 or 32 columns, or 8 rows ahead instead of 4, are within 20% either way.
+constexpr int kLnCols = 16;
+constexpr int ln_cols_lds(int threads) { return threads * 8 / kLnCols * (2 * kLnCols + 1); }
+template <typename E, int THREADS>
+__device__ __forceinline__ void ln_grad_cols(const LnGradParams &p, int block, float *lds) {
+    constexpr int PER_ROW = kLnCols / 8, ROWS = THREADS / PER_ROW, OUT = 2 * kLnCols, PARTS = THREADS / OUT;
+    const int tc = threadIdx.x % PER_ROW, tr = threadIdx.x / PER_ROW;
+    const int c = block * kLnCols + tc * 8;
+    float dg[8] = {}, db[8] = {};
+    if (c < p.c)
+#pragma unroll 4
+        for (int64_t r = tr; r < p.rows; r += ROWS) {
+            const float2 st = p.stats[r];
+            const e16x8_t x = load_vec<E>(p.x + r * p.x_stride + c), dy = load_vec<E>(p.dy + r * p.y_stride + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = to_f32<E>(dy[e]);
+                dg[e] = fmaf(d, (to_f32<E>(x[e]) - st.x) * st.y, dg[e]);
+                db[e] += d;
+            }
+        }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        lds[tr * (OUT + 1) + tc * 8 + e] = dg[e];
+        lds[tr * (OUT + 1) + kLnCols + tc * 8 + e] = db[e];
+    }
+    __syncthreads();
+    const int o = threadIdx.x % OUT, part = threadIdx.x / OUT;
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < ROWS / PARTS; ++i) t += lds[(part * (ROWS / PARTS) + i) * (OUT + 1) + o];
+    __syncthreads();
+    lds[part * OUT + o] = t;
+    __syncthreads();
+    if (part) return;
+#pragma unroll
+    for (int i = 1; i < PARTS; ++i) t += lds[i * OUT + o];
+    const int oc = block * kLnCols + o % kLnCols;
+    _Float16 *out = o < kLnCols ? p.dgamma : p.dbeta;
+    if (out && oc < p.c) out[oc] = from_f32<E>(t);
+}
+
+template <typename E, int NV, int WPR>
+__global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_kernel(LnGradParams p) {
+    constexpr int TEAMS = ln_threads<WPR>() / 64 / WPR;
+    __shared__ __attribute__((aligned(16))) float join[TEAMS > 1 ? TEAMS * NV * WPR * 512 : 4];
+    ln_grad_rows<E, NV, WPR, true>(p, blockIdx.x, gridDim.x, join);
+}
+
+// Blocks [0, col_blocks) own columns of the weights' gradients, the others rows of dx.
+template <typename E, int NV, int WPR>
+__global__ __launch_bounds__(ln_threads<WPR>()) void layernorm_grad_split_kernel(LnGradParams p, int col_blocks) {
+    __shared__ float lds[ln_cols_lds(ln_threads<WPR>())];
+    const int b = blockIdx.x;
+    if (b < col_blocks)
+        ln_grad_cols<E, ln_threads<WPR>()>(p, xcd_range(b, col_blocks), lds);
+    else
+        ln_grad_rows<E, NV, WPR, false>(p, b - col_blocks, gridDim.x - col_blocks, nullptr);
 }
 
 template <typename E>
@@ -304,17 +375,39 @@ int32_t ln_grad_blocks(int64_t rows, int32_t c) {
 }
 
 hipError_t launch_layernorm_grad(const LnGradParams &p, hipStream_t s) {
+    const bool wide = ln_wide(p.rows);
+    // One launch for few rows (all gradients, bf16: 1 x 1024 4.6 -> 2.6 us, 613 x 2048
+    // 9.8 -> 5.0, 1543 x 1032 9.8 -> 5.1, 2000 x 1024 9.8 -> 6.6, 2000 x 8192 40 -> 28;
+    // 3000 x 2048 14.7 -> 15.7, 4097 x 1024 13.0 -> 16.3) and for dx alone (36864 x 2048
+    // 92 -> 78).  dx in place of dy or x would change what the columns' blocks read.
+    const bool in_place = p.dx == p.dy || p.dx == p.x;
+    if (!p.part || (!in_place && p.rows <= kLnColumnRows)) {
+        const int cols = p.part ? (p.c + kLnCols - 1) / kLnCols : 0;
+        const int64_t want = (p.rows + ln_teams(p.rows, p.c) - 1) / ln_teams(p.rows, p.c);
+        const unsigned grid = (unsigned)(cols + (want < 65536 ? want : 65536));
+        return ln_dispatch(p.c, wide, [&](auto nv, auto wpr) {
+            constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
+            const auto go = [&](auto *kernel) {
+                hipLaunchKernelGGL(kernel, dim3(grid), dim3(ln_threads<WPR>()), 0, s, p, cols);
+            };
+            if (p.bf16)
+                go(layernorm_grad_split_kernel<__bf16, NV, WPR>);
+            else
+                go(layernorm_grad_split_kernel<_Float16, NV, WPR>);
+            return hipGetLastError();
+        });
+    }
     const unsigned grid = (unsigned)ln_grad_blocks(p.rows, p.c);
-    hipError_t e = ln_dispatch(p.c, ln_wide(p.rows), [&](auto nv, auto wpr) {
+    hipError_t e = ln_dispatch(p.c, wide, [&](auto nv, auto wpr) {
         constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
+        const auto go = [&](auto *kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(ln_threads<WPR>()), 0, s, p); };
         if (p.bf16)
-            hipLaunchKernelGGL((layernorm_grad_kernel<__bf16, NV, WPR>), dim3(grid), dim3(ln_threads<WPR>()), 0, s, p);
+            go(layernorm_grad_kernel<__bf16, NV, WPR>);
         else
-            hipLaunchKernelGGL((layernorm_grad_kernel<_Float16, NV, WPR>), dim3(grid), dim3(ln_threads<WPR>()), 0, s,
-                               p);
+            go(layernorm_grad_kernel<_Float16, NV, WPR>);
         return hipGetLastError();
     });
-    if (e != hipSuccess || !p.part) return e;
+    if (e != hipSuccess) return e;
     const ColumnSumParams cs = {p.part, p.dgamma, p.dbeta, (int32_t)grid, 2 * p.c, p.c, p.bf16};
     return launch_column_sum(cs, s);
 }

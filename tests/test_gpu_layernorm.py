@@ -145,6 +145,18 @@ def test_backward(size, dtype):
         assert_within(a, ref, s, what)
 
 
+@pytest.mark.parametrize("rows", [2047, 2048, 2049])
+@pytest.mark.parametrize("c", [8, 520, 1032, 2048])
+def test_column_sums_either_side_of_2048_rows(rows, c):
+    dy, x, gamma, dres, stats = make_grad(rows, c, "bf16", 8, rows + c)
+    got = run_grad(dy, x, gamma, stats, dres, 8)
+    refs, slacks = grad64(dy, x, gamma, stats, dres)
+    for a, ref, s, what in zip(got, refs, slacks, ("dx", "dgamma", "dbeta")):
+        assert_within(a, ref, s, what)
+    for again, a in zip(run_grad(dy, x, gamma, stats, dres, 8), got):
+        assert torch.equal(again, a)
+
+
 @pytest.mark.parametrize("want", [(False, False), (True, False), (False, True)])
 @pytest.mark.parametrize("affine", [True, False])
 def test_backward_computes_only_what_is_asked_for(want, affine):
