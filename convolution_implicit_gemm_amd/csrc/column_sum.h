@@ -1,5 +1,6 @@
-// Column sums of fp32 partials: the second half of the weight gradients that are
-// sums over rows (layer norm's dgamma and dbeta, linear's dbias).
+// Column sums: of fp32 partials, the second half of the weight gradients that are
+// sums over rows (layer norm's dgamma and dbeta, linear's dbias), or of the rows
+// themselves (dbias without an activation).
 #pragma once
 
 #include "elem16.h"
@@ -18,9 +19,19 @@ template <typename E, int THREADS>
 __device__ __forceinline__ void column_sum_block(const ColumnSumParams &p, int b, float *lds) {
     constexpr int LANES = THREADS / 4, PER = LANES / 16;
     const int tc = threadIdx.x & 3, tr = threadIdx.x >> 2;
+    b = xcd_range(b, (p.cols + 15) / 16);  // the blocks that share cache lines on one XCD
     const int c = b * 16 + tc * 4;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (c < p.cols) {
+    if (c < p.cols && p.in16) {
+#pragma unroll 8
+        for (int r = tr; r < p.rows; r += LANES) {
+            const e16x4_t u = *reinterpret_cast<const e16x4_t *>(p.in16 + r * p.stride + c);
+            v.x += to_f32<E>(u[0]);
+            v.y += to_f32<E>(u[1]);
+            v.z += to_f32<E>(u[2]);
+            v.w += to_f32<E>(u[3]);
+        }
+    } else if (c < p.cols) {
 #pragma unroll 8
         for (int r = tr; r < p.rows; r += LANES) {
             const float4 u = *reinterpret_cast<const float4 *>(p.part + (int64_t)r * p.cols + c);

@@ -10,6 +10,7 @@
 
 namespace c3d {
 
+typedef _Float16 e16x4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 e16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float e32x16_t __attribute__((ext_vector_type(16)));

@@ -408,7 +408,14 @@ hipError_t launch_layernorm_grad(const LnGradParams &p, hipStream_t s) {
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    const ColumnSumParams cs = {p.part, p.dgamma, p.dbeta, (int32_t)grid, 2 * p.c, p.c, p.bf16};
+    ColumnSumParams cs = {};
+    cs.part = p.part;
+    cs.out0 = p.dgamma;
+    cs.out1 = p.dbeta;
+    cs.rows = (int32_t)grid;
+    cs.cols = 2 * p.c;
+    cs.split = p.c;
+    cs.bf16 = p.bf16;
     return launch_column_sum(cs, s);
 }
 

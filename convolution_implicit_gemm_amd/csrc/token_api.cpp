@@ -456,24 +456,30 @@ conv3d_status linear_backward(linear_plan_t p, const void *dy, const void *x, co
     const _Float16 *dz = in16(dy);
     int64_t dz_stride = p->ys;
     c3d::ColumnSumParams cs = {};
-    if (act || dbias) {
+    // few rows without an activation: dbias straight from dy
+    const bool direct = !act && dbias && d.m <= c3d::kColumnRows;
+    if (dbias) {
+        cs.part = reinterpret_cast<float *>(ws + p->off_col);
+        cs.in16 = direct ? in16(dy) : nullptr;
+        cs.stride = p->ys;
+        cs.out0 = out16(dbias);
+        cs.rows = direct ? (int32_t)d.m : p->strips;
+        cs.cols = cs.split = d.n;
+        cs.bf16 = bf16;
+    }
+    if (act || (dbias && !direct)) {
         c3d::ActGradParams a = {};
         a.dy = in16(dy);
         a.dy_stride = p->ys;
         a.z = in16(preact);
         a.dz = act ? reinterpret_cast<_Float16 *>(ws) : nullptr;
-        a.colpart = dbias ? reinterpret_cast<float *>(ws + p->off_col) : nullptr;
+        a.colpart = dbias ? const_cast<float *>(cs.part) : nullptr;
         a.m = d.m;
         a.n = d.n;
         a.act = d.act;
         a.bf16 = bf16;
         a.strips = p->strips;
         e = c3d::launch_act_grad(a, s);
-        cs.part = a.colpart;
-        cs.out0 = out16(dbias);
-        cs.rows = p->strips;
-        cs.cols = cs.split = d.n;
-        cs.bf16 = bf16;
         if (act) {
             dz = a.dz;
             dz_stride = d.n;

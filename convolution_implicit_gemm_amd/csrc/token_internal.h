@@ -72,14 +72,20 @@ struct ActGradParams {
 };
 int32_t act_grad_strips(int64_t m, int32_t n);
 hipError_t launch_act_grad(const ActGradParams &p, hipStream_t s);
-// The sums over the rows of part [rows][cols] (cols a multiple of 8), rounded to
-// the element type: columns below split into out0, the others into out1 (either
-// may be null).
+// The sums over the rows of part [rows][cols] (cols a multiple of 8), or of in16's
+// rows of elements, `stride` apart, rounded to the element type: columns below
+// split into out0, the others into out1 (either may be null).
 struct ColumnSumParams {
     const float *part;
+    const _Float16 *in16;
+    int64_t stride;
     _Float16 *out0, *out1;
     int32_t rows, cols, split, bf16;
 };
+// The most rows of elements summed by whole columns instead of strips (bf16 dbias
+// alone: 613 x 2048 3.4 against 7.5 us, 4097 x 2048 5.3 and 14.7, 8192 x 2048 8.9 and
+// 13.5; 8192 x 8192 28.9 and 26.3, 16384 x 2048 25.9 and 18.0).
+constexpr int kColumnRows = 6144;
 hipError_t launch_column_sum(const ColumnSumParams &p, hipStream_t s);
 // Zeros into rows of `width` elements, `stride` apart.
 hipError_t launch_zero_rows(_Float16 *y, int64_t rows, int32_t width, int64_t stride, hipStream_t s);

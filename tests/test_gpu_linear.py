@@ -230,6 +230,12 @@ def test_backward_sizes(size, dtype):
     check_backward(*size, act="gelu_tanh", dtype=dtype, gap=16, seed=sum(size))
 
 
+@pytest.mark.parametrize("tile", [None, "m64n64k64", "m64n64k64g4+pair"])
+@pytest.mark.parametrize("m", [1, 63, 65, 1000, 6144, 6145])
+def test_backward_bias_without_activation(m, tile):
+    check_backward(m, 136, 72, act="none", dtype="bf16", gap=8, seed=m, tile=tile)
+
+
 @pytest.mark.parametrize("act", sorted(ACTS))
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 def test_backward_activations(act, dtype):
