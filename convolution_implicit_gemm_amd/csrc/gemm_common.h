@@ -15,6 +15,9 @@ constexpr int kGemmRow = kGemmBK * 2;       // bytes of one LDS row, contraction
 // GELU (erf form) through Abramowitz and Stegun 7.1.26, erf(x) = 1 - (a1 t + ...
 // + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), absolute error 1.5e-7; the tanh
 // form as z * sigmoid(2u), u = sqrt(2 / pi) (z + 0.044715 z^3).
+// Defined for every z: the kept z is rounded to 16 bits and a finite one of fp16's
+// product may be infinite there.  act(+inf) = +inf, act(-inf) = 0, the slopes 1
+// and 0; a NaN stays one.
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGeluA = 0.797884560802865356f, kGeluB = 0.044715f;
 
@@ -36,37 +39,52 @@ __device__ __forceinline__ float normal_tail(float z, float &ex) {
     q = fmaf(t, q, 0.5f * 0.254829592f);
     return q * t * ex;
 }
+// z bounded to +-1e4, where every activation has its limit's value to the last
+// bit: the factor of a term that tends to 0 (which an infinite z would make NaN).
+// The exponentials take z itself, so that a NaN comes through.
+__device__ __forceinline__ float bounded(float z) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_amdgcn_fmed3f(z, -1e4f, 1e4f);
+#else
+    return z;
+#endif
+}
+// z bounded below (and max(z, 0)) the same way: one v_med3 with an upper bound that
+// the compiler cannot see is infinite (its own maximum first quiets z, one
+// instruction more: 1% of a product with SiLU).
+__device__ __forceinline__ float bounded_below(float z, float low) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    float inf = __builtin_inff();
+    asm("" : "+v"(inf));
+    return __builtin_amdgcn_fmed3f(z, low, inf);
+#else
+    return z < low ? low : z;
+#endif
+}
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
-    if constexpr (ACT == CONV3D_ACT_SILU) return z * sigmoid_f(z);
+    if constexpr (ACT == CONV3D_ACT_SILU) return bounded_below(z, -1e4f) * sigmoid_f(z);
     if constexpr (ACT == CONV3D_ACT_GELU) {
         float ex;
-        return fmaf(-fabsf(z), normal_tail(z, ex), fmaxf(z, 0.0f));  // z Phi(z) for either sign
+        return fmaf(-fabsf(bounded(z)), normal_tail(z, ex), bounded_below(z, 0.0f));  // z Phi(z) for either sign
     }
-    if constexpr (ACT == CONV3D_ACT_GELU_TANH) return z * sigmoid_2u(z);
+    if constexpr (ACT == CONV3D_ACT_GELU_TANH) return bounded_below(z, -1e4f) * sigmoid_2u(z);
     return z;
 }
-// (Finite z of any size: the exponentials reach 0 or infinity before a product
-// with z overflows, except for the tanh form's z^2, whose z is bounded where the
-// derivative is 0 or 1 to the last bit.  A NaN comes through.)
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == CONV3D_ACT_NONE) return 1.0f;
+    const float b = bounded(z);
     if constexpr (ACT == CONV3D_ACT_SILU) {
         const float s = sigmoid_f(z);
-        return s * fmaf(z, 1.0f - s, 1.0f);
+        return s * fmaf(b, 1.0f - s, 1.0f);
     }
     if constexpr (ACT == CONV3D_ACT_GELU) {
         float ex;
         const float tail = normal_tail(z, ex);
-        return fmaf(z * 0.398942280401432678f, ex, z < 0.0f ? tail : 1.0f - tail);
+        return fmaf(b * 0.398942280401432678f, ex, z < 0.0f ? tail : 1.0f - tail);
     }
     const float s = sigmoid_2u(z);
-#if defined(__HIP_DEVICE_COMPILE__)
-    const float b = __builtin_amdgcn_fmed3f(z, -1e4f, 1e4f);
-#else
-    const float b = z;
-#endif
     return s * fmaf(b * (1.0f - s), fmaf(6.0f * kGeluA * kGeluB * b, b, 2.0f * kGeluA), 1.0f);
 }
 

@@ -296,7 +296,9 @@ conv3d_status groupnorm_silu_noalloc(const void *x, const void *gamma, const voi
  */
 
 /* Activations of linear.  GELU is z * Phi(z) with the normal distribution's
- * Phi; GELU_TANH its form 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+ * Phi; GELU_TANH its form 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).
+ * All three are +inf at +inf and 0 at -inf, with slopes 1 and 0 (a z beyond the
+ * range of fp16 is kept for the backward pass as an infinity); a NaN stays NaN. */
 typedef enum {
     CONV3D_ACT_NONE = 0,
     CONV3D_ACT_SILU = 1,
