@@ -11,7 +11,7 @@ import torch
 import convolution_implicit_gemm_amd as c3d
 from helpers import env_var
 from test_gpu_linear import backward_slacks
-from token_helpers import ACTS, DTYPES, act64, assert_within, gen, normal, scratch, slope64
+from token_helpers import ACTS, DTYPES, U24, act64, assert_within, gen, normal, scratch, slope64
 
 pytestmark = pytest.mark.gpu
 
@@ -125,3 +125,56 @@ def test_large_preactivations_saturate_exactly(act, dtype, big):
         y = forward(z, act, m, k, tile)
         assert torch.equal(y, z.clamp(min=0).expand(m, -1))
     assert torch.equal(slopes(z, act), (z > 0).to(z.dtype))
+
+
+def exponent(z, act):
+    """|the argument of the activation's exponential|."""
+    if act == "silu":
+        return z.abs()
+    return z * z / 2 if act == "gelu" else (2.0 * math.sqrt(2.0 / math.pi) * (z + 0.044715 * z ** 3)).abs()
+
+
+def relative(z, act):
+    # the exponential's argument is rounded three times and its constants once, 2^-24 of
+    # it each, which is as much of the exponential; the other steps (two transcendental
+    # instructions, the polynomial, a dozen products) stay below 2^-18 together
+    return 2.0 ** -18 + 4 * U24 * exponent(z, act)
+
+
+TAIL = 2.0 ** -122  # below it the instructions may flush to 0, times |z|: bf16 only
+
+
+def sweep(dtype):
+    # fp16: down to where z Phi(z) is below its smallest value
+    return torch.linspace(-12.5, 12.5, 8192, device="cuda:0", dtype=torch.float64).to(DTYPES[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("act", CURVED)
+def test_far_negative_preactivations_keep_their_digits(act, dtype):
+    z = sweep(dtype)
+    zd = z.double()
+    ref = act64(zd, act)
+    slack = ref.abs() * relative(zd, act) + TAIL * (1 + zd.abs())
+    for m, k, tile in KERNELS:
+        assert_within(forward(z, act, m, k, tile), ref.expand(m, -1), slack, "%s, %s" % (act, tile))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("act", CURVED)
+def test_slopes_of_far_negative_preactivations_keep_their_digits(act, dtype):
+    z = sweep(dtype)
+    zd = z.double()
+    # the two terms of the slope, whose rounding errors stay when they cancel
+    if act == "gelu":
+        first, second = 0.5 * torch.special.erfc(zd.abs() / math.sqrt(2.0)), \
+            zd.abs() * torch.exp(-zd * zd / 2) / math.sqrt(2.0 * math.pi)
+    else:
+        grow = 1.0 if act == "silu" else 2.0 * math.sqrt(2.0 / math.pi) * (1.0 + 3 * 0.044715 * zd * zd)
+        arg = zd if act == "silu" else 2.0 * math.sqrt(2.0 / math.pi) * (zd + 0.044715 * zd ** 3)
+        first = torch.sigmoid(arg)
+        second = first * zd.abs() * grow * torch.sigmoid(-arg)
+    # for positive z, 1 - sigmoid is a difference from 1: 2^-24 times what it multiplies
+    far = torch.where(zd > 0, (1.0 + zd.abs() * (1.0 if act == "gelu" else grow)) * 2 * U24, torch.zeros_like(zd))
+    slack = (first + second) * relative(zd, act) + far + TAIL * (1 + zd.abs()) ** 3
+    assert_within(slopes(z, act), slope64(zd, act), slack, act)
