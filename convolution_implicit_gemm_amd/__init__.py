@@ -222,14 +222,16 @@ def _addr(t, what="tensor", elems=None, dtype=None):
 
 
 # What calls need of torch, bound at the first one that needs it (importing this
-# module does not import torch).
+# module does not import torch).  The name that callers test is assigned last:
+# another thread that finds it set finds the others set too.
 _F16 = _BF16 = _F32 = _I32 = _raw_stream = _current_device = None
 
 
 def _bind_torch():
     global _F16, _BF16, _F32, _I32
     import torch
-    _F16, _BF16, _F32, _I32 = torch.float16, torch.bfloat16, torch.float32, torch.int32
+    _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+    _F16 = torch.float16
 
 
 def _bind_streams():
@@ -238,7 +240,8 @@ def _bind_streams():
     global _raw_stream, _current_device
     import torch
     torch.cuda.current_device()  # initialises the device
-    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _current_device = torch._C._cuda_getDevice
+    _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _elem_dtype(bf16):
