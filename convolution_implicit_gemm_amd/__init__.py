@@ -413,31 +413,35 @@ def groupnorm_silu_noalloc(x, gamma, beta, y, n, thw, c, groups, eps, apply_silu
 # ---- the token operators
 
 def _strided_addr(t, what, sizes, strides, dtype):
-    """Device address of a tensor whose elements, at the given sizes and strides
-    (in elements, outermost first) from its first one, lie inside its storage."""
+    """Device address of a tensor that holds the elements at the given sizes and
+    strides (in elements, outermost first) from its first one: a view laid out so
+    and at least as large, or a contiguous tensor of any shape with as many
+    elements.  What its storage holds behind it does not count."""
     if t is None or isinstance(t, int):
         return t
     if not t.is_cuda:
         raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is on %s, not on a GPU" % (what, t.device))
     if t.dtype != dtype:
         raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is %s, %s expected" % (what, t.dtype, dtype))
-    have = t.stride()
-    if have == strides and t.shape == sizes:
+    have, shape = t.stride(), t.shape
+    if have == strides and shape == sizes:
         return t.data_ptr() or None  # a view laid out as the call reads it
     if 0 in sizes:
         return t.data_ptr() or None
     if len(have) >= 2 and len(have) == len(sizes):
         # a size of one may have any stride
-        for n, st, want in zip(t.shape, have, strides):
+        for n, st, want in zip(shape, have, strides):
             if n > 1 and st != want:
                 raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s has strides %s, the call reads %s"
                                   % (what, tuple(have), tuple(strides)))
-    elif not t.is_contiguous():
-        raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is not contiguous" % what)
+        if all(n >= size for n, size in zip(shape, sizes)):
+            return t.data_ptr()
+    if not t.is_contiguous():
+        raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s is %s and not contiguous, the call reads %s"
+                          % (what, tuple(shape), tuple(sizes)))
     last = sum((n - 1) * st for n, st in zip(sizes, strides))
-    room = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
-    if last >= room:
-        raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s holds %d elements, %d needed" % (what, room, last + 1))
+    if last >= t.numel():
+        raise Conv3dError(CONV3D_ERR_INVALID_ARG, "%s holds %d elements, %d needed" % (what, t.numel(), last + 1))
     return t.data_ptr()
 
 
