@@ -655,6 +655,7 @@ struct rope3d_plan_s {
     rope3d_desc d;
     int64_t tokens;
     int64_t qs[3], ks[3], qos[3], kos[3];
+    bool folds_in, folds_out;  // the inputs' or the outputs' strides put different elements on one address
     c3d::RopeParams prm;  // pointers, strides and direction filled per call
 };
 
@@ -684,6 +685,91 @@ Span rope_span(const void *p, const int64_t *s, int64_t n, int64_t tokens, int h
 
 bool same3(const int64_t *a, const int64_t *b) { return a[0] == b[0] && a[1] == b[1] && a[2] == b[2]; }
 
+// Heads of dim elements at base + (sample, token, head) . strides: whether two of
+// them share an element, by search over the differences of their indices.  A
+// term of the search is a stride and the range of its index (or of the difference
+// of two); from the largest stride down, only such indices are followed as the
+// smaller ones can still bring back, a handful for layouts whose strides nest.
+class HeadSearch {
+    struct Term {
+        int64_t stride, lo, hi;
+    };
+    Term t_[6];
+    int64_t below_[7], above_[7];  // how far the terms from i on reach down and up
+    int n_ = 0;
+    const int64_t dim_;
+    const bool itself_;   // one tensor: different indices only
+    bool twice_ = false;  // two of its indices step by the same stride
+    int64_t left_ = 1 << 16;       // steps until the search counts as unanswered
+
+    bool search(int i, int64_t at, bool same) {
+        if (i == n_) return at > -dim_ && at < dim_ && !(itself_ && same);
+        const Term &t = t_[i];
+        if (t.stride == 0) return search(i + 1, at, false);
+        // at + c stride + rest in (-dim, dim), rest in [-below, above]
+        const int64_t from = -dim_ + 1 - above_[i + 1] - at, to = dim_ - 1 + below_[i + 1] - at;
+        int64_t c = from > 0 ? (from + t.stride - 1) / t.stride : -(-from / t.stride);
+        int64_t last = to >= 0 ? to / t.stride : -((-to + t.stride - 1) / t.stride);
+        if (c < t.lo) c = t.lo;
+        if (last > t.hi) last = t.hi;
+        for (; c <= last && left_ > 0; ++c) {
+            --left_;
+            if (search(i + 1, at + c * t.stride, same && c == 0)) return true;
+        }
+        return false;
+    }
+
+public:
+    HeadSearch(int64_t dim, bool itself) : dim_(dim), itself_(itself) {}
+    // lo <= 0 <= hi; terms of one stride are one
+    void add(int64_t stride, int64_t lo, int64_t hi) {
+        if (lo == hi) return;
+        int i = 0;
+        while (i < n_ && t_[i].stride > stride) ++i;
+        if (i < n_ && t_[i].stride == stride) {
+            t_[i].lo += lo;
+            t_[i].hi += hi;
+            twice_ = true;
+            return;
+        }
+        for (int j = n_++; j > i; --j) t_[j] = t_[j - 1];
+        t_[i] = {stride, lo, hi};
+    }
+    bool found(int64_t offset) {
+        below_[n_] = above_[n_] = 0;
+        for (int i = n_ - 1; i >= 0; --i) {
+            below_[i] = below_[i + 1] - t_[i].lo * t_[i].stride;
+            above_[i] = above_[i + 1] + t_[i].hi * t_[i].stride;
+        }
+        return (itself_ && twice_) || search(0, offset, true);
+    }
+    bool unanswered() const { return left_ <= 0; }
+};
+
+// Whether heads of one tensor share an element (or cannot be shown not to).
+bool rope_folds(const rope3d_desc &d, int64_t tokens, const int64_t *s, int heads) {
+    if (d.n < 1 || tokens < 1 || heads < 1) return false;
+    const int64_t ext[3] = {d.n, tokens, heads};
+    HeadSearch h(d.head_dim, true);
+    for (int i = 0; i < 3; ++i) h.add(s[i], -(ext[i] - 1), ext[i] - 1);
+    return h.found(0) || h.unanswered();
+}
+
+// Whether heads of two tensors share an element.
+bool rope_share(const rope3d_desc &d, int64_t tokens, const void *a, const int64_t *sa, int ha, const void *b,
+                const int64_t *sb, int hb) {
+    if (!rope_span(a, sa, d.n, tokens, ha, d.head_dim).meets(rope_span(b, sb, d.n, tokens, hb, d.head_dim)))
+        return false;
+    const int64_t ea[3] = {d.n, tokens, ha}, eb[3] = {d.n, tokens, hb};
+    HeadSearch h(d.head_dim, false);
+    for (int i = 0; i < 3; ++i) {
+        h.add(sa[i], -(ea[i] - 1), 0);
+        h.add(sb[i], 0, eb[i] - 1);
+    }
+    const int64_t bytes = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+    return h.found(bytes / 2);  // both are 16-byte aligned
+}
+
 conv3d_status rope_run(rope3d_plan_t p, const void *q, const void *k, void *qo, void *ko, const void *positions,
                        int32_t t_offset, void *stream, bool inverse) {
     if (!p) return api_fail(CONV3D_ERR_INVALID_ARG, "plan is null");
@@ -707,6 +793,16 @@ conv3d_status rope_run(rope3d_plan_t p, const void *q, const void *k, void *qo, 
     if (clash(q, qi, qo, qj, d.heads_q) || clash(k, ki, ko, kj, d.heads_k))
         return api_fail(CONV3D_ERR_INVALID_ARG, "an output overlaps its input without being it");
     if (!any) return api_ok();
+    if (inverse ? p->folds_in : p->folds_out)
+        return api_fail(CONV3D_ERR_INVALID_ARG, "different elements of an output overlap");
+    if (d.heads_k && (rope_share(d, p->tokens, qo, qj, d.heads_q, ko, kj, d.heads_k) ||
+                      rope_share(d, p->tokens, qo, qj, d.heads_q, k, ki, d.heads_k) ||
+                      rope_share(d, p->tokens, ko, kj, d.heads_k, q, qi, d.heads_q)))
+        return api_fail(CONV3D_ERR_INVALID_ARG, "an output overlaps the other output or its input");
+    const Span pos(positions, positions ? (size_t)d.n * p->tokens * 12 : 0);
+    if (pos.meets(rope_span(qo, qj, d.n, p->tokens, d.heads_q, d.head_dim)) ||
+        pos.meets(rope_span(ko, kj, d.n, p->tokens, d.heads_k, d.head_dim)))
+        return api_fail(CONV3D_ERR_INVALID_ARG, "an output overlaps the positions");
     conv3d_status st = api_check_device();
     if (st != CONV3D_OK) return st;
     c3d::RopeParams r = p->prm;
@@ -773,6 +869,8 @@ conv3d_status rope3d_plan(const rope3d_desc *d, rope3d_plan_t *out) {
         delete p;
         return st;
     }
+    p->folds_in = rope_folds(*d, p->tokens, p->qs, d->heads_q) || rope_folds(*d, p->tokens, p->ks, d->heads_k);
+    p->folds_out = rope_folds(*d, p->tokens, p->qos, d->heads_q) || rope_folds(*d, p->tokens, p->kos, d->heads_k);
     c3d::RopeParams &r = p->prm;
     r.tokens = p->tokens;
     r.n = d->n;

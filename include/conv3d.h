@@ -454,7 +454,11 @@ void rope3d_plan_destroy(rope3d_plan_t p);
 /*
  * Enqueue the rotation of q into q_out and k into k_out (k, k_out ignored when
  * heads_k is 0).  Each output may be its input (same pointer and strides), and
- * must not overlap it otherwise.  positions is required with
+ * must not overlap it otherwise.  The outputs must not share an element with each
+ * other, with the other's input or, through their strides, with themselves (heads
+ * of q and k side by side in one row are fine, and so are inputs that repeat
+ * elements, as strides of 0 make them), nor overlap the positions.
+ * positions is required with
  * CONV3D_F_POSITIONS, otherwise ignored; t_offset is added to the grid's times
  * (the frames before this chunk), and ignored with given positions.
  * rope3d_backward is the gradient: dq, dk from dq_out, dk_out, with the
