@@ -8,6 +8,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <new>
+#include <utility>
 
 #include "token_internal.h"
 
@@ -20,6 +21,7 @@ namespace {
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 constexpr int64_t kMaxStride = (int64_t)1 << 20;
 constexpr int kMaxWidth = 65536;
+constexpr double kMaxElements = 281474976710656.0;  // 2^48, from a tensor's first element to its last
 constexpr int kCUs = 256;
 
 bool misaligned(const void *p, uintptr_t bytes = 16) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
@@ -852,8 +854,8 @@ conv3d_status rope3d_plan(const rope3d_desc *d, rope3d_plan_t *out) {
     if (d->pairing == ROPE3D_PAIR_HALVES && sum % 16)
         return api_fail(CONV3D_ERR_UNSUPPORTED, "ROPE3D_PAIR_HALVES needs dims that are a multiple of 16 together");
     if (d->heads_q > 16384 || d->heads_k > 16384) return api_fail(CONV3D_ERR_UNSUPPORTED, "too many heads");
-    double total = (double)d->n * d->t * d->h * d->w;
-    if (total >= 2147483648.0 || (double)d->h * d->w >= 2147483648.0)
+    const double per_sample = (double)d->t * d->h * d->w, total = per_sample * d->n;
+    if (per_sample >= 2147483648.0 || total >= 2147483648.0 || (double)d->h * d->w >= 2147483648.0)
         return api_fail(CONV3D_ERR_UNSUPPORTED, "2^31 tokens or more");
     rope3d_plan_s *p = new (std::nothrow) rope3d_plan_s();
     if (!p) return api_fail(CONV3D_ERR_INVALID_ARG, "out of host memory");
@@ -865,6 +867,17 @@ conv3d_status rope3d_plan(const rope3d_desc *d, rope3d_plan_t *out) {
         st = rope_strides(d->q_out_stride, p->tokens, d->heads_q, d->head_dim, "q_out_stride", p->qos);
     if (st == CONV3D_OK)
         st = rope_strides(d->k_out_stride, p->tokens, d->heads_k, d->head_dim, "k_out_stride", p->kos);
+    // every offset within a tensor, in bytes, fits 64 bits
+    const auto length = [&](const int64_t *s, int heads) {
+        return d->n && p->tokens && heads
+                   ? (double)(d->n - 1) * s[0] + (double)(p->tokens - 1) * s[1] + (double)(heads - 1) * s[2]
+                   : 0.0;
+    };
+    if (st == CONV3D_OK)
+        for (const auto &t : {std::pair<const int64_t *, int>{p->qs, d->heads_q}, {p->qos, d->heads_q},
+                              {p->ks, d->heads_k}, {p->kos, d->heads_k}})
+            if (length(t.first, t.second) >= kMaxElements)
+                st = api_fail(CONV3D_ERR_UNSUPPORTED, "a tensor is 2^48 elements long or longer");
     if (st != CONV3D_OK) {
         delete p;
         return st;

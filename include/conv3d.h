@@ -446,8 +446,9 @@ typedef struct rope3d_plan_s *rope3d_plan_t; /* host-only, immutable */
  * negative dims, dims that exceed head_dim or are all 0, a base that is not
  * positive and finite, or bad strides; UNSUPPORTED for head_dim not a multiple
  * of 8 or above 512, dims above 256 together, dims not a multiple of 16
- * together for ROPE3D_PAIR_HALVES, more than 16384 query or key heads, or 2^31
- * tokens or more.
+ * together for ROPE3D_PAIR_HALVES, more than 16384 query or key heads, 2^31
+ * tokens or more (of a sample or together), strides of 2^40 or more, or a tensor of
+ * 2^48 elements or more from its first to its last.
  */
 conv3d_status rope3d_plan(const rope3d_desc *d, rope3d_plan_t *out);
 void rope3d_plan_destroy(rope3d_plan_t p);

@@ -109,3 +109,20 @@ def test_overlaps_found_are_the_ones_there_are():
                 c3d.rope3d_forward(p, A, B, C, C + 2 * off, stream=0)
             assert e.value.status == c3d.CONV3D_ERR_NO_DEVICE
     assert found > 100 and (passed > 100 or torch.cuda.is_available())
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n=1 << 30, t=1, h=1, w=1, q_stride=(1 << 39, 256, 64)),
+    dict(n=1 << 12, t=1 << 10, h=1 << 4, w=1, k_out_stride=(1 << 37, 128, 64)),
+    dict(n=1, t=1 << 30, h=1, w=1, k_stride=(0, 1 << 30, 64)), dict(n=0, t=1 << 30, h=1 << 10, w=1 << 20),
+    dict(n=0, t=2, h=1 << 15, w=1 << 15)])
+def test_tensors_too_long_for_their_offsets_are_refused(bad):
+    with pytest.raises(c3d.Conv3dError) as e:
+        c3d.rope3d_plan(c3d.make_rope3d_desc(heads_q=H, heads_k=K, head_dim=DIM, dims=(16, 24, 24), **bad))
+    assert e.value.status == UNSUP
+
+
+def test_the_longest_tensors_are_planned():
+    for good in (dict(n=1 << 8, t=1, h=1, w=1, q_stride=((1 << 40) - 64, 256, 64)), dict(n=0, t=1 << 10, h=1 << 10, w=1 << 10),
+                 dict(n=1, t=1 << 10, h=1 << 10, w=(1 << 11) - 1)):
+        c3d.rope3d_plan(c3d.make_rope3d_desc(heads_q=H, heads_k=K, head_dim=DIM, dims=(16, 24, 24), **good))
