@@ -33,7 +33,8 @@ struct Span {
         : lo(reinterpret_cast<uintptr_t>(p)),
           hi(p && rows > 0 ? lo + (uintptr_t)(((rows - 1) * stride + cols) * elem) : lo) {}
     Span(const void *p, size_t bytes) : lo(reinterpret_cast<uintptr_t>(p)), hi(p ? lo + bytes : lo) {}
-    bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
+    // nothing meets an empty one
+    bool meets(const Span &o) const { return lo < o.hi && o.lo < hi && lo < hi && o.lo < o.hi; }
 };
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }

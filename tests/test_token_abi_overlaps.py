@@ -126,3 +126,11 @@ def test_the_longest_tensors_are_planned():
     for good in (dict(n=1 << 8, t=1, h=1, w=1, q_stride=((1 << 40) - 64, 256, 64)), dict(n=0, t=1 << 10, h=1 << 10, w=1 << 10),
                  dict(n=1, t=1 << 10, h=1 << 10, w=(1 << 11) - 1)):
         c3d.rope3d_plan(c3d.make_rope3d_desc(heads_q=H, heads_k=K, head_dim=DIM, dims=(16, 24, 24), **good))
+
+
+def test_empty_tensors_overlap_nothing():
+    # views of no rows, wherever they point, and a workspace that is not used
+    p = c3d.linear_plan(c3d.make_linear_desc(0, 64, 32, flags=c3d.CONV3D_F_BIAS))
+    c3d.linear_forward(p, B + 64, B, C, None, B + 128, None, C + 16, stream=0)
+    c3d.layernorm(A + 16, A, C, A + 32, None, 0, 64, 1e-6, stream=0)
+    c3d.layernorm(A + 16, A, C, C + 64, A + 64, 0, 64, 1e-6, stream=0)
