@@ -459,8 +459,8 @@ conv3d_status linear_backward(linear_plan_t p, const void *dy, const void *x, co
     const _Float16 *dz = in16(dy);
     int64_t dz_stride = p->ys;
     c3d::ColumnSumParams cs = {};
-    // few rows without an activation: dbias straight from dy
-    const bool direct = !act && dbias && d.m <= c3d::kColumnRows;
+    // without an activation dbias can come straight from dy
+    const bool direct = !act && dbias && c3d::sum_whole_columns(d.m, d.n);
     if (dbias) {
         cs.part = reinterpret_cast<float *>(ws + p->off_col);
         cs.in16 = direct ? in16(dy) : nullptr;

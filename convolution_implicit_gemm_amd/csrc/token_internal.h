@@ -82,10 +82,19 @@ struct ColumnSumParams {
     _Float16 *out0, *out1;
     int32_t rows, cols, split, bf16;
 };
-// The most rows of elements summed by whole columns instead of strips (bf16 dbias
-// alone: 613 x 2048 3.4 against 7.5 us, 4097 x 2048 5.3 and 14.7, 8192 x 2048 8.9 and
-// 13.5; 8192 x 8192 28.9 and 26.3, 16384 x 2048 25.9 and 18.0).
-constexpr int kColumnRows = 6144;
+// Rows of elements are summed by whole columns up to 6144 rows and 6144 x 8192
+// elements, else by strips of rows, whose sums need a launch more but take all CUs
+// for any shape.  bf16 dbias without an activation, strips against whole columns, in
+// us, alone and in one pass with dx and dw (k = 512):
+//   64 x 64 7.0 and 4.8, 8.1 and 6.3;        6144 x 64 6.9 and 5.1, 17.2 and 14.3
+//   4000 x 2048 13.6 and 5.2, 37 and 31;     6144 x 8192 20.8 and 21.5, 124 and 114
+//   2000 x 16384 16.8 and 15.3, 95 and 89;   512 x 65536 17.9 and 12.4, 125 and 114
+// and beyond: 8192 x 8192 25 and 28, 155 and 148;  12288 x 2048 15 and 21, 75 and 75;
+//   4000 x 16384 26 and 28, 175 and 176;     6144 x 65536 144 and 209, 843 and 908.
+constexpr int64_t kColumnRows = 6144, kColumnElements = kColumnRows * 8192;
+inline bool sum_whole_columns(int64_t rows, int32_t cols) {
+    return rows <= kColumnRows && rows * cols <= kColumnElements;
+}
 hipError_t launch_column_sum(const ColumnSumParams &p, hipStream_t s);
 // Zeros into rows of `width` elements, `stride` apart.
 hipError_t launch_zero_rows(_Float16 *y, int64_t rows, int32_t width, int64_t stride, hipStream_t s);

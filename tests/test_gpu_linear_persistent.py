@@ -129,3 +129,9 @@ def test_bias_gradient_of_rows_past_four_gib(dtype):
         _, slacks = backward_slacks(dy, torch.zeros((m, 8), dtype=dt, device="cuda:0"),
                                     torch.zeros((n, 8), dtype=dt, device="cuda:0"), dy, "none")
         assert_within(db, dy.double().sum(0), slacks[2], "dbias")
+
+
+@pytest.mark.parametrize("m,n", [(6144, 8192), (6144, 8200), (6145, 64), (767, 65536), (769, 65536)])
+def test_bias_gradient_by_whole_columns_and_by_strips(m, n):
+    # either side of the sizes that are summed by whole columns, alone and beside dx and dw
+    check_backward(m, n, 8, act="none", dtype="bf16", gap=8, seed=m)
