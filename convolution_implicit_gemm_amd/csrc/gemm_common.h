@@ -109,7 +109,7 @@ __device__ __forceinline__ void act_switch(int act, F &&f) {
 // ---- operand tiles in LDS.  An operand tile is ROWS output rows (or columns)
 // x 64 of the contraction, ROWS x 128 bytes in either order (a whole cache line
 // of every row per stage: with 32 of the contraction and half lines the forward
-// product of 8192^3 ran at 1130 instead of 1410 TFLOP/s):
+// product of 8192^3 ran at 1130 TFLOP/s, with whole ones at 1320 to 1410):
 //   contraction contiguous (TR = false): ROWS rows of 128 bytes; 16-byte chunk
 //     c of row r sits at chunk c ^ swz<64>(r);
 //   transposed (TR = true): 64 rows (one per contraction index) of 2 ROWS

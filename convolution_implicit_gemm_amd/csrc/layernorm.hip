@@ -19,7 +19,7 @@
 // rows, whose statistics are known, instead: dy and x are read twice, from L2,
 // but nothing has to be joined.
 //
-// Measured, bf16: 36864 x 2048 forward 54-57 us, 5.3-5.6 TB/s (a copy runs at 5.0);
+// Measured, bf16: 36864 x 2048 forward 54-57 us, 5.3-5.6 TB/s (copies: 4.9 to 6.0);
 // its gradient with a residual's 120 us, 5.0 TB/s.  Few rows are bound by latency: 1
 // x 1024 2.4 us, the gradients of 1543 x 1032 5.1 us.
 #include "column_sum.h"
@@ -377,7 +377,8 @@ int32_t ln_grad_blocks(int64_t rows, int32_t c) {
 hipError_t launch_layernorm_grad(const LnGradParams &p, hipStream_t s) {
     const bool wide = ln_wide(p.rows);
     // One launch for few rows (all gradients, bf16: 1 x 1024 4.6 -> 2.6 us, 613 x 2048
-    // 9.8 -> 5.0, 1543 x 1032 9.8 -> 5.1, 2000 x 1024 9.8 -> 6.6, 2000 x 8192 40 -> 28;
+    // 9.8 -> 5.0, 1543 x 1032 9.8 -> 5.1, 2000 x 1024 9.8 -> 6.6, 2000 x 8192 40 -> 28,
+    // 513 x 16384 level, 2048 x 16384 56 -> 63;
     // 3000 x 2048 14.7 -> 15.7, 4097 x 1024 13.0 -> 16.3) and for dx alone (36864 x 2048
     // 92 -> 78).  dx in place of dy or x would change what the columns' blocks read.
     const bool in_place = p.dx == p.dy || p.dx == p.x;

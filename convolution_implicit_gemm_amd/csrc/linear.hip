@@ -33,7 +33,7 @@ __device__ __forceinline__ void gemm_my_unit(const GemmParams &p, int b, int &m_
 // their sums meet in LDS, in group order.  Bound by what L2 delivers: 16 to 20
 // TB/s over the card, so the tile is the largest that still fills it.  Forward,
 // bf16: 64 x 64 tiles 613 x 2048 x 2048 14 us; 128 x 128 with two groups 2048^3
-// 21.7 us (790 TFLOP/s; one group 24.5); 64 x 64 with four 64 x 2048 x 2048 8.6 us.
+// 23.5 us (730 TFLOP/s; one group 26.7); 64 x 64 with four 64 x 2048 x 2048 8.6 us.
 template <int BM_, int BN_, int WM_, int WN_, int NS_, int KG_>
 struct RingTile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, KG = KG_;
@@ -193,10 +193,11 @@ __global__ __launch_bounds__(T::THREADS) void gemm_pair_kernel(GemmParams px, Ge
 // next.  At its end the two buffers of the last stage are free and serve the
 // epilogue, 8 KiB per wave, so that its stores drain under the next unit's
 // stages (2 to 3% less time than one workgroup per unit).  Bound by power: the
-// matrix cores are busy 82% of the cycles on dw and 71% with a contraction of
-// 2048, an activation and 600 MB of output, at the clock that leaves.  bf16: 8192^3
-// 1410 TFLOP/s forward, 1390 dx, 1400 dw; 36864 x 8192 x 2048 950 us (1300
-// TFLOP/s), with tanh GELU 1000.
+// matrix cores are busy 80% of the cycles on dw and 71% with a contraction of
+// 2048, an activation and 600 MB of output, at the clock that leaves.  In TFLOP/s:
+// 8192^3 bf16 1320-1400 forward, 1375 dx and dw, fp16 1290, 1270 and 1280; 36864 x
+// 8192 x 2048 bf16 1310 (945 us), 1345 and 1390, fp16 1235, 1250 and 1310; with bf16
+// tanh GELU 1000-1030 us.
 template <typename E, bool PT, bool QT>
 __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p0) {
     constexpr int BM = 256, BN = 256, WM = BM / 4, WN = BN / 2, TN = WN / 32, TM = WM / 32, WAVES = 8;
@@ -383,11 +384,12 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p0) {
 // reads w's rows straight into the MFMA's A fragment (16x16x32: 16 columns, 64
 // contiguous bytes of each), several in flight, and the rows of x (which stay
 // in cache) into B.  The waves' sums meet in LDS, in wave order; one wave runs the
-// epilogue.  No LDS staging, no second launch.  1 x 4096 x 1024: 4.1 us, of which
-// the launch is about 2; 64 x 64 tiles take 6.3 us.  A CU draws 32 bytes a
-// nanosecond this way, whatever its waves (4, 8 and 16 measured level), so few
-// columns of a long contraction go to the tiles that split it: 512 x 8192 8.1 us,
-// here 10.6.
+// epilogue.  No LDS staging, no second launch.  Launches one after the other, w from
+// the caches and from HBM: 1 x 4096 x 1024 3.2 and 4.4 us, of which the launch is
+// about 2 (64 x 64 tiles 6.3 and 7.4).  A CU draws 32 bytes a nanosecond this way,
+// whatever its waves (4, 8 and 16 measured level), so few columns of a long
+// contraction go to the tiles that split it: 512 x 8192 8.7 and 10.4 us, here 10.4
+// and 11.5.
 template <typename E>
 __device__ __forceinline__ f32x4 mfma_16x16x32(half8_t a, half8_t b, f32x4 c) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -508,10 +510,18 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p, GemmParams
 
 // ---- dz = dy act'(z) and its column sums.  A block walks a strip of rows for
 // 256 groups of 8 columns (or, where there are fewer, several rows at once) and
-// writes the strip's fp32 sums.  A separate pass, because both products read dz
-// (dx every column panel, dw every row panel, through loads that go straight to
-// LDS).  A stream: 36864 x 8192 bf16 358 us, 5.0 TB/s; 4097 x 2048 fp16 12 us, half of
-// it the activation's arithmetic.
+// writes the strip's fp32 sums, of dz before its rounding.  A separate pass, because
+// both products read dz (dx every column panel, dw every row panel, through loads
+// that go straight to LDS).  A stream: 36864 x 8192 bf16 360 us, 5.0 TB/s; 4097 x 2048
+// fp16 13 us, half of it the activation's arithmetic.
+//
+// dz is rounded once to the element type, as the matrix cores' operand.  Its
+// rounding error adds to that of rounding dx and dw themselves, in their L2 norms
+// 2.08e-4 -> 2.93e-4 in fp16 and 1.66e-3 -> 2.35e-3 in bf16 (against 64-bit products of
+// the rounded dz the error is the results' rounding alone).  The matrix cores have
+// no product of a wider operand with a 16-bit one: to keep what the rounding drops,
+// dz would have to go in as two 16-bit terms, which doubles both products, 1.8 of the
+// 2.2 ms that the gradients of 36864 x 8192 x 2048 take.
 template <typename E, int ACT, bool DZ>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradParams p, int groups, int rows_at_once) {
     __shared__ float s[256 * 8];

@@ -26,7 +26,6 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeBatch = 4;       // tasks of a thread whose loads are in flight at once
 constexpr int kRopeMaxTokens = 16;  // tokens of a block
 
-// HALVES: the pair is (p, p + pairs) instead of (2p, 2p + 1).
 // a / b for 0 <= a < 2^22: the float quotient is off by at most one
 __device__ __forceinline__ int small_div(int a, int b, float rcp_b) {
     int q = (int)((float)a * rcp_b);
@@ -36,8 +35,9 @@ __device__ __forceinline__ int small_div(int a, int b, float rcp_b) {
     return q;
 }
 
-// The block's tokens from `first` on.  turn: [token][pair] (cos, sin); place: a
-// token's offsets in q, q's output, k, k's output.
+// The block's tokens from `first` on.  HALVES: the pair is (p, p + pairs) instead of
+// (2p, 2p + 1).  turn: [token][pair] (cos, sin); place: a token's offsets in q, q's
+// output, k, k's output.
 template <typename E, bool HALVES>
 __device__ __forceinline__ void rope3d_tokens(const RopeParams &p, int64_t first, int tasks, int tokens_per_block,
                                               float2 *turn, int64_t (*place)[4]) {

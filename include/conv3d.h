@@ -329,7 +329,8 @@ typedef struct linear_plan_s *linear_plan_t;
 /* What a plan chose for the forward product. */
 typedef struct {
     int32_t tile_m, tile_n, tile_k, threads;
-    int64_t grid;                 /* workgroups of the product kernel */
+    int64_t grid;                 /* work units of the product kernel: whole tiles and pieces of split ones, a
+                                   * workgroup each (m256n256k64: at most 256 workgroups take them in turn) */
     int32_t split_tiles;          /* tiles whose contraction is split over several workgroups */
     int32_t split_pieces;         /* pieces per split tile (0 if none) */
     size_t workspace_bytes, backward_workspace_bytes;
