@@ -33,6 +33,10 @@ CONV3D_F_CHUNK = 16
 CONV3D_F_GN_STATS = 32
 CONV3D_F_PREACT = 64
 CONV3D_F_POSITIONS = 128
+CONV3D_F_LENGTHS = 256
+CONV3D_F_TAIL = 512
+CONV3D_F_STATE8 = 1024
+CONV3D_F_GRAD32 = 2048
 
 CONV3D_ACT_NONE = 0
 CONV3D_ACT_SILU = 1
@@ -56,6 +60,9 @@ EXPORTED = ("conv3d_plan", "conv3d_plan_query", "conv3d_plan_destroy", "conv3d_f
             "layernorm", "layernorm_bf16", "layernorm_backward_workspace", "layernorm_backward",
             "layernorm_backward_bf16",
             "rope3d_plan", "rope3d_plan_destroy", "rope3d_forward", "rope3d_backward",
+            "attention_plan", "attention_plan_query", "attention_plan_destroy", "attention_forward",
+            "attention_backward_workspace", "attention_backward",
+            "adamw_plan", "adamw_plan_destroy", "adamw_hyper_pack", "adamw_step",
             "conv3d_calibrate_scratch_bytes",
             "conv3d_calibrate_mfma", "conv3d_calibrate_hbm", "conv3d_clock_stamp_bytes",
             "conv3d_clock_stamp", "conv3d_status_str",
@@ -98,6 +105,32 @@ class rope3d_desc(ctypes.Structure):
                 ("n", "t", "h", "w", "heads_q", "heads_k", "head_dim", "dim_t", "dim_h", "dim_w", "pairing")] + \
                [("flags", ctypes.c_uint32), ("base", ctypes.c_double)] + \
                [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
+
+
+class attention_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n", "heads_q", "heads_k", "head_dim", "tq", "tk", "frame", "window")] + \
+               [("scale", ctypes.c_float), ("flags", ctypes.c_uint32)] + \
+               [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "o_stride")]
+
+
+class attention_plan_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tile_rows", "tile_keys", "threads", "splits")] + \
+               [("grid", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t),
+                ("backward_workspace_bytes", ctypes.c_size_t), ("kernel_name", ctypes.c_char * 64)]
+
+
+class adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + \
+               [("count", ctypes.c_int64), ("decay", ctypes.c_float)]
+
+
+class adamw_hyper(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + \
+               [("step", ctypes.c_int64)]
+
+
+ADAMW_DEVICE_HYPER = 9
+ADAMW_BLOCK = 128
 
 
 class Conv3dError(RuntimeError):
@@ -175,7 +208,17 @@ def load_library(path: str = LIB_PATH):
             ("rope3d_plan", [ctypes.POINTER(rope3d_desc), ctypes.POINTER(vp)], ctypes.c_int),
             ("rope3d_plan_destroy", [vp], None),
             ("rope3d_forward", [vp] * 6 + [i32, vp], ctypes.c_int),
-            ("rope3d_backward", [vp] * 6 + [i32, vp], ctypes.c_int)):
+            ("rope3d_backward", [vp] * 6 + [i32, vp], ctypes.c_int),
+            ("attention_plan", [ctypes.POINTER(attention_desc), ctypes.POINTER(vp), ctypes.POINTER(sz)], ctypes.c_int),
+            ("attention_plan_query", [vp, ctypes.POINTER(attention_plan_info)], ctypes.c_int),
+            ("attention_plan_destroy", [vp], None),
+            ("attention_forward", [vp] * 7 + [i64, vp, sz, vp], ctypes.c_int),
+            ("attention_backward_workspace", [vp], sz),
+            ("attention_backward", [vp] * 11 + [i64, vp, sz, vp], ctypes.c_int),
+            ("adamw_plan", [ctypes.POINTER(adamw_tensor), i32, ctypes.c_uint32, ctypes.POINTER(vp)], ctypes.c_int),
+            ("adamw_plan_destroy", [vp], None),
+            ("adamw_hyper_pack", [ctypes.POINTER(adamw_hyper), ctypes.POINTER(f32)], ctypes.c_int),
+            ("adamw_step", [vp, ctypes.POINTER(adamw_hyper), vp, vp], ctypes.c_int)):
         getattr(lib, fn).argtypes = args
         getattr(lib, fn).restype = res
     dp = ctypes.POINTER(ctypes.c_double)
@@ -639,6 +682,203 @@ def rope3d_backward(plan: RopePlan, dq_out, dk_out, dq, dk, positions=None, t_of
     lq, lk, lqo, lko = plan.layouts
     _rope_call((_lib or load_library()).rope3d_backward, plan, dq_out, dk_out, dq, dk, positions, t_offset, stream,
                (lqo, lko, lq, lk))
+
+
+class AttentionPlan:
+    """Owns an attention_plan_t; destroyed with the object."""
+
+    def __init__(self, handle, workspace_bytes, desc):
+        self.handle = handle
+        self.workspace_bytes = workspace_bytes
+        self.desc = desc
+        d = desc
+
+        def layout(tokens, heads, stride):
+            stride = tuple(stride)
+            if not any(stride):
+                stride = (tokens * heads * d.head_dim, heads * d.head_dim, d.head_dim)
+            return (d.n, tokens, heads, d.head_dim), stride + (1,)
+
+        # (sizes, strides) of q, k, v and o
+        self.layouts = (layout(d.tq, d.heads_q, d.q_stride), layout(d.tk, d.heads_k, d.k_stride),
+                        layout(d.tk, d.heads_k, d.v_stride), layout(d.tq, d.heads_q, d.o_stride))
+        self.lse = d.n * d.heads_q * d.tq
+        self.lengths = 2 * d.n if d.flags & CONV3D_F_LENGTHS else 0
+        self.dtype = _elem_dtype(d.flags & CONV3D_F_BF16)
+
+    def info(self) -> attention_plan_info:
+        return attention_plan_query(self)
+
+    def __del__(self):
+        if self.handle and _lib is not None:
+            _lib.attention_plan_destroy(self.handle)
+            self.handle = None
+
+
+def make_attention_desc(n, tq, tk, heads_q, heads_k, head_dim, frame=0, window=0, scale=0.0, flags=0,
+                        q_stride=(0, 0, 0), k_stride=(0, 0, 0), v_stride=(0, 0, 0),
+                        o_stride=(0, 0, 0)) -> attention_desc:
+    """frame: tokens of a frame (0: every query sees every key); window: the frames that a query sees, its
+    own and those before it (0: all); scale 0: 1 / sqrt(head_dim); strides: elements between samples,
+    tokens and heads (all 0: contiguous)."""
+    arr = ctypes.c_int64 * 3
+    return attention_desc(n, heads_q, heads_k, head_dim, tq, tk, frame, window, scale, flags, arr(*q_stride),
+                          arr(*k_stride), arr(*v_stride), arr(*o_stride))
+
+
+def attention_plan(desc: attention_desc) -> AttentionPlan:
+    lib = load_library()
+    h = ctypes.c_void_p()
+    ws = ctypes.c_size_t()
+    _check(lib.attention_plan(ctypes.byref(desc), ctypes.byref(h), ctypes.byref(ws)))
+    return AttentionPlan(h.value, ws.value, desc)
+
+
+def attention_plan_query(plan: AttentionPlan) -> attention_plan_info:
+    info = attention_plan_info()
+    _check(load_library().attention_plan_query(plan.handle, ctypes.byref(info)))
+    return info
+
+
+def attention_plan_destroy(plan: AttentionPlan) -> None:
+    if plan.handle:
+        load_library().attention_plan_destroy(plan.handle)
+        plan.handle = None
+
+
+def attention_forward(plan: AttentionPlan, q, k, v, o, lse=None, lengths=None, q_offset=0, workspace=None,
+                      workspace_bytes=None, stream=None) -> None:
+    """Enqueue o = softmax(scale q k^T) v over the keys that each query sees (and lse, the logarithm of its
+    exponentials' sum, fp32 [n, heads_q, tq]) on ``stream``; lengths: int32 [n, 2] (queries, keys)."""
+    lq, lk, lv, lo = plan.layouts
+    dt = plan.dtype
+    given = lengths if plan.lengths else None
+    _check((_lib or load_library()).attention_forward(
+        plan.handle, _strided_addr(q, "q", *lq, dt), _strided_addr(k, "k", *lk, dt), _strided_addr(v, "v", *lv, dt),
+        _strided_addr(o, "o", *lo, dt), _addr(lse, "lse", plan.lse, _F32), _addr(given, "lengths", plan.lengths, _I32),
+        q_offset, _addr(workspace, "workspace"), _workspace_bytes(workspace, workspace_bytes, plan.workspace_bytes),
+        _stream(stream)))
+
+
+def attention_backward_workspace(plan: AttentionPlan) -> int:
+    return load_library().attention_backward_workspace(plan.handle)
+
+
+def attention_backward(plan: AttentionPlan, dout, q, k, v, o, lse, dq, dk, dv, lengths=None, q_offset=0,
+                       workspace=None, workspace_bytes=None, stream=None) -> None:
+    """Enqueue the gradients dq, dk and dv (each may be None) of attention_forward on ``stream``."""
+    lq, lk, lv, lo = plan.layouts
+    dt = plan.dtype
+    given = lengths if plan.lengths else None
+    if workspace_bytes is None and isinstance(workspace, int):
+        workspace_bytes = attention_backward_workspace(plan)
+    _check((_lib or load_library()).attention_backward(
+        plan.handle, _strided_addr(dout, "dout", *lo, dt), _strided_addr(q, "q", *lq, dt),
+        _strided_addr(k, "k", *lk, dt), _strided_addr(v, "v", *lv, dt), _strided_addr(o, "o", *lo, dt),
+        _addr(lse, "lse", plan.lse, _F32), _strided_addr(dq, "dq", *lq, dt), _strided_addr(dk, "dk", *lk, dt),
+        _strided_addr(dv, "dv", *lv, dt), _addr(given, "lengths", plan.lengths, _I32), q_offset,
+        _addr(workspace, "workspace"), _workspace_bytes(workspace, workspace_bytes), _stream(stream)))
+
+
+class AdamwList:
+    """The tensors of an AdamW step: owns an adamw_plan_t and keeps the tensors alive."""
+
+    def __init__(self, handle, tensors):
+        self.handle = handle
+        self.tensors = tensors
+
+    def __del__(self):
+        if self.handle and _lib is not None:
+            _lib.adamw_plan_destroy(self.handle)
+            self.handle = None
+
+
+def adamw_list(params, grads, m, v, master=None, m_scale=None, v_scale=None, decay=None) -> AdamwList:
+    """The tensors that adamw_step updates, as lists of equal length.
+
+    params: fp16 or bf16 weights, or None; master: fp32 weights, or None (their entries
+    too may be None, one of the two is needed for every tensor); grads: of params' type (with
+    params None, any of fp16 and bf16) or fp32; m and v: fp32, or float8_e4m3fn / uint8 with m_scale and
+    v_scale, uint8 with one scale for each 128 elements; decay: a factor of the weight
+    decay for each tensor (1).  The tensors have to stay where they are as long as the list is used."""
+    _elem_dtype(False)
+    import torch
+    count = len(grads)
+    none = [None] * count
+
+    def bad(message):
+        raise Conv3dError(CONV3D_ERR_INVALID_ARG, message)
+
+    lists = [none if x is None else list(x) for x in (params, master, grads, m, v, m_scale, v_scale)]
+    decay = [1.0] * count if decay is None else list(decay)
+    if any(len(x) != count for x in lists + [decay]):
+        bad("the lists have different lengths")
+    kinds = {t.dtype for t in lists[0] if t is not None}
+    if len(kinds) > 1 or not kinds <= {_F16, _BF16}:
+        bad("params are %s, all fp16 or all bf16 expected" % sorted(map(str, kinds)))
+    grad_kinds = {t.dtype for t in grads}
+    if len(grad_kinds) > 1:
+        bad("grads are of different types")
+    grad32 = grad_kinds == {_F32}
+    half = kinds or (grad_kinds - {_F32}) or {_F16}
+    half, = half
+    byte = torch.uint8
+    state8 = m_scale is not None or v_scale is not None
+    state = ({byte, getattr(torch, "float8_e4m3fn", byte)} if state8 else {_F32})
+    wanted = ({half}, {_F32}, {_F32} if grad32 else {half}, state, state, {byte}, {byte})
+    names = ("params", "master", "grads", "m", "v", "m_scale", "v_scale")
+    array = (adamw_tensor * max(count, 1))()
+    device = None
+    for i in range(count):
+        g = lists[2][i]
+        n = g.numel()
+        for name, kind, tensors, field in zip(names, wanted, lists, ("param", "master", "grad", "m", "v", "m_scale",
+                                                                     "v_scale")):
+            t = tensors[i]
+            if t is None:
+                if name in ("m", "v") or (state8 and name.endswith("scale")):
+                    bad("%s[%d] is missing" % (name, i))
+                continue
+            what = "%s[%d]" % (name, i)
+            if t.dtype not in kind:
+                bad("%s is %s, %s expected" % (what, t.dtype, " or ".join(sorted(map(str, kind)))))
+            need = -(-n // ADAMW_BLOCK) if name.endswith("scale") else n
+            if t.numel() != need:
+                bad("%s holds %d elements, %d expected" % (what, t.numel(), need))
+            address = _addr(t, what)
+            device = t.device if device is None else device
+            if t.device != device:
+                bad("%s is on %s, others on %s" % (what, t.device, device))
+            setattr(array[i], field, address or None)
+        array[i].count = n
+        array[i].decay = float(decay[i])
+    flags = (CONV3D_F_BF16 if half == _BF16 else 0) | (CONV3D_F_STATE8 if state8 else 0) | \
+        (CONV3D_F_GRAD32 if grad32 else 0)
+    h = ctypes.c_void_p()
+    _check(load_library().adamw_plan(array, count, flags, ctypes.byref(h)))
+    return AdamwList(h.value, lists)
+
+
+def make_adamw_hyper(lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step=1, grad_scale=1.0) -> adamw_hyper:
+    return adamw_hyper(lr, beta1, beta2, eps, weight_decay, grad_scale, step)
+
+
+def adamw_hyper_pack(hyper: adamw_hyper):
+    """The floats that a device tensor of hyperparameters holds, as a list."""
+    out = (ctypes.c_float * ADAMW_DEVICE_HYPER)()
+    _check(load_library().adamw_hyper_pack(ctypes.byref(hyper), out))
+    return list(out)
+
+
+def adamw_step(tensors: AdamwList, hyper, stream=None) -> None:
+    """Enqueue one AdamW step over ``tensors`` on ``stream``.  hyper: an adamw_hyper, or a
+    device fp32 tensor that holds adamw_hyper_pack's numbers when the step runs."""
+    lib = _lib or load_library()
+    if isinstance(hyper, adamw_hyper):
+        _check(lib.adamw_step(tensors.handle, ctypes.byref(hyper), None, _stream(stream)))
+    else:
+        _elem_dtype(False)
+        _check(lib.adamw_step(tensors.handle, None, _addr(hyper, "hyper", ADAMW_DEVICE_HYPER, _F32), _stream(stream)))
 
 
 def conv3d_calibrate_scratch_bytes() -> int:

@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libconv3d.so")
 SOURCES = ["conv3d_igemm.hip", "conv3d_ps.hip", "pointwise.hip", "groupnorm_silu.hip", "calibrate.hip",
-           "linear.hip", "layernorm.hip", "rope3d.hip", "api.cpp", "token_api.cpp", "selftest.cpp"]
+           "linear.hip", "layernorm.hip", "rope3d.hip", "attention.hip", "attention_grad.hip", "adamw.hip",
+           "api.cpp", "token_api.cpp", "attention_api.cpp", "adamw_api.cpp", "selftest.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

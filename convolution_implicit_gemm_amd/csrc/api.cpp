@@ -207,7 +207,7 @@ const char *conv3d_status_str(conv3d_status s) {
 
 const char *conv3d_last_error(void) { return g_last_error; }
 
-int32_t conv3d_version(void) { return 200; }
+int32_t conv3d_version(void) { return 300; }
 
 conv3d_status conv3d_plan(const conv3d_desc *d, conv3d_plan_t *out, size_t *workspace_bytes) {
     if (!d || !out || !workspace_bytes) return fail(CONV3D_ERR_INVALID_ARG, "null argument");

@@ -1,0 +1,423 @@
+// Attention over the tokens of a latent grid, forward:
+//   o_i = sum_j exp(s_ij - lse_i) v_j,  s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij)
+// over the keys j that query i sees.
+//
+// One pass over the keys with a running maximum and sum per query (in the
+// exponent of 2, fp32).  Scores are computed transposed, S^T = K Q^T: an MFMA's
+// result then holds one query per lane, so that the maximum, the sum and the
+// rescaling of a query's output are a lane's own business (one exchange between
+// the halves of the wave for the maximum), and its registers are, as they stand, the operand
+// P^T of O^T = V^T P^T.  Probabilities are rounded to the element type for that
+// product (one rounding of each, half an ulp, as the tensors themselves have); their sum
+// is taken of the fp32 values.
+#include "attention_common.h"
+
+namespace c3d {
+
+constexpr float kAttnLog2e = 1.44269504088896341f, kAttnLn2 = 0.693147180559945309f;
+
+// The running softmax of one query per lane, scores in units of log2.
+struct AttnSoftmax {
+    float max, use;  // the running maximum; the same where there is one, else 0
+    float sum;       // of the lane's own half of the keys
+    __device__ __forceinline__ void init() {
+        max = -__builtin_inff();
+        use = 0.0f;
+        sum = 0.0f;
+    }
+};
+
+// 1 / sum; 0 for a row that saw no key.
+__device__ __forceinline__ float attn_inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+
+// ---- tiles of WAVES x 32 rows: wave w holds rows 32 w .. + 31, every lane one of
+// them, and all waves share the tile of 64 keys in LDS (two of each of K and V in
+// turn, loaded straight into LDS while the tile before is computed).
+template <typename E, int DP, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void attention_tile_kernel(AttnParams p) {
+    constexpr int BN = kAttnTileKeys, NT = DP / 32, KK = DP / 16, TILE = BN * DP * 2;
+    __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // the longest tiles of a masked problem first, heads side by side
+    const int heads = p.n * p.hk, tiles = (int)gridDim.x / heads;
+    const int head = blockIdx.x % heads, tile = tiles - 1 - blockIdx.x / heads;
+    const int b = head / p.hk, hk = head % p.hk;
+    const AttnSample s = attn_sample(p, b);
+    const int r0 = tile * WAVES * 32;
+
+    // this lane's row; rows past the sample's last query take that one's place
+    const int r = r0 + wave * 32 + (lane & 31);
+    const int i = r / p.group, g = r - i * p.group;
+    const bool alive = i < s.queries;
+    const int last = s.queries - 1;
+    const AttnRange seen = last < 0 ? AttnRange{0, 0} : attn_range(p, s, i < last ? i : last);
+    const int t_first = r0 / p.group, t_last = (r0 + WAVES * 32 - 1) / p.group;
+    int lo = 0, hi = 0;  // of the whole tile
+    if (t_first <= last) {
+        lo = attn_range(p, s, t_first).lo;
+        hi = attn_range(p, s, t_last < last ? t_last : last).hi;
+    }
+    lo &= ~(BN - 1);
+    if (p.splits > 1) {
+        lo += blockIdx.y * p.pieces * BN;
+        const int end = lo + p.pieces * BN;
+        hi = hi < end ? hi : end;
+    }
+    const int wave_lo = __builtin_amdgcn_readfirstlane(seen.lo), wave_hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
+    const int wave_lo_all = __builtin_amdgcn_readlane(seen.lo, 31), wave_hi = __builtin_amdgcn_readlane(seen.hi, 31);
+
+    const int d = p.d;
+    half8_t q[KK];
+    {
+        const _Float16 *row = p.q + b * p.qs[0] + i * p.qs[1] + (int64_t)(hk * p.group + g) * p.qs[2];
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            const int e = 16 * kk + 8 * (lane >> 5);
+            half8_t z = {};
+            q[kk] = alive && e < d ? *reinterpret_cast<const half8_t *>(row + e) : z;
+        }
+    }
+    AttnTile<DP, BN, WAVES> tk, tv;
+    tk.init(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane);
+    tv.init(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
+    AttnRows<DP> fk;
+    AttnCols<DP> fv;
+    fk.init(lane);
+    fv.init(lane);
+
+    const float c = p.scale * kAttnLog2e;
+    AttnSoftmax sm;
+    sm.init();
+    f32x16 acc[NT] = {};
+    int buf = 0;
+    if (lo < hi) {
+        tk.load(smem, lo, wave);
+        tv.load(smem + TILE, lo, wave);
+    }
+    for (int j0 = lo; j0 < hi; j0 += BN) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        const char *ks = smem + buf * 2 * TILE, *vs = ks + TILE;
+        buf ^= 1;
+        if (j0 + BN < hi) {
+            char *next = smem + buf * 2 * TILE;
+            tk.load(next, j0 + BN, wave);
+            tv.load(next + TILE, j0 + BN, wave);
+        }
+        if (j0 + BN <= wave_lo || j0 >= wave_hi) continue;
+        f32x16 x[2] = {};
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) x[t] = mfma_32x32x16<E>(fk.read(ks, 32 * t, kk), q[kk], x[t]);
+        if (j0 < wave_lo_all || j0 + BN > wave_hi_all) {
+            const int from = seen.lo - j0, to = seen.hi - j0;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int j = 32 * t + acc_row(e, lane >> 5);
+                    x[t][e] = j >= from && j < to ? x[t][e] : -__builtin_inff();
+                }
+        }
+        float mx = x[0][0];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[t][e]);
+        mx = both_max(mx) * c;
+        // the maximum follows only where it would be passed by more than 2^8: probabilities
+        // are at most that, far inside the range of either type
+        if (__builtin_amdgcn_ballot_w64(mx > sm.max + 8.0f)) {
+            const float m = fmaxf(sm.max, mx);
+            const float use = m == -__builtin_inff() ? 0.0f : m;
+            const float f = __builtin_amdgcn_exp2f(sm.max - use);
+            sm.max = m;
+            sm.use = use;
+            sm.sum *= f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[t][e] *= f;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                x[t][e] = __builtin_amdgcn_exp2f(fmaf(x[t][e], c, -sm.use));
+                sm.sum += x[t][e];
+            }
+        static_for<4>([&](auto step) {
+            constexpr int S = decltype(step)::value;
+            half8_t f[NT];
+            fv.template read<S>(vs, f);
+            const half8_t w = pack8<E>(x[S / 2], (S & 1) * 8);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = mfma_32x32x16<E>(f[t], w, acc[t]);
+        });
+    }
+    const float sum = both_sum(sm.sum);
+    if (r >= p.rows) return;
+    if (p.splits > 1) {
+        const int64_t at = ((int64_t)blockIdx.y * heads + head) * p.rows + r;
+        if (lane < 32) p.part_ml[at] = make_float2(sm.max, sum);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const int e0 = 32 * t + acc_row(e, lane >> 5);
+                if (e0 < d)
+                    *reinterpret_cast<f32x4 *>(p.part_o + at * d + e0) =
+                        f32x4{acc[t][e], acc[t][e + 1], acc[t][e + 2], acc[t][e + 3]};
+            }
+        return;
+    }
+    if (!alive) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[t] = f32x16{};
+    }
+    const float inv = attn_inverse(sum);
+    const int h = hk * p.group + g;
+    if (p.lse && lane < 32)
+        p.lse[((int64_t)b * p.hq + h) * p.tq + i] =
+            alive ? (sm.use + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -__builtin_inff();
+    _Float16 *out = p.o + b * p.os[0] + i * p.os[1] + h * p.os[2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, acc[t], inv, d - 32 * t, lane, true);
+}
+
+// ---- few rows (at most 32 to a key head: single tokens): the time is that of reading
+// K and V once.  Every wave takes 32 keys at a time, in turn with the other waves, through
+// LDS buffers of its own, so that no barrier ties the waves' loads together; their sums
+// meet in LDS at the end.
+template <typename E, int DP>
+__global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
+    constexpr int WAVES = 4, BN = 32, NT = DP / 32, KK = DP / 16, TILE = BN * DP * 2, NL = 2 * AttnTile<DP, BN, 1>::LOADS;
+    static_assert(WAVES * BN == kAttnFewKeys, "keys of a step");
+    __shared__ __attribute__((aligned(1024))) char smem[WAVES * 4 * TILE];
+    static_assert(WAVES * (32 * DP + 64) * 4 <= (int)sizeof(smem), "the waves' sums fit the buffers");
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int heads = p.n * p.hk, head = blockIdx.x % heads, split = blockIdx.x / heads;
+    const int b = head / p.hk, hk = head % p.hk;
+    const AttnSample s = attn_sample(p, b);
+    const int r = lane & 31;
+    const int i = r / p.group, g = r - i * p.group;
+    const bool alive = r < p.rows && i < s.queries;
+    const int last = s.queries - 1;
+    const AttnRange seen = last < 0 ? AttnRange{0, 0} : attn_range(p, s, i < last ? i : last);
+    const int lo_all = __builtin_amdgcn_readlane(seen.lo, 31), hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
+    int lo = __builtin_amdgcn_readfirstlane(seen.lo) & ~(BN - 1), hi = __builtin_amdgcn_readlane(seen.hi, 31);
+    if (p.splits > 1) {
+        lo += split * p.pieces * kAttnFewKeys;
+        const int end = lo + p.pieces * kAttnFewKeys;
+        hi = hi < end ? hi : end;
+    }
+    const int d = p.d;
+    half8_t q[KK];
+    {
+        const _Float16 *row = p.q + b * p.qs[0] + i * p.qs[1] + (int64_t)(hk * p.group + g) * p.qs[2];
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            const int e = 16 * kk + 8 * (lane >> 5);
+            half8_t z = {};
+            q[kk] = alive && e < d ? *reinterpret_cast<const half8_t *>(row + e) : z;
+        }
+    }
+    AttnTile<DP, BN, 1> tk, tv;
+    tk.init(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, 0, lane);
+    tv.init(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, 0, lane);
+    AttnRows<DP> fk;
+    AttnCols<DP> fv;
+    fk.init(lane);
+    fv.init(lane);
+    const float c = p.scale * kAttnLog2e;
+    AttnSoftmax sm;
+    sm.init();
+    f32x16 acc[NT] = {};
+    char *mine = smem + wave * 4 * TILE;
+    int buf = 0;
+    int j0 = lo + wave * BN;
+    // rows past the last key load zeros, so every step has the same number of loads
+    tk.load(mine, j0, 0);
+    tv.load(mine + TILE, j0, 0);
+    for (; j0 < hi; j0 += WAVES * BN) {
+        char *next = mine + (buf ^ 1) * 2 * TILE;
+        tk.load(next, j0 + WAVES * BN, 0);
+        tv.load(next + TILE, j0 + WAVES * BN, 0);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NL) : "memory");
+        const char *ks = mine + buf * 2 * TILE, *vs = ks + TILE;
+        buf ^= 1;
+        f32x16 x = {};
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) x = mfma_32x32x16<E>(fk.read(ks, 0, kk), q[kk], x);
+        if (j0 < lo_all || j0 + BN > hi_all) {
+            const int from = seen.lo - j0, to = seen.hi - j0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int j = acc_row(e, lane >> 5);
+                x[e] = j >= from && j < to ? x[e] : -__builtin_inff();
+            }
+        }
+        float mx = x[0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) mx = fmaxf(mx, x[e]);
+        mx = both_max(mx) * c;
+        if (__builtin_amdgcn_ballot_w64(mx > sm.max + 8.0f)) {
+            const float m = fmaxf(sm.max, mx);
+            const float use = m == -__builtin_inff() ? 0.0f : m;
+            const float f = __builtin_amdgcn_exp2f(sm.max - use);
+            sm.max = m;
+            sm.use = use;
+            sm.sum *= f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[t][e] *= f;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], c, -sm.use));
+            sm.sum += x[e];
+        }
+        static_for<2>([&](auto step) {
+            constexpr int S = decltype(step)::value;
+            half8_t f[NT];
+            fv.template read<S>(vs, f);
+            const half8_t w = pack8<E>(x, S * 8);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = mfma_32x32x16<E>(f[t], w, acc[t]);
+        });
+    }
+    // the waves' results meet: [wave][row][element] sums, then [wave][row] (maximum, sum)
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    float *sums = reinterpret_cast<float *>(smem);
+    float2 *ml = reinterpret_cast<float2 *>(sums + WAVES * 32 * DP);
+    const float total = both_sum(sm.sum);
+    if (lane < 32) ml[wave * 32 + r] = make_float2(sm.max, total);
+    // 16-byte pieces exchange places so that the rows' equal elements lie in different banks
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const int piece = (32 * t + acc_row(e, lane >> 5)) >> 2;
+            *reinterpret_cast<f32x4 *>(sums + (wave * 32 + r) * DP + ((piece ^ (r & 7)) << 2)) =
+                f32x4{acc[t][e], acc[t][e + 1], acc[t][e + 2], acc[t][e + 3]};
+        }
+    __syncthreads();
+    const int pieces = d >> 2;
+    for (int at = threadIdx.x; at < p.rows * pieces; at += 256) {
+        const int row = at / pieces, e = (at - row * pieces) * 4;
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) m = fmaxf(m, ml[w * 32 + row].x);
+        const float use = m == -__builtin_inff() ? 0.0f : m;
+        float sum = 0.0f;
+        f32x4 v = {};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float2 x = ml[w * 32 + row];
+            const float f = __builtin_amdgcn_exp2f(x.x - use);
+            sum = fmaf(x.y, f, sum);
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(sums + (w * 32 + row) * DP + (((e >> 2) ^ (row & 7)) << 2));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = fmaf(a[k], f, v[k]);
+        }
+        if (p.splits > 1) {
+            const int64_t to = ((int64_t)split * heads + head) * p.rows + row;
+            *reinterpret_cast<f32x4 *>(p.part_o + to * d + e) = v;
+            if (e == 0) p.part_ml[to] = make_float2(m, sum);
+            continue;
+        }
+        const int ti = row / p.group, h = hk * p.group + row - ti * p.group;
+        const bool live = ti < s.queries;
+        const float inv = attn_inverse(sum);
+        if (e == 0 && p.lse)
+            p.lse[((int64_t)b * p.hq + h) * p.tq + ti] =
+                live ? (use + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -__builtin_inff();
+        half4_t o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = live ? from_f32<E>(v[k] * inv) : (_Float16)0.0f;
+        *reinterpret_cast<half4_t *>(p.o + b * p.os[0] + ti * p.os[1] + h * p.os[2] + e) = o;
+    }
+}
+
+// The pieces of each row's keys joined, in their order: a wave per row, two elements
+// per lane.
+template <typename E>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnParams p) {
+    const int heads = p.n * p.hk, lane = threadIdx.x & 63;
+    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), count = (int64_t)heads * p.rows;
+    if (unit >= count) return;
+    const int head = (int)(unit / p.rows), row = (int)(unit - (int64_t)head * p.rows);
+    const int b = head / p.hk, hk = head - b * p.hk;
+    const int ti = row / p.group, h = hk * p.group + row - ti * p.group;
+    const bool live = ti < attn_sample(p, b).queries;
+    float m = -__builtin_inff();
+    for (int k = lane; k < p.splits; k += 64) m = fmaxf(m, p.part_ml[k * count + unit].x);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+    const float use = m == -__builtin_inff() ? 0.0f : m;
+    const int e = 2 * lane;
+    float sum = 0.0f, v0 = 0.0f, v1 = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < p.splits; ++k) {
+        const float2 x = p.part_ml[k * count + unit];
+        const float f = __builtin_amdgcn_exp2f(x.x - use);
+        sum = fmaf(x.y, f, sum);
+        if (e < p.d) {
+            const float2 a = *reinterpret_cast<const float2 *>(p.part_o + (k * count + unit) * p.d + e);
+            v0 = fmaf(a.x, f, v0);
+            v1 = fmaf(a.y, f, v1);
+        }
+    }
+    const float inv = attn_inverse(sum);
+    if (lane == 0 && p.lse)
+        p.lse[((int64_t)b * p.hq + h) * p.tq + ti] =
+            live ? (use + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -__builtin_inff();
+    if (e < p.d) {
+        typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+        h2 o;
+        o[0] = live ? from_f32<E>(v0 * inv) : (_Float16)0.0f;
+        o[1] = live ? from_f32<E>(v1 * inv) : (_Float16)0.0f;
+        *reinterpret_cast<h2 *>(p.o + b * p.os[0] + ti * p.os[1] + h * p.os[2] + e) = o;
+    }
+}
+
+template <typename E, int DP>
+static void launch_forward(const AttnParams &p, bool few, hipStream_t s) {
+    const int heads = p.n * p.hk;
+    if (few) {
+        attention_few_kernel<E, DP><<<dim3(heads * p.splits), dim3(256), 0, s>>>(p);
+    } else {
+        const int tiles = (p.rows + kAttnTileRows - 1) / kAttnTileRows;
+        attention_tile_kernel<E, DP, kAttnTileRows / 32>
+            <<<dim3(heads * tiles, p.splits), dim3(kAttnTileRows * 2), 0, s>>>(p);
+    }
+    if (p.splits > 1) {
+        const int64_t count = (int64_t)heads * p.rows;
+        attention_join_kernel<E><<<dim3((uint32_t)((count + 3) / 4)), dim3(256), 0, s>>>(p);
+    }
+}
+
+template <typename E>
+static void launch_forward_dim(const AttnParams &p, bool few, hipStream_t s) {
+    if (p.d <= 32)
+        launch_forward<E, 32>(p, few, s);
+    else if (p.d <= 64)
+        launch_forward<E, 64>(p, few, s);
+    else if (p.d <= 96)
+        launch_forward<E, 96>(p, few, s);
+    else
+        launch_forward<E, 128>(p, few, s);
+}
+
+hipError_t launch_attention(const AttnParams &p, bool few, hipStream_t s) {
+    if (p.bf16)
+        launch_forward_dim<__bf16>(p, few, s);
+    else
+        launch_forward_dim<_Float16>(p, few, s);
+    return hipGetLastError();
+}
+
+}  // namespace c3d

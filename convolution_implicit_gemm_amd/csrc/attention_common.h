@@ -1,0 +1,252 @@
+// Device helpers of the attention kernels (attention.hip, attention_grad.hip):
+// which keys a query sees, tiles of rows in LDS and their MFMA fragments, and
+// exchanges between the halves of a wave.
+#pragma once
+
+#include "igemm_common.h"
+#include "token_internal.h"
+
+namespace c3d {
+
+// ---- rows.  The query heads that share a key head are rows of one problem:
+// row r of a (sample, key head) is query token r / group, query head r % group of
+// the key head's group.  Keys and values are then read once for all of them.
+
+// What a sample has and where its queries stand.
+struct AttnSample {
+    int queries, keys;  // of this sample
+    int64_t offset;     // position of query 0
+};
+__device__ __forceinline__ AttnSample attn_sample(const AttnParams &p, int b) {
+    AttnSample s{p.tq, p.tk, p.q_offset};
+    if (p.lengths) {
+        const int ql = p.lengths[2 * b], kl = p.lengths[2 * b + 1];
+        s.queries = ql < 0 ? 0 : ql < p.tq ? ql : p.tq;
+        s.keys = kl < 0 ? 0 : kl < p.tk ? kl : p.tk;
+    }
+    if (p.tail) s.offset += s.keys - s.queries;
+    return s;
+}
+
+// The keys [lo, hi) that query token i sees (lo <= hi): those up to the end of its own
+// frame, from `window` frames back.  Both ends grow with i.  Positions are below
+// 2^32 (the host checks).
+struct AttnRange {
+    int lo, hi;
+};
+__device__ __forceinline__ AttnRange attn_range(const AttnParams &p, const AttnSample &s, int i) {
+    if (!p.frame) return {0, s.keys};
+    const int64_t pos = s.offset + i;
+    if (pos < 0) return {0, 0};
+    const uint32_t f = (uint32_t)pos / (uint32_t)p.frame;
+    const uint64_t end = ((uint64_t)f + 1) * (uint32_t)p.frame;
+    const int hi = end < (uint64_t)s.keys ? (int)end : s.keys;
+    int lo = 0;
+    if (p.window && (uint64_t)f + 1 > (uint32_t)p.window) {
+        const uint64_t from = ((uint64_t)f + 1 - (uint32_t)p.window) * (uint32_t)p.frame;
+        lo = from < (uint64_t)s.keys ? (int)from : s.keys;
+    }
+    return {lo, hi};
+}
+
+// ---- tiles in LDS: rows of DP elements (the head's, then zeros), 2 DP bytes.
+// 16-byte chunk c of row r sits at chunk c ^ attn_swz(r): the 16 rows that a read of
+// one chunk touches at a time, and the 4 rows x 64 bytes of a transposing read, each
+// lie in different banks (16 chunks fill all of them once).
+template <int DP>
+__device__ __forceinline__ int attn_swz(int r) {
+    static_assert(DP == 32 || DP == 64 || DP == 96 || DP == 128, "padded head sizes");
+    if constexpr (DP == 128) return (r & 3) << 2 | ((r >> 2) & 3);
+    if constexpr (DP == 64) return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
+    return (r >> 2) & 3;
+}
+
+// Rows of a tensor on their way into LDS tiles of ROWS rows, by WAVES waves.
+template <int DP, int ROWS, int WAVES>
+struct AttnTile {
+    static constexpr int CH = DP / 8, LOADS = ROWS * CH / 64, NI = (LOADS + WAVES - 1) / WAVES;
+    static constexpr int BYTES = ROWS * DP * 2;
+    const _Float16 *base;  // row 0
+    int64_t stride;
+    int rows, dim;
+    uint32_t voff[NI];
+
+    __device__ __forceinline__ void init(const _Float16 *base_, int64_t stride_, int rows_, int dim_, int wave, int lane) {
+        base = base_;
+        stride = stride_;
+        rows = rows_;
+        dim = dim_;
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+            const int lin = (wave + j * WAVES) * 64 + lane;
+            const int r = lin / CH, c = (lin % CH) ^ attn_swz<DP>(r);
+            voff[j] = c * 8 < dim ? (uint32_t)(r * (int)stride + c * 8) * 2u : kOOB;
+        }
+    }
+    // rows [row0, row0 + ROWS) into lds; those past the end, and elements past the head, as zeros
+    __device__ __forceinline__ void load(char *lds, int row0, int wave) const {
+        const int left = rows - row0, n = left < ROWS ? left : ROWS;
+        const buf_rsrc r = make_rsrc(base + row0 * stride, n > 0 ? (uint32_t)((n - 1) * (int)stride + dim) * 2u : 0u);
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+            if (LOADS % WAVES == 0 || wave + j * WAVES < LOADS) dma16(r, lds + (wave + j * WAVES) * 1024, voff[j], 0u);
+    }
+};
+
+// The MFMA fragment of 32 rows x 16 elements, contraction along the row: lane l
+// holds row l % 32, elements 16 kk + 8 (l / 32) .. + 7.
+template <int DP>
+struct AttnRows {
+    uint32_t off;  // of chunk 0, without the swizzle
+    int swz, hi;
+    __device__ __forceinline__ void init(int lane) {
+        const int r = lane & 31;
+        off = r * DP * 2;
+        swz = attn_swz<DP>(r);
+        hi = lane >> 5;
+    }
+    __device__ __forceinline__ half8_t read(const char *tile, int row0, int kk) const {
+        return *reinterpret_cast<const half8_t *>(tile + row0 * DP * 2 + off + (((2 * kk + hi) ^ swz) << 4));
+    }
+};
+
+// Fragments with the rows as contraction: lane l holds column (element) l % 32 of
+// each group of 32, and of the 16 rows of a step rows 4 h .. + 3 and 8 + 4 h .. + 3,
+// h = l / 32: the order in which a 32 x 32 accumulator holds its rows, so that
+// probabilities go from one MFMA's result into the next one's operand in place.
+// ds_read_b64_tr_b16: within 16 lanes, lane j gives the address of 8 bytes of row
+// j / 4 and lane i receives column i of the 4 rows.  In assembly that waits for itself:
+// for the compiler's own form it would wait for every load into LDS still in flight.
+template <int DP>
+struct AttnCols {
+    static constexpr int NT = DP / 32, ROW = DP * 2;
+    uint32_t a0[NT], a1[NT];
+    __device__ __forceinline__ void init(int lane) {
+        const int j = lane & 15, g = (lane >> 4) & 1, h = lane >> 5;
+        const int r0 = 4 * h + (j >> 2), r1 = r0 + 8;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int c = 4 * t + 2 * g + ((j & 3) >> 1);
+            a0[t] = r0 * ROW + ((c ^ attn_swz<DP>(r0)) << 4) + (j & 1) * 8;
+            a1[t] = r1 * ROW + ((c ^ attn_swz<DP>(r1)) << 4) + (j & 1) * 8;
+        }
+    }
+    // the fragments of rows [16 S, 16 S + 16) of the tile
+    template <int S>
+    __device__ __forceinline__ void read(const char *tile, half8_t (&f)[NT]) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+        const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)tile;
+        uint64_t lo[NT], hi[NT];
+        if constexpr (NT == 4) {
+            asm volatile(
+                "ds_read_b64_tr_b16 %0, %8 offset:%16\n\tds_read_b64_tr_b16 %4, %12 offset:%16\n\t"
+                "ds_read_b64_tr_b16 %1, %9 offset:%16\n\tds_read_b64_tr_b16 %5, %13 offset:%16\n\t"
+                "ds_read_b64_tr_b16 %2, %10 offset:%16\n\tds_read_b64_tr_b16 %6, %14 offset:%16\n\t"
+                "ds_read_b64_tr_b16 %3, %11 offset:%16\n\tds_read_b64_tr_b16 %7, %15 offset:%16\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(lo[2]), "=&v"(lo[3]), "=&v"(hi[0]), "=&v"(hi[1]), "=&v"(hi[2]),
+                  "=&v"(hi[3])
+                : "v"(base + a0[0]), "v"(base + a0[1]), "v"(base + a0[2]), "v"(base + a0[3]), "v"(base + a1[0]),
+                  "v"(base + a1[1]), "v"(base + a1[2]), "v"(base + a1[3]), "n"(S * 16 * ROW)
+                : "memory");
+        } else if constexpr (NT == 3) {
+            asm volatile(
+                "ds_read_b64_tr_b16 %0, %6 offset:%12\n\tds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+                "ds_read_b64_tr_b16 %1, %7 offset:%12\n\tds_read_b64_tr_b16 %4, %10 offset:%12\n\t"
+                "ds_read_b64_tr_b16 %2, %8 offset:%12\n\tds_read_b64_tr_b16 %5, %11 offset:%12\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(lo[2]), "=&v"(hi[0]), "=&v"(hi[1]), "=&v"(hi[2])
+                : "v"(base + a0[0]), "v"(base + a0[1]), "v"(base + a0[2]), "v"(base + a1[0]), "v"(base + a1[1]),
+                  "v"(base + a1[2]), "n"(S * 16 * ROW)
+                : "memory");
+        } else if constexpr (NT == 2) {
+            asm volatile(
+                "ds_read_b64_tr_b16 %0, %4 offset:%8\n\tds_read_b64_tr_b16 %2, %6 offset:%8\n\t"
+                "ds_read_b64_tr_b16 %1, %5 offset:%8\n\tds_read_b64_tr_b16 %3, %7 offset:%8\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(hi[0]), "=&v"(hi[1])
+                : "v"(base + a0[0]), "v"(base + a0[1]), "v"(base + a1[0]), "v"(base + a1[1]), "n"(S * 16 * ROW)
+                : "memory");
+        } else {
+            asm volatile(
+                "ds_read_b64_tr_b16 %0, %2 offset:%4\n\tds_read_b64_tr_b16 %1, %3 offset:%4\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(lo[0]), "=&v"(hi[0])
+                : "v"(base + a0[0]), "v"(base + a1[0]), "n"(S * 16 * ROW)
+                : "memory");
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            f[t] = __builtin_shufflevector(__builtin_bit_cast(half4_t, lo[t]), __builtin_bit_cast(half4_t, hi[t]), 0, 1,
+                                           2, 3, 4, 5, 6, 7);
+#endif
+    }
+};
+
+// Row (of a 32 x 32 accumulator) that register i of a lane in half h holds.
+__device__ __forceinline__ constexpr int acc_row(int i, int h) { return (i & 3) + 8 * (i >> 2) + 4 * h; }
+
+// The values that lanes l % 32 and l % 32 + 32 hold, to both.
+struct Halves {
+    float low, high;
+    __device__ __forceinline__ explicit Halves(float v) : low(v), high(v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        uint32_t a = __builtin_bit_cast(uint32_t, v), b = a;
+        asm("" : "+v"(b));  // a swap of one value with itself: the compiler takes both results for the same
+        const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+        low = __builtin_bit_cast(float, (uint32_t)r[0]);
+        high = __builtin_bit_cast(float, (uint32_t)r[1]);
+#endif
+    }
+};
+__device__ __forceinline__ float both_max(float v) {
+    const Halves x(v);
+    return fmaxf(x.low, x.high);
+}
+__device__ __forceinline__ float both_sum(float v) {
+    const Halves x(v);
+    return x.low + x.high;
+}
+
+// Eight consecutive accumulator registers as an operand's fragment.
+template <typename E>
+__device__ __forceinline__ half8_t pack8(const f32x16 &v, int first) {
+    half8_t f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = from_f32<E>(v[first + e]);
+    return f;
+}
+
+// A column of an accumulator (32 elements of one output row, times `mul`) to
+// memory: lane l holds row l % 32's elements acc_row(i, l / 32); the halves swap so
+// that each writes 16 bytes at a time.  out: the row's element 0 of this tile; left: elements
+// of the head from there on.
+template <typename E>
+__device__ __forceinline__ void store_column(_Float16 *out, const f32x16 &v, float mul, int left, int lane, bool on) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const int h = lane >> 5;
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {  // elements 8 g .. 8 g + 15
+        uint32_t w[2][2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+                h2 t;
+                t[0] = from_f32<E>(v[4 * (g + q) + 2 * x] * mul);
+                t[1] = from_f32<E>(v[4 * (g + q) + 2 * x + 1] * mul);
+                w[q][x] = __builtin_bit_cast(uint32_t, t);
+            }
+        // half 0 takes elements 8 g .. + 7 (its own first four, the other's), half 1 the next eight
+        const auto r0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+        const auto r1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+        typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+        const u4 q = {r0[0], r1[0], r0[1], r1[1]};
+        const int e0 = 8 * (g + h);
+        if (on && e0 < left) *reinterpret_cast<u4 *>(out + e0) = q;
+    }
+#endif
+}
+
+}  // namespace c3d

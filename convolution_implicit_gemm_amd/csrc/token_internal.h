@@ -142,4 +142,64 @@ struct RopeParams {
 };
 hipError_t launch_rope3d(const RopeParams &p, hipStream_t s);
 
+// ---- attention
+constexpr int kAttnMaxDim = 128;
+struct AttnParams {
+    const _Float16 *q, *k, *v;
+    _Float16 *o;                 // backward: read
+    float *lse;                  // [n][heads_q][tq], forward: or null
+    const int32_t *lengths;      // [n][2] (queries, keys) or null
+    int64_t qs[3], ks[3], vs[3], os[3];  // sample, token, head, in elements
+    int64_t q_offset;
+    int32_t n, hq, hk, group, d, tq, tk;
+    int32_t rows;                // tq * group: the rows of one (sample, key head)
+    int32_t frame, window, tail, bf16;
+    float scale;
+    // forward: `splits` pieces of each row's keys; more than one leave partials
+    int32_t splits, pieces;      // pieces: keys of a piece, in tiles of the kernel
+    float *part_o;               // [splits][n * hk][rows][d] sums of unnormalised values
+    float2 *part_ml;             // [splits][n * hk][rows] (maximum, sum), in the exponent of 2
+    // backward
+    const _Float16 *dout;
+    _Float16 *dq, *dk, *dv;
+    float *nlse, *ndelta;        // [n * hk][rows] in the workspace
+};
+struct AttnKernel {
+    const char *name;
+    int rows, keys, threads;     // of a workgroup's tile
+};
+// few: all rows of a key head in one tile of kAttnFewRows
+constexpr int kAttnFewRows = 32, kAttnFewKeys = 128, kAttnTileRows = 256, kAttnTileKeys = 64;
+hipError_t launch_attention(const AttnParams &p, bool few, hipStream_t s);
+hipError_t launch_attention_grad(const AttnParams &p, hipStream_t s);
+
+// ---- adamw
+constexpr int kAdamwBlock = 128;    // elements that share a scale
+constexpr int kAdamwTensors = 48;   // of a launch: their table travels in the kernel's arguments (4 KiB)
+constexpr int kAdamwUnit = 2048;    // elements that a workgroup takes at a time
+struct AdamwTensor {
+    _Float16 *param;
+    float *master;
+    const void *grad;
+    void *m, *v;
+    uint8_t *m_scale, *v_scale;
+    int64_t count;
+    float decay;
+};
+struct AdamwHyper {
+    float grad_scale, beta1, rest1, beta2, rest2;  // rest: 1 - beta
+    float lr1;          // lr / (1 - beta1^step)
+    float root2;        // 1 / sqrt(1 - beta2^step)
+    float eps, lr_decay;  // lr * weight_decay
+};
+struct AdamwParams {
+    AdamwTensor t[kAdamwTensors];
+    int32_t first[kAdamwTensors];  // of each tensor's workgroups; INT32_MAX behind the last tensor
+    const AdamwHyper *device_hyper;
+    AdamwHyper hyper;
+    int32_t units;     // of kAdamwUnit elements to a workgroup
+};
+static_assert(sizeof(AdamwParams) <= 4096, "kernel arguments");
+hipError_t launch_adamw(const AdamwParams &p, int64_t blocks, bool bf16, bool state8, bool grad32, hipStream_t s);
+
 }  // namespace c3d

@@ -63,7 +63,11 @@ enum {
     CONV3D_F_CHUNK = 16u,          /* chunked causal decoding: see conv3d_forward_chunk */
     CONV3D_F_GN_STATS = 32u,       /* also write GroupNorm partial statistics of y: see below */
     CONV3D_F_PREACT = 64u,         /* linear only: keep the value before the activation */
-    CONV3D_F_POSITIONS = 128u      /* rope3d only: positions are given per token */
+    CONV3D_F_POSITIONS = 128u,     /* rope3d only: positions are given per token */
+    CONV3D_F_LENGTHS = 256u,       /* attention only: the samples' lengths are given */
+    CONV3D_F_TAIL = 512u,          /* attention only: the queries are a sample's last tokens */
+    CONV3D_F_STATE8 = 1024u,       /* adamw only: states in 8 bits */
+    CONV3D_F_GRAD32 = 2048u        /* adamw only: fp32 gradients */
 };
 
 /* Execution paths a plan may choose. */
@@ -470,6 +474,155 @@ conv3d_status rope3d_forward(rope3d_plan_t p, const void *q, const void *k, void
                              const void *positions, int32_t t_offset, void *stream);
 conv3d_status rope3d_backward(rope3d_plan_t p, const void *dq_out, const void *dk_out, void *dq, void *dk,
                               const void *positions, int32_t t_offset, void *stream);
+
+/*
+ * Attention of query tokens over key tokens:
+ *   o_i = sum_j exp(s_ij - lse_i) v_j,  s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij)
+ * over the keys j that query i sees.
+ *   q, o: [n][tq][heads_q][head_dim];  k, v: [n][tk][heads_k][head_dim]
+ *   lse:  fp32 [n][heads_q][tq] contiguous
+ * Query head h reads key head h / (heads_q / heads_k).  *_stride: elements between
+ * samples, tokens and heads of each tensor (multiples of 8; all three 0 for the
+ * contiguous layout above), so that heads can be read inside the rows of a fused
+ * projection, or lie heads first.
+ *   lengths: int32 [n][2] on the device (CONV3D_F_LENGTHS): the queries and keys of each
+ *     sample (clamped to 0 .. tq and 0 .. tk); otherwise every sample has tq and tk.
+ *     Tokens behind them are never read; o and the gradients are written as zeros
+ *     there, lse as -inf.
+ * What a query sees: with frame 0 every key of its sample.  Otherwise tokens count by
+ * frames of `frame` tokens: query i, at position p = q_offset + i (with CONV3D_F_TAIL
+ * the queries are the sample's last tokens, p = q_offset + keys - queries + i), sees the
+ * keys of its own frame and of those before it, at most `window` frames altogether
+ * (0: all).  frame = h w is attention causal by frames, with window = 1 each
+ * frame by itself; frame = 1 is causal token by token.  A query that sees no key has
+ * o = 0, lse = -inf and no part in any gradient.
+ * Arithmetic is fp32, o is rounded once; probabilities (and in the backward pass their
+ * gradients) are rounded to the element type as operands of the second products.
+ * Values that a query does not see do not reach it as long as they are finite: an
+ * infinite or NaN v in a sample may reach all queries of that sample.
+ */
+typedef struct {
+    int32_t n, heads_q, heads_k, head_dim;
+    int32_t tq, tk;        /* query and key tokens of a sample */
+    int32_t frame, window;
+    float scale;           /* 0: 1 / sqrt(head_dim) */
+    uint32_t flags;        /* CONV3D_F_BF16 | CONV3D_F_LENGTHS | CONV3D_F_TAIL */
+    int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+} attention_desc;
+
+typedef struct attention_plan_s *attention_plan_t; /* host-only, immutable */
+
+/* What a plan chose for the forward pass. */
+typedef struct {
+    int32_t tile_rows, tile_keys, threads;  /* rows: query tokens times query heads of a key head */
+    int32_t splits;                         /* pieces that each row's keys are split into */
+    int64_t grid;
+    size_t workspace_bytes, backward_workspace_bytes;
+    char kernel_name[64];
+} attention_plan_info;
+
+/*
+ * Validate *d and choose the kernels.  Host only.  *workspace_bytes: device workspace
+ * of attention_forward (0 if none).
+ * Errors: INVALID_ARG for null pointers, negative n, tq, tk, frame or window, heads_q
+ * not a positive multiple of heads_k, head_dim < 1, a scale that is negative or not
+ * finite, unknown flags, or strides that are negative, not a multiple of 8, or
+ * (between tokens, with more than one) shorter than a head; UNSUPPORTED for head_dim
+ * not a multiple of 8 or above 128, more than 16384 heads, 2^30 tokens or more (of a sample, times
+ * heads_q / heads_k for queries), token strides above 2^20, others of 2^40 or more, a tensor of 2^48
+ * elements or more from its first to its last, or more than 2^31 threads' work.
+ * Few rows against many keys split the keys over workgroups, which leave fp32
+ * partials in the workspace that a second small kernel joins in a fixed order.
+ */
+conv3d_status attention_plan(const attention_desc *d, attention_plan_t *out, size_t *workspace_bytes);
+conv3d_status attention_plan_query(attention_plan_t p, attention_plan_info *info);
+void attention_plan_destroy(attention_plan_t p);
+
+/*
+ * Enqueue o and, unless lse is null, lse on stream.  lengths is required with
+ * CONV3D_F_LENGTHS, otherwise ignored.  o and lse must not overlap an input or
+ * each other, nor o itself through its strides.  The workspace is scratch; calls on
+ * different streams must not share one.
+ * Errors: INVALID_ARG (null or misaligned pointers, |q_offset| above 2^30, overlaps),
+ * WORKSPACE, HIP.
+ */
+conv3d_status attention_forward(attention_plan_t p, const void *q, const void *k, const void *v, void *o, void *lse,
+                                const void *lengths, int64_t q_offset, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/*
+ * The gradients from dout, the gradient of o (o's strides), and what the forward
+ * pass gave (o and lse, which is required here), with the probabilities computed again:
+ *   P = exp(s - lse),  dS = P * (dout v^T - rowsum(dout * o)),
+ *   dq = scale dS k,  dk = scale dS^T q,  dv = P^T dout
+ * dq, dk and dv have the strides of q, k and v; those of shared key heads are summed
+ * over their query heads.  Each may be null and is then not computed.  Sums run in a fixed order:
+ * results do not vary from call to call.
+ * Errors: as attention_forward, and INVALID_ARG if every gradient is null.
+ */
+size_t attention_backward_workspace(attention_plan_t p);
+conv3d_status attention_backward(attention_plan_t p, const void *dout, const void *q, const void *k, const void *v,
+                                 const void *o, const void *lse, void *dq, void *dk, void *dv, const void *lengths,
+                                 int64_t q_offset, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The AdamW step over many tensors at once.  For every element of weight w, gradient
+ * grad and states m, v, in fp32:
+ *   g = grad_scale grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   w = w - lr (weight_decay decay w + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps))
+ * The weights are master (fp32) where it is given, and param, where given too, is
+ * their rounded copy; without a master, param alone holds them, rounded at every step.
+ *   param: fp16 / bf16 [count] or null;  master: fp32 [count] or null; one of them is given
+ *   grad:  fp16 / bf16 [count], or fp32 with CONV3D_F_GRAD32
+ *   m, v:  fp32 [count]; with CONV3D_F_STATE8 OCP e4m3 [count], with a scale for each
+ *          block of 128 elements (the last one may be shorter): uint8 [(count + 127) / 128]
+ * In 8 bits a block's byte s and codes c stand for m = c 2^(s - 127) and sqrt(v) =
+ * c 2^(s - 127), s - 127 the least power (from -126 on) at which the block's largest value is
+ * 448 or less; values are rounded to nearest, and a positive sqrt(v) never to 0, so that no step divides
+ * by a state that vanished.  Zero bytes are the states before the first step.  The step itself
+ * uses the states before they are rounded.  A value that is not finite becomes a NaN code and
+ * does not count for its block's scale.
+ */
+typedef struct {
+    void *param, *master;
+    const void *grad;
+    void *m, *v, *m_scale, *v_scale;
+    int64_t count;
+    float decay; /* times weight_decay; usually 1 for weights, 0 for biases and norms */
+} adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay, grad_scale;
+    int64_t step; /* from 1 on */
+} adamw_hyper;
+
+/* The tensors of a step, checked once.  Host-only and immutable; it holds the tensors'
+ * addresses, which have to stay valid as long as it is used. */
+typedef struct adamw_plan_s *adamw_plan_t;
+
+/*
+ * Errors: INVALID_ARG for null pointers, count < 0, neither param nor master, a decay that
+ * is negative or not finite, misaligned pointers (16 bytes, scales 1), unknown flags, or
+ * tensors that overlap (gradients may overlap each other); UNSUPPORTED for 2^40 elements or more.
+ */
+conv3d_status adamw_plan(const adamw_tensor *tensors, int32_t count, uint32_t flags, adamw_plan_t *out);
+void adamw_plan_destroy(adamw_plan_t p);
+
+/* The numbers that the kernels take, as fp32 (computed in 64 bits). */
+enum { ADAMW_DEVICE_HYPER = 9 };
+/* INVALID_ARG for lr, eps or weight_decay negative or not finite, betas outside [0, 1), a
+ * grad_scale that is not finite, or step < 1. */
+conv3d_status adamw_hyper_pack(const adamw_hyper *h, float *out);
+
+/*
+ * Enqueue one step on stream: a launch for every 48 tensors.  The hyperparameters are those
+ * of *hyper, or, if device_hyper is not null, the ADAMW_DEVICE_HYPER floats of adamw_hyper_pack that
+ * device memory holds when the step runs (so that a captured step can be replayed
+ * with others; hyper is then ignored).
+ * Errors: INVALID_ARG (as adamw_hyper_pack; a misaligned (4) device_hyper, or one that overlaps
+ * a tensor that is written), HIP.
+ */
+conv3d_status adamw_step(adamw_plan_t p, const adamw_hyper *hyper, const void *device_hyper, void *stream);
 
 /*
  * Measurement aids, not on the convolution path: the ceilings of the machine
