@@ -78,9 +78,7 @@ __global__ __launch_bounds__(WAVES * 64) void attention_tile_kernel(AttnParams p
             q[kk] = alive && e < d ? *reinterpret_cast<const half8_t *>(row + e) : z;
         }
     }
-    AttnTile<DP, BN, WAVES> tk, tv;
-    tk.init(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane);
-    tv.init(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
+    const AttnTile<DP, BN, WAVES> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane), tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
     AttnRows<DP> fk;
     AttnCols<DP> fv;
     fk.init(lane);
@@ -105,11 +103,12 @@ __global__ __launch_bounds__(WAVES * 64) void attention_tile_kernel(AttnParams p
             tv.load(next + TILE, j0 + BN, wave);
         }
         if (j0 + BN <= wave_lo || j0 >= wave_hi) continue;
+        const uint32_t kr = lds_address(ks) + fk.off;
         f32x16 x[2] = {};
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) x[t] = mfma_32x32x16<E>(fk.read(ks, 32 * t, kk), q[kk], x[t]);
+            for (int t = 0; t < 2; ++t) x[t] = mfma_32x32x16<E>(fk.read(kr, 32 * t, kk), q[kk], x[t]);
         if (j0 < wave_lo_all || j0 + BN > wave_hi_all) {
             const int from = seen.lo - j0, to = seen.hi - j0;
 #pragma unroll
@@ -224,9 +223,7 @@ __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
             q[kk] = alive && e < d ? *reinterpret_cast<const half8_t *>(row + e) : z;
         }
     }
-    AttnTile<DP, BN, 1> tk, tv;
-    tk.init(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, 0, lane);
-    tv.init(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, 0, lane);
+    const AttnTile<DP, BN, 1> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, 0, lane), tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, 0, lane);
     AttnRows<DP> fk;
     AttnCols<DP> fv;
     fk.init(lane);
@@ -248,9 +245,10 @@ __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NL) : "memory");
         const char *ks = mine + buf * 2 * TILE, *vs = ks + TILE;
         buf ^= 1;
+        const uint32_t kr = lds_address(ks) + fk.off;
         f32x16 x = {};
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) x = mfma_32x32x16<E>(fk.read(ks, 0, kk), q[kk], x);
+        for (int kk = 0; kk < KK; ++kk) x = mfma_32x32x16<E>(fk.read(kr, 0, kk), q[kk], x);
         if (j0 < lo_all || j0 + BN > hi_all) {
             const int from = seen.lo - j0, to = seen.hi - j0;
 #pragma unroll

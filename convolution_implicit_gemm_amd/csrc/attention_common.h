@@ -61,23 +61,31 @@ __device__ __forceinline__ int attn_swz(int r) {
     return (r >> 2) & 3;
 }
 
-// Rows of a tensor on their way into LDS tiles of ROWS rows, by WAVES waves.
+// The lane as the compiler cannot see through it: what is worked out of it is worked out where it
+// is used, and not kept in registers across a kernel's loop.
+__device__ __forceinline__ int opaque(int v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(v));
+#endif
+    return v;
+}
+
+// Rows of a tensor straight into LDS tiles of ROWS rows, by WAVES waves.
 template <int DP, int ROWS, int WAVES>
 struct AttnTile {
     static constexpr int CH = DP / 8, LOADS = ROWS * CH / 64, NI = (LOADS + WAVES - 1) / WAVES;
-    static constexpr int BYTES = ROWS * DP * 2;
+    static constexpr int STEP = WAVES * 64 / CH;  // rows from one of a lane's loads to the next
+    // where these rows swizzle alike one offset does for all loads, each with a resource of its own
+    static constexpr bool ONE = WAVES * 64 % CH == 0 && STEP % 16 == 0;
     const _Float16 *base;  // row 0
     int64_t stride;
     int rows, dim;
-    uint32_t voff[NI];
+    uint32_t voff[ONE ? 1 : NI];
 
-    __device__ __forceinline__ void init(const _Float16 *base_, int64_t stride_, int rows_, int dim_, int wave, int lane) {
-        base = base_;
-        stride = stride_;
-        rows = rows_;
-        dim = dim_;
+    __device__ __forceinline__ AttnTile(const _Float16 *base_, int64_t stride_, int rows_, int dim_, int wave, int lane)
+        : base(base_), stride(stride_), rows(rows_), dim(dim_) {
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
+        for (int j = 0; j < (ONE ? 1 : NI); ++j) {
             const int lin = (wave + j * WAVES) * 64 + lane;
             const int r = lin / CH, c = (lin % CH) ^ attn_swz<DP>(r);
             voff[j] = c * 8 < dim ? (uint32_t)(r * (int)stride + c * 8) * 2u : kOOB;
@@ -85,28 +93,40 @@ struct AttnTile {
     }
     // rows [row0, row0 + ROWS) into lds; those past the end, and elements past the head, as zeros
     __device__ __forceinline__ void load(char *lds, int row0, int wave) const {
-        const int left = rows - row0, n = left < ROWS ? left : ROWS;
-        const buf_rsrc r = make_rsrc(base + row0 * stride, n > 0 ? (uint32_t)((n - 1) * (int)stride + dim) * 2u : 0u);
 #pragma unroll
-        for (int j = 0; j < NI; ++j)
-            if (LOADS % WAVES == 0 || wave + j * WAVES < LOADS) dma16(r, lds + (wave + j * WAVES) * 1024, voff[j], 0u);
+        for (int j = 0; j < NI; ++j) {
+            const int first = row0 + (ONE ? j * STEP : 0), most = ONE && STEP < ROWS ? STEP : ROWS;
+            const int left = rows - first, n = left < most ? left : most;
+            const buf_rsrc rs = make_rsrc(base + first * stride, n > 0 ? (uint32_t)((n - 1) * (int)stride + dim) * 2u : 0u);
+            if (LOADS % WAVES == 0 || wave + j * WAVES < LOADS)
+                dma16(rs, lds + (wave + j * WAVES) * 1024, voff[ONE ? 0 : j], 0u);
+        }
     }
 };
+
+__device__ __forceinline__ uint32_t lds_address(const char *p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)p;
+}
 
 // The MFMA fragment of 32 rows x 16 elements, contraction along the row: lane l
 // holds row l % 32, elements 16 kk + 8 (l / 32) .. + 7.
 template <int DP>
 struct AttnRows {
-    uint32_t off;  // of chunk 0, without the swizzle
-    int swz, hi;
+    // chunk bits that the swizzle changes: the others are added
+    static constexpr int XOR = DP == 128 ? 7 : DP == 64 ? 3 : 1;
+    uint32_t off;  // of kk = 0
     __device__ __forceinline__ void init(int lane) {
         const int r = lane & 31;
-        off = r * DP * 2;
-        swz = attn_swz<DP>(r);
-        hi = lane >> 5;
+        off = r * DP * 2 + (((lane >> 5) ^ attn_swz<DP>(r)) << 4);
     }
-    __device__ __forceinline__ half8_t read(const char *tile, int row0, int kk) const {
-        return *reinterpret_cast<const half8_t *>(tile + row0 * DP * 2 + off + (((2 * kk + hi) ^ swz) << 4));
+    // tile + off of a tile (which lies on 256 bytes), and row0 of its rows
+    static __device__ __forceinline__ half8_t read(uint32_t at, int row0, int kk) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        typedef const __attribute__((address_space(3))) half8_t lds_half8;
+        return *(lds_half8 *)((at ^ ((kk & XOR) << 5)) + (uint32_t)((kk & ~XOR) * 32 + row0 * DP * 2));
+#else
+        return half8_t{};
+#endif
     }
 };
 
@@ -117,63 +137,50 @@ struct AttnRows {
 // ds_read_b64_tr_b16: within 16 lanes, lane j gives the address of 8 bytes of row
 // j / 4 and lane i receives column i of the 4 rows.  In assembly that waits for itself:
 // for the compiler's own form it would wait for every load into LDS still in flight.
+#define C3D_TR(d, a, o) "ds_read_b64_tr_b16 %" #d ", %" #a " offset:%" #o "\n\t"
 template <int DP>
 struct AttnCols {
     static constexpr int NT = DP / 32, ROW = DP * 2;
-    uint32_t a0[NT], a1[NT];
+    static constexpr bool XOR = DP == 128 || DP == 64;  // the column group's bits are swizzled
+    uint32_t off0, off1;  // rows 4 h .. and 8 + 4 h .. of a step, column group 0
     __device__ __forceinline__ void init(int lane) {
         const int j = lane & 15, g = (lane >> 4) & 1, h = lane >> 5;
-        const int r0 = 4 * h + (j >> 2), r1 = r0 + 8;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int c = 4 * t + 2 * g + ((j & 3) >> 1);
-            a0[t] = r0 * ROW + ((c ^ attn_swz<DP>(r0)) << 4) + (j & 1) * 8;
-            a1[t] = r1 * ROW + ((c ^ attn_swz<DP>(r1)) << 4) + (j & 1) * 8;
-        }
+        const int r0 = 4 * h + (j >> 2), r1 = r0 + 8, c = 2 * g + ((j & 3) >> 1);
+        off0 = r0 * ROW + ((c ^ attn_swz<DP>(r0)) << 4) + (j & 1) * 8;
+        off1 = r1 * ROW + ((c ^ attn_swz<DP>(r1)) << 4) + (j & 1) * 8;
     }
+    static __device__ __forceinline__ uint32_t group(uint32_t at, int t) { return XOR ? at ^ (t << 6) : at + (t << 6); }
     // the fragments of rows [16 S, 16 S + 16) of the tile
     template <int S>
     __device__ __forceinline__ void read(const char *tile, half8_t (&f)[NT]) const {
 #if defined(__HIP_DEVICE_COMPILE__)
-        const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)tile;
+        const uint32_t b0 = lds_address(tile) + off0, b1 = lds_address(tile) + off1;
         uint64_t lo[NT], hi[NT];
         if constexpr (NT == 4) {
-            asm volatile(
-                "ds_read_b64_tr_b16 %0, %8 offset:%16\n\tds_read_b64_tr_b16 %4, %12 offset:%16\n\t"
-                "ds_read_b64_tr_b16 %1, %9 offset:%16\n\tds_read_b64_tr_b16 %5, %13 offset:%16\n\t"
-                "ds_read_b64_tr_b16 %2, %10 offset:%16\n\tds_read_b64_tr_b16 %6, %14 offset:%16\n\t"
-                "ds_read_b64_tr_b16 %3, %11 offset:%16\n\tds_read_b64_tr_b16 %7, %15 offset:%16\n\t"
-                "s_waitcnt lgkmcnt(0)"
-                : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(lo[2]), "=&v"(lo[3]), "=&v"(hi[0]), "=&v"(hi[1]), "=&v"(hi[2]),
-                  "=&v"(hi[3])
-                : "v"(base + a0[0]), "v"(base + a0[1]), "v"(base + a0[2]), "v"(base + a0[3]), "v"(base + a1[0]),
-                  "v"(base + a1[1]), "v"(base + a1[2]), "v"(base + a1[3]), "n"(S * 16 * ROW)
-                : "memory");
+            asm volatile(C3D_TR(0, 8, 16) C3D_TR(4, 12, 16) C3D_TR(1, 9, 16) C3D_TR(5, 13, 16) C3D_TR(2, 10, 16)
+                             C3D_TR(6, 14, 16) C3D_TR(3, 11, 16) C3D_TR(7, 15, 16) "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(lo[2]), "=&v"(lo[3]), "=&v"(hi[0]), "=&v"(hi[1]), "=&v"(hi[2]),
+                           "=&v"(hi[3])
+                         : "v"(group(b0, 0)), "v"(group(b0, 1)), "v"(group(b0, 2)), "v"(group(b0, 3)), "v"(group(b1, 0)),
+                           "v"(group(b1, 1)), "v"(group(b1, 2)), "v"(group(b1, 3)), "n"(S * 16 * ROW)
+                         : "memory");
         } else if constexpr (NT == 3) {
-            asm volatile(
-                "ds_read_b64_tr_b16 %0, %6 offset:%12\n\tds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
-                "ds_read_b64_tr_b16 %1, %7 offset:%12\n\tds_read_b64_tr_b16 %4, %10 offset:%12\n\t"
-                "ds_read_b64_tr_b16 %2, %8 offset:%12\n\tds_read_b64_tr_b16 %5, %11 offset:%12\n\t"
-                "s_waitcnt lgkmcnt(0)"
-                : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(lo[2]), "=&v"(hi[0]), "=&v"(hi[1]), "=&v"(hi[2])
-                : "v"(base + a0[0]), "v"(base + a0[1]), "v"(base + a0[2]), "v"(base + a1[0]), "v"(base + a1[1]),
-                  "v"(base + a1[2]), "n"(S * 16 * ROW)
-                : "memory");
+            asm volatile(C3D_TR(0, 6, 12) C3D_TR(3, 9, 12) C3D_TR(1, 7, 12) C3D_TR(4, 10, 12) C3D_TR(2, 8, 12)
+                             C3D_TR(5, 11, 12) "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(lo[2]), "=&v"(hi[0]), "=&v"(hi[1]), "=&v"(hi[2])
+                         : "v"(group(b0, 0)), "v"(group(b0, 1)), "v"(group(b0, 2)), "v"(group(b1, 0)), "v"(group(b1, 1)),
+                           "v"(group(b1, 2)), "n"(S * 16 * ROW)
+                         : "memory");
         } else if constexpr (NT == 2) {
-            asm volatile(
-                "ds_read_b64_tr_b16 %0, %4 offset:%8\n\tds_read_b64_tr_b16 %2, %6 offset:%8\n\t"
-                "ds_read_b64_tr_b16 %1, %5 offset:%8\n\tds_read_b64_tr_b16 %3, %7 offset:%8\n\t"
-                "s_waitcnt lgkmcnt(0)"
-                : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(hi[0]), "=&v"(hi[1])
-                : "v"(base + a0[0]), "v"(base + a0[1]), "v"(base + a1[0]), "v"(base + a1[1]), "n"(S * 16 * ROW)
-                : "memory");
+            asm volatile(C3D_TR(0, 4, 8) C3D_TR(2, 6, 8) C3D_TR(1, 5, 8) C3D_TR(3, 7, 8) "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(hi[0]), "=&v"(hi[1])
+                         : "v"(group(b0, 0)), "v"(group(b0, 1)), "v"(group(b1, 0)), "v"(group(b1, 1)), "n"(S * 16 * ROW)
+                         : "memory");
         } else {
-            asm volatile(
-                "ds_read_b64_tr_b16 %0, %2 offset:%4\n\tds_read_b64_tr_b16 %1, %3 offset:%4\n\t"
-                "s_waitcnt lgkmcnt(0)"
-                : "=&v"(lo[0]), "=&v"(hi[0])
-                : "v"(base + a0[0]), "v"(base + a1[0]), "n"(S * 16 * ROW)
-                : "memory");
+            asm volatile(C3D_TR(0, 2, 4) C3D_TR(1, 3, 4) "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(lo[0]), "=&v"(hi[0])
+                         : "v"(b0), "v"(b1), "n"(S * 16 * ROW)
+                         : "memory");
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -182,6 +189,7 @@ struct AttnCols {
 #endif
     }
 };
+#undef C3D_TR
 
 // Row (of a 32 x 32 accumulator) that register i of a lane in half h holds.
 __device__ __forceinline__ constexpr int acc_row(int i, int h) { return (i & 3) + 8 * (i >> 2) + 4 * h; }

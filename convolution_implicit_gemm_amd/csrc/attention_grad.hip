@@ -82,9 +82,7 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dq_kernel(AttnParams p) 
         }
     }
     if (!p.dq) return;  // only the rows' sums were asked for
-    AttnTile<DP, BN, WAVES> tk, tv;
-    tk.init(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane);
-    tv.init(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
+    const AttnTile<DP, BN, WAVES> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane), tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
     AttnRows<DP> fr;
     AttnCols<DP> fc;
     fr.init(lane);
@@ -98,7 +96,7 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dq_kernel(AttnParams p) 
     }
     for (int j0 = lo; j0 < hi; j0 += BN) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const char *ks = smem + buf * 2 * TILE, *vs = ks + TILE;
+        const char *ks = smem + buf * 2 * TILE;
         buf ^= 1;
         if (j0 + BN < hi) {
             char *next = smem + buf * 2 * TILE;
@@ -107,6 +105,7 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dq_kernel(AttnParams p) 
         }
         if (j0 + BN <= wave_lo || j0 >= wave_hi) continue;
         const bool edge = j0 < wave_lo_all || j0 + BN > wave_hi_all;
+        const uint32_t kr = lds_address(ks) + fr.off;
         static_for<2>([&](auto sub) {
             constexpr int T = decltype(sub)::value;
             f32x16 x = {}, y;
@@ -114,8 +113,8 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dq_kernel(AttnParams p) 
             for (int e = 0; e < 16; ++e) y[e] = -delta;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                x = mfma_32x32x16<E>(fr.read(ks, 32 * T, kk), q[kk], x);
-                y = mfma_32x32x16<E>(fr.read(vs, 32 * T, kk), go[kk], y);
+                x = mfma_32x32x16<E>(fr.read(kr, 32 * T, kk), q[kk], x);
+                y = mfma_32x32x16<E>(fr.read(kr, BN + 32 * T, kk), go[kk], y);
             }
             if (edge) {
                 const int from = seen.lo - j0, to = seen.hi - j0;
@@ -147,24 +146,27 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dq_kernel(AttnParams p) 
     for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, acc[t], p.scale, d - 32 * t, lane, true);
 }
 
-// ---- dk, dv: WAVES x 32 keys, wave w holds keys 32 w .. + 31 (k and v in registers, one
-// key per lane of every result) and all waves share the tile of 64 query tokens in LDS;
-// the query heads of the key head are taken one after the other.  S = Q K^T and dP =
-// dout V^T; P and dS are, as they stand, the operands of dv^T = dout^T P and dk^T = Q^T dS.
+// ---- dk, dv: WAVES x 32 keys, wave w holds keys 32 w .. + 31 (one key per lane of every
+// result) and all waves share the tile of 64 query tokens in LDS; the query heads of the
+// key head are taken one after the other.  S = Q K^T and dP = dout V^T; P and dS are,
+// as they stand, the operands of dv^T = dout^T P and dk^T = Q^T dS.
 template <typename E, int DP, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void attention_dkv_kernel(AttnParams p) {
-    constexpr int BM = 64, NT = DP / 32, KK = DP / 16, TILE = BM * DP * 2;
-    __shared__ __attribute__((aligned(1024))) char smem[4 * TILE + 4 * BM * 4];
-    float *rows_at = reinterpret_cast<float *>(smem + 4 * TILE);  // [2][nlse, ndelta][BM]
+__global__ __launch_bounds__(WAVES * 64, 2) void attention_dkv_kernel(AttnParams p) {
+    constexpr int BM = 64, NT = DP / 32, KK = DP / 16, TILE = BM * DP * 2, BN = WAVES * 32;
+    constexpr bool KLDS = DP > 64;  // k in LDS: with both in registers two waves would not fit a SIMD
+    constexpr int KBYTES = KLDS ? BN * DP * 2 : 0;
+    __shared__ __attribute__((aligned(1024))) char smem[KBYTES + 4 * TILE + 4 * BM * 4];
+    char *tiles = smem + KBYTES;
+    float *rows_at = reinterpret_cast<float *>(tiles + 4 * TILE);  // [2][nlse, ndelta][BM]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int heads = p.n * p.hk;
     const int head = blockIdx.x % heads, tile = blockIdx.x / heads;  // the longest of a masked problem first
     const int b = head / p.hk, hk = head % p.hk;
     const AttnSample s = attn_sample(p, b);
-    const int j0 = tile * WAVES * 32, j = j0 + wave * 32 + (lane & 31);
+    const int j0 = tile * BN, j = j0 + wave * 32 + (lane & 31);
     const bool alive = j < s.keys;
-    // the query tokens [lo, hi) that see key j
+    // the query tokens [lo, hi) that see a key
     auto seen_by = [&](int key) -> AttnRange {
         if (!p.frame) return {0, s.queries};
         const int64_t f = (uint32_t)key / (uint32_t)p.frame;
@@ -180,13 +182,13 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dkv_kernel(AttnParams p)
     int lo = 0, hi = 0;
     if (j0 <= last) {
         lo = seen_by(j0).lo & ~(BM - 1);
-        const int jl = j0 + WAVES * 32 - 1;
+        const int jl = j0 + BN - 1;
         hi = seen_by(jl < last ? jl : last).hi;
     }
     const int wave_lo = __builtin_amdgcn_readfirstlane(seen.lo), wave_hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
     const int wave_lo_all = __builtin_amdgcn_readlane(seen.lo, 31), wave_hi = __builtin_amdgcn_readlane(seen.hi, 31);
     const int d = p.d;
-    half8_t k[KK], v[KK];
+    half8_t k[KLDS ? 1 : KK], v[KK];
     {
         const _Float16 *rk = p.k + b * p.ks[0] + j * p.ks[1] + hk * p.ks[2];
         const _Float16 *rv = p.v + b * p.vs[0] + j * p.vs[1] + hk * p.vs[2];
@@ -194,9 +196,13 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dkv_kernel(AttnParams p)
         for (int kk = 0; kk < KK; ++kk) {
             const int e = 16 * kk + 8 * (lane >> 5);
             half8_t z = {};
-            k[kk] = alive && e < d ? *reinterpret_cast<const half8_t *>(rk + e) : z;
+            if constexpr (!KLDS) k[kk] = alive && e < d ? *reinterpret_cast<const half8_t *>(rk + e) : z;
             v[kk] = alive && e < d ? *reinterpret_cast<const half8_t *>(rv + e) : z;
         }
+    }
+    if constexpr (KLDS) {
+        const AttnTile<DP, BN, WAVES> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane);
+        tk.load(smem, j0, wave);
     }
     AttnRows<DP> fr;
     AttnCols<DP> fc;
@@ -204,46 +210,44 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dkv_kernel(AttnParams p)
     fc.init(lane);
     const float c = p.scale * kAttnLog2e;
     f32x16 ak[NT] = {}, av[NT] = {};
-    AttnTile<DP, BM, WAVES> tq, tg;
-    int buf = 0;
-    auto load = [&](int at, int head_q, int i0) {
-        char *to = smem + at * 2 * TILE;
+    AttnTile<DP, BM, WAVES> tq(nullptr, p.qs[1], s.queries, d, wave, lane), tg(nullptr, p.os[1], s.queries, d, wave, lane);
+    const int steps = hi > lo ? (hi - lo + BM - 1) / BM : 0, total = steps * p.group;
+    int load_g = 0, load_step = 0;
+    auto load = [&](int at) {  // the next tile of the sequence
+        const int h = hk * p.group + load_g, i0 = lo + load_step * BM;
+        char *to = tiles + at * 2 * TILE;
+        tq.base = p.q + b * p.qs[0] + h * p.qs[2];
+        tg.base = p.dout + b * p.os[0] + h * p.os[2];
         tq.load(to, i0, wave);
         tg.load(to + TILE, i0, wave);
         // a row's two numbers: waves 0 and 1, one row per lane
         if (wave < 2) {
-            const float *from = (wave ? p.ndelta : p.nlse) + ((int64_t)b * p.hq + head_q) * p.tq + i0;
+            const float *from = (wave ? p.ndelta : p.nlse) + ((int64_t)b * p.hq + h) * p.tq + i0;
             const int left = s.queries - i0;
             const buf_rsrc rs = make_rsrc(from, left > 0 ? (uint32_t)(left < BM ? left : BM) * 4u : 0u);
 #if defined(__HIP_DEVICE_COMPILE__)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(rows_at + (at * 2 + wave) * BM), 4, lane * 4, 0, 0, 0);
 #endif
         }
+        if (++load_step == steps) {
+            load_step = 0;
+            ++load_g;
+        }
     };
-    const int steps = hi > lo ? (hi - lo + BM - 1) / BM : 0, total = steps * p.group;
-    auto aim = [&](int g) {
-        const int h = hk * p.group + g;
-        tq.init(p.q + b * p.qs[0] + h * p.qs[2], p.qs[1], s.queries, d, wave, lane);
-        tg.init(p.dout + b * p.os[0] + h * p.os[2], p.os[1], s.queries, d, wave, lane);
-    };
-    int g = 0, step = 0;
-    if (total) {
-        aim(0);
-        load(0, hk * p.group, lo);
-    }
+    int buf = 0, step = 0;
+    if (total) load(0);
     for (int n = 0; n < total; ++n) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const char *qs = smem + buf * 2 * TILE, *gs = qs + TILE;
+        const char *qs = tiles + buf * 2 * TILE, *gs = qs + TILE;
         const float *starts = rows_at + buf * 2 * BM;
         const int i0 = lo + step * BM;
         buf ^= 1;
-        if (++step == steps) {
-            step = 0;
-            if (++g < p.group) aim(g);
-        }
-        if (n + 1 < total) load(buf, hk * p.group + g, lo + step * BM);
+        if (++step == steps) step = 0;
+        if (n + 1 < total) load(buf);
         if (i0 + BM <= wave_lo || i0 >= wave_hi) continue;
         const bool edge = i0 < wave_lo_all || i0 + BM > wave_hi_all;
+        const uint32_t qr = lds_address(qs) + fr.off;
+        const uint32_t kr = opaque(lds_address(smem) + wave * 32 * DP * 2 + fr.off);
         static_for<2>([&](auto sub) {
             constexpr int T = decltype(sub)::value;
             f32x16 x, y;
@@ -259,8 +263,11 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dkv_kernel(AttnParams p)
             }
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                x = mfma_32x32x16<E>(fr.read(qs, 32 * T, kk), k[kk], x);
-                y = mfma_32x32x16<E>(fr.read(gs, 32 * T, kk), v[kk], y);
+                if constexpr (KLDS)
+                    x = mfma_32x32x16<E>(fr.read(qr, 32 * T, kk), fr.read(kr, 0, kk), x);
+                else
+                    x = mfma_32x32x16<E>(fr.read(qr, 32 * T, kk), k[kk], x);
+                y = mfma_32x32x16<E>(fr.read(qr, BM + 32 * T, kk), v[kk], y);
             }
             if (edge) {
                 const int from = seen.lo - i0, to = seen.hi - i0;
@@ -314,7 +321,7 @@ static void launch_grad(const AttnParams &p, hipStream_t s) {
         attention_dq_kernel<E, DP, kAttnTileRows / 32><<<dim3(heads * tiles), dim3(kAttnTileRows * 2), 0, s>>>(p);
     }
     if (p.tk > 0 && (p.dk || p.dv))
-        attention_dkv_kernel<E, DP, 4><<<dim3(heads * ((p.tk + 127) / 128)), dim3(256), 0, s>>>(p);
+        attention_dkv_kernel<E, DP, 8><<<dim3(heads * ((p.tk + 255) / 256)), dim3(512), 0, s>>>(p);
 }
 
 template <typename E>
