@@ -25,49 +25,64 @@ struct AttnSoftmax {
         use = 0.0f;
         sum = 0.0f;
     }
+    // the maximum up to m; the factor of what was summed before
+    __device__ __forceinline__ float raise(float m) {
+        const float before = max;
+        max = fmaxf(max, m);
+        use = max == -__builtin_inff() ? 0.0f : max;
+        const float f = __builtin_amdgcn_exp2f(before - use);
+        sum *= f;
+        return f;
+    }
 };
 
 // 1 / sum; 0 for a row that saw no key.
 __device__ __forceinline__ float attn_inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 
-// ---- tiles of WAVES x 32 rows: wave w holds rows 32 w .. + 31, every lane one of
-// them, and all waves share the tile of 64 keys in LDS (two of each of K and V in
-// turn, loaded straight into LDS while the tile before is computed).
-template <typename E, int DP, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void attention_tile_kernel(AttnParams p) {
-    constexpr int BN = kAttnTileKeys, NT = DP / 32, KK = DP / 16, TILE = BN * DP * 2;
+// ---- tiles of 32 RG rows and BN KG keys, 8 waves: wave (rg, kg) holds rows 32 rg .. + 31,
+// every lane one of them, and takes the kg-th BN keys of each step; the kg waves of the same rows
+// meet in LDS at the end.  Two steps' K and V are in LDS in turn, loaded straight into it while
+// the step before is computed.  More rows to a tile read K and V less often, more waves to a
+// row shorten the way through its keys: where the rows alone do not fill the card.
+template <typename E, int DP, int RG, int KG, int BN>
+__global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_tile_kernel(AttnParams p) {
+    constexpr int NT = DP / 32, KK = DP / 16, XN = BN / 32, STEP = KG * BN, TILE = STEP * DP * 2;
+    static_assert(RG * KG == 8, "eight waves");
     __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];
+    static_assert((KG - 1) * RG * (NT * 4096 + 512) <= (int)sizeof(smem), "the waves' sums fit the buffers");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rg = wave % RG, kg = wave / RG;
     // the longest tiles of a masked problem first, heads side by side
     const int heads = p.n * p.hk, tiles = (int)gridDim.x / heads;
     const int head = blockIdx.x % heads, tile = tiles - 1 - blockIdx.x / heads;
     const int b = head / p.hk, hk = head % p.hk;
     const AttnSample s = attn_sample(p, b);
-    const int r0 = tile * WAVES * 32;
+    const int r0 = tile * RG * 32, d = p.d, last = s.queries - 1;
 
-    // this lane's row; rows past the sample's last query take that one's place
-    const int r = r0 + wave * 32 + (lane & 31);
-    const int i = r / p.group, g = r - i * p.group;
-    const bool alive = i < s.queries;
-    const int last = s.queries - 1;
-    const AttnRange seen = last < 0 ? AttnRange{0, 0} : attn_range(p, s, i < last ? i : last);
-    const int t_first = r0 / p.group, t_last = (r0 + WAVES * 32 - 1) / p.group;
-    int lo = 0, hi = 0;  // of the whole tile
-    if (t_first <= last) {
-        lo = attn_range(p, s, t_first).lo;
-        hi = attn_range(p, s, t_last < last ? t_last : last).hi;
+    int lo = 0, hi = 0;  // the keys that the tile's rows see
+    {
+        const int t_first = r0 / p.group, t_last = (r0 + RG * 32 - 1) / p.group;
+        if (t_first <= last) {
+            lo = attn_range(p, s, t_first).lo & ~(BN - 1);
+            hi = attn_range(p, s, t_last < last ? t_last : last).hi;
+        }
     }
-    lo &= ~(BN - 1);
     if (p.splits > 1) {
-        lo += blockIdx.y * p.pieces * BN;
-        const int end = lo + p.pieces * BN;
+        lo += blockIdx.y * p.pieces * STEP;
+        const int end = lo + p.pieces * STEP;
         hi = hi < end ? hi : end;
     }
-    const int wave_lo = __builtin_amdgcn_readfirstlane(seen.lo), wave_hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
-    const int wave_lo_all = __builtin_amdgcn_readlane(seen.lo, 31), wave_hi = __builtin_amdgcn_readlane(seen.hi, 31);
-
-    const int d = p.d;
+    const AttnTile<DP, STEP, 8> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane),
+        tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
+    if (lo < hi) {
+        tk.load(smem, lo, wave);
+        tv.load(smem + TILE, lo, wave);
+    }
+    // this lane's row; rows past the sample's last query take that one's place
+    const int r = r0 + rg * 32 + (lane & 31);
+    const int i = r / p.group, g = r - i * p.group;
+    const bool alive = i < s.queries;
     half8_t q[KK];
     {
         const _Float16 *row = p.q + b * p.qs[0] + i * p.qs[1] + (int64_t)(hk * p.group + g) * p.qs[2];
@@ -78,7 +93,9 @@ __global__ __launch_bounds__(WAVES * 64) void attention_tile_kernel(AttnParams p
             q[kk] = alive && e < d ? *reinterpret_cast<const half8_t *>(row + e) : z;
         }
     }
-    const AttnTile<DP, BN, WAVES> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane), tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
+    const AttnRange seen = last < 0 ? AttnRange{0, 0} : attn_range(p, s, i < last ? i : last);
+    const int wave_lo = __builtin_amdgcn_readfirstlane(seen.lo), wave_hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
+    const int wave_lo_all = __builtin_amdgcn_readlane(seen.lo, 31), wave_hi = __builtin_amdgcn_readlane(seen.hi, 31);
     AttnRows<DP> fk;
     AttnCols<DP> fv;
     fk.init(lane);
@@ -89,30 +106,27 @@ __global__ __launch_bounds__(WAVES * 64) void attention_tile_kernel(AttnParams p
     sm.init();
     f32x16 acc[NT] = {};
     int buf = 0;
-    if (lo < hi) {
-        tk.load(smem, lo, wave);
-        tv.load(smem + TILE, lo, wave);
-    }
-    for (int j0 = lo; j0 < hi; j0 += BN) {
+    for (int at = lo; at < hi; at += STEP) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const char *ks = smem + buf * 2 * TILE, *vs = ks + TILE;
+        const char *ks = smem + buf * 2 * TILE + kg * BN * DP * 2, *vs = ks + TILE;
         buf ^= 1;
-        if (j0 + BN < hi) {
+        if (at + STEP < hi) {
             char *next = smem + buf * 2 * TILE;
-            tk.load(next, j0 + BN, wave);
-            tv.load(next + TILE, j0 + BN, wave);
+            tk.load(next, at + STEP, wave);
+            tv.load(next + TILE, at + STEP, wave);
         }
+        const int j0 = at + kg * BN;
         if (j0 + BN <= wave_lo || j0 >= wave_hi) continue;
         const uint32_t kr = lds_address(ks) + fk.off;
-        f32x16 x[2] = {};
+        f32x16 x[XN] = {};
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) x[t] = mfma_32x32x16<E>(fk.read(kr, 32 * t, kk), q[kk], x[t]);
+            for (int t = 0; t < XN; ++t) x[t] = mfma_32x32x16<E>(fk.read(kr, 32 * t, kk), q[kk], x[t]);
         if (j0 < wave_lo_all || j0 + BN > wave_hi_all) {
             const int from = seen.lo - j0, to = seen.hi - j0;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < XN; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int j = 32 * t + acc_row(e, lane >> 5);
@@ -121,32 +135,27 @@ __global__ __launch_bounds__(WAVES * 64) void attention_tile_kernel(AttnParams p
         }
         float mx = x[0][0];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < XN; ++t)
 #pragma unroll
             for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[t][e]);
         mx = both_max(mx) * c;
         // the maximum follows only where it would be passed by more than 2^8: probabilities
         // are at most that, far inside the range of either type
         if (__builtin_amdgcn_ballot_w64(mx > sm.max + 8.0f)) {
-            const float m = fmaxf(sm.max, mx);
-            const float use = m == -__builtin_inff() ? 0.0f : m;
-            const float f = __builtin_amdgcn_exp2f(sm.max - use);
-            sm.max = m;
-            sm.use = use;
-            sm.sum *= f;
+            const float f = sm.raise(mx);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[t][e] *= f;
         }
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < XN; ++t)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 x[t][e] = __builtin_amdgcn_exp2f(fmaf(x[t][e], c, -sm.use));
                 sm.sum += x[t][e];
             }
-        static_for<4>([&](auto step) {
+        static_for<2 * XN>([&](auto step) {
             constexpr int S = decltype(step)::value;
             half8_t f[NT];
             fv.template read<S>(vs, f);
@@ -154,6 +163,191 @@ __global__ __launch_bounds__(WAVES * 64) void attention_tile_kernel(AttnParams p
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[t] = mfma_32x32x16<E>(f[t], w, acc[t]);
         });
+    }
+    if constexpr (KG > 1) {
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the buffers are free
+        float *sums = reinterpret_cast<float *>(smem);
+        float2 *ml = reinterpret_cast<float2 *>(sums + (KG - 1) * RG * NT * 1024);
+        if (kg > 0) {
+            const int at = (kg - 1) * RG + rg;
+            acc_put<NT>(sums + at * NT * 1024, acc, lane);
+            ml[at * 64 + lane] = make_float2(sm.max, sm.sum);
+        }
+        __syncthreads();
+        if (kg > 0) return;
+#pragma unroll 1
+        for (int o = 0; o < KG - 1; ++o) {
+            const int at = o * RG + rg;
+            const float2 x = ml[at * 64 + lane];
+            const float own = sm.raise(x.x), f = __builtin_amdgcn_exp2f(x.x - sm.use);
+            sm.sum = fmaf(x.y, f, sm.sum);
+            acc_join<NT>(sums + at * NT * 1024, acc, own, f, lane);
+        }
+    }
+    const float sum = both_sum(sm.sum);
+    if (r >= p.rows) return;
+    if (p.splits > 1) {
+        const int64_t at = ((int64_t)blockIdx.y * heads + head) * p.rows + r;
+        if (lane < 32) p.part_ml[at] = make_float2(sm.max, sum);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const int e0 = 32 * t + acc_row(e, lane >> 5);
+                if (e0 < d)
+                    *reinterpret_cast<f32x4 *>(p.part_o + at * d + e0) =
+                        f32x4{acc[t][e], acc[t][e + 1], acc[t][e + 2], acc[t][e + 3]};
+            }
+        return;
+    }
+    if (!alive) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[t] = f32x16{};
+    }
+    const float inv = attn_inverse(sum);
+    const int h = hk * p.group + g;
+    if (p.lse && lane < 32)
+        p.lse[((int64_t)b * p.hq + h) * p.tq + i] =
+            alive ? (sm.use + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -__builtin_inff();
+    _Float16 *out = p.o + b * p.os[0] + i * p.os[1] + h * p.os[2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, acc[t], inv, d - 32 * t, lane, true);
+}
+
+// ---- 256 rows, 64 keys to a step, for problems that fill the card: the same computation with
+// the two waves of each SIMD (w and w + 4) one phase apart.  A phase is either a step's
+// softmax, on the vector units, or the products around it (the next step's scores and this
+// step's share of the output), on the matrix core, so that each SIMD's matrix core always has
+// one of its two waves.  One barrier per phase.  K and V are in LDS three steps deep: in the
+// softmax of step t a wave issues its share of K(t + 2) and V(t + 1), which take the places of
+// K(t - 1) and V(t - 2), whose last readers were one phase and two phases ago, and sees that they have landed
+// at the end of the products that follow; the other group's first reads of them are two phases later.
+template <typename E, int DP>
+__global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_phase_kernel(AttnParams p) {
+    constexpr int BN = 64, NT = DP / 32, KK = DP / 16, TILE = BN * DP * 2;
+    __shared__ __attribute__((aligned(1024))) char smem[6 * TILE];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int heads = p.n * p.hk, tiles = (int)gridDim.x / heads;
+    const int head = blockIdx.x % heads, tile = tiles - 1 - blockIdx.x / heads;
+    const int b = head / p.hk, hk = head % p.hk;
+    const AttnSample s = attn_sample(p, b);
+    const int r0 = tile * 256, d = p.d, last = s.queries - 1;
+    int lo = 0, hi = 0;
+    {
+        const int t_first = r0 / p.group, t_last = (r0 + 255) / p.group;
+        if (t_first <= last) {
+            lo = attn_range(p, s, t_first).lo & ~(BN - 1);
+            hi = attn_range(p, s, t_last < last ? t_last : last).hi;
+        }
+    }
+    if (p.splits > 1) {
+        lo += blockIdx.y * p.pieces * BN;
+        const int end = lo + p.pieces * BN;
+        hi = hi < end ? hi : end;
+    }
+    const AttnTile<DP, BN, 8> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane),
+        tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
+    char *const vbuf = smem + 3 * TILE;
+    const bool any = lo < hi;
+    if (any) {
+        tk.load(smem, lo, wave);
+        tv.load(vbuf, lo, wave);
+        tk.load(smem + TILE, lo + BN, wave);  // behind the last key: zeros
+    }
+    const int r = r0 + wave * 32 + (lane & 31);
+    const int i = r / p.group, g = r - i * p.group;
+    const bool alive = i < s.queries;
+    half8_t q[KK];
+    {
+        const _Float16 *row = p.q + b * p.qs[0] + i * p.qs[1] + (int64_t)(hk * p.group + g) * p.qs[2];
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            const int e = 16 * kk + 8 * (lane >> 5);
+            half8_t z = {};
+            q[kk] = alive && e < d ? *reinterpret_cast<const half8_t *>(row + e) : z;
+        }
+    }
+    const AttnRange seen = last < 0 ? AttnRange{0, 0} : attn_range(p, s, i < last ? i : last);
+    const int all_lo = __builtin_amdgcn_readlane(seen.lo, 31), all_hi = __builtin_amdgcn_readfirstlane(seen.hi);
+    AttnRows<DP> fk;
+    AttnCols<DP> fv;
+    fk.init(lane);
+    fv.init(lane);
+    const float c = p.scale * kAttnLog2e;
+    AttnSoftmax sm;
+    sm.init();
+    f32x16 acc[NT] = {};
+    if (any) {
+        auto phase_end = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+        f32x16 x[2];
+        half8_t w[4];
+        auto scores = [&](const char *ks) {
+            const uint32_t kr = lds_address(ks) + fk.off;
+            x[0] = x[1] = f32x16{};
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) x[t] = mfma_32x32x16<E>(fk.read(kr, 32 * t, kk), q[kk], x[t]);
+        };
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (wave >= 4) phase_end();
+        scores(smem);
+        phase_end();
+        int k1 = 1, v0 = 0;  // the places of K(t + 1) and V(t)
+        for (int j0 = lo; j0 < hi; j0 += BN) {
+            const int k2 = k1 == 2 ? 0 : k1 + 1, v1 = v0 == 2 ? 0 : v0 + 1;
+            tk.load(smem + k2 * TILE, j0 + 2 * BN, wave);
+            tv.load(vbuf + v1 * TILE, j0 + BN, wave);
+            if (j0 < all_lo || j0 + BN > all_hi) {
+                const int from = seen.lo - j0, to = seen.hi - j0;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int j = 32 * t + acc_row(e, lane >> 5);
+                        x[t][e] = j >= from && j < to ? x[t][e] : -__builtin_inff();
+                    }
+            }
+            float mx = x[0][0];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[t][e]);
+            mx = both_max(mx) * c;
+            if (__builtin_amdgcn_ballot_w64(mx > sm.max + 8.0f)) {
+                const float f = sm.raise(mx);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[t][e] *= f;
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    x[t][e] = __builtin_amdgcn_exp2f(fmaf(x[t][e], c, -sm.use));
+                    sm.sum += x[t][e];
+                }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) w[t] = pack8<E>(x[t / 2], (t & 1) * 8);
+            __builtin_amdgcn_sched_barrier(0);
+            phase_end();
+            __builtin_amdgcn_s_setprio(2);
+            scores(smem + k1 * TILE);
+            const uint32_t b0 = lds_address(vbuf + v0 * TILE) + fv.off0, b1 = lds_address(vbuf + v0 * TILE) + fv.off1;
+            static_for<4>([&](auto step) {
+                constexpr int S = decltype(step)::value;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[t] = mfma_32x32x16<E>(fv.template fragment<S>(b0, b1, t), w[S], acc[t]);
+            });
+            __builtin_amdgcn_s_setprio(0);
+            k1 = k2;
+            v0 = v1;
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+        if (wave < 4) phase_end();  // as many barriers as the other group
     }
     const float sum = both_sum(sm.sum);
     if (r >= p.rows) return;
@@ -192,7 +386,7 @@ __global__ __launch_bounds__(WAVES * 64) void attention_tile_kernel(AttnParams p
 template <typename E, int DP>
 __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
     constexpr int WAVES = 4, BN = 32, NT = DP / 32, KK = DP / 16, TILE = BN * DP * 2, NL = 2 * AttnTile<DP, BN, 1>::LOADS;
-    static_assert(WAVES * BN == kAttnFewKeys, "keys of a step");
+    static_assert(WAVES * BN == attn_tile(kAttnFew).keys, "keys of a step");
     __shared__ __attribute__((aligned(1024))) char smem[WAVES * 4 * TILE];
     static_assert(WAVES * (32 * DP + 64) * 4 <= (int)sizeof(smem), "the waves' sums fit the buffers");
     const int lane = threadIdx.x & 63;
@@ -208,11 +402,18 @@ __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
     const int lo_all = __builtin_amdgcn_readlane(seen.lo, 31), hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
     int lo = __builtin_amdgcn_readfirstlane(seen.lo) & ~(BN - 1), hi = __builtin_amdgcn_readlane(seen.hi, 31);
     if (p.splits > 1) {
-        lo += split * p.pieces * kAttnFewKeys;
-        const int end = lo + p.pieces * kAttnFewKeys;
+        lo += split * p.pieces * WAVES * BN;
+        const int end = lo + p.pieces * WAVES * BN;
         hi = hi < end ? hi : end;
     }
     const int d = p.d;
+    const AttnTile<DP, BN, 1> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, 0, lane), tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, 0, lane);
+    char *mine = smem + wave * 4 * TILE;
+    int buf = 0;
+    int j0 = lo + wave * BN;
+    // rows past the last key load zeros, so every step has the same number of loads
+    tk.load(mine, j0, 0);
+    tv.load(mine + TILE, j0, 0);
     half8_t q[KK];
     {
         const _Float16 *row = p.q + b * p.qs[0] + i * p.qs[1] + (int64_t)(hk * p.group + g) * p.qs[2];
@@ -223,7 +424,6 @@ __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
             q[kk] = alive && e < d ? *reinterpret_cast<const half8_t *>(row + e) : z;
         }
     }
-    const AttnTile<DP, BN, 1> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, 0, lane), tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, 0, lane);
     AttnRows<DP> fk;
     AttnCols<DP> fv;
     fk.init(lane);
@@ -232,12 +432,6 @@ __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
     AttnSoftmax sm;
     sm.init();
     f32x16 acc[NT] = {};
-    char *mine = smem + wave * 4 * TILE;
-    int buf = 0;
-    int j0 = lo + wave * BN;
-    // rows past the last key load zeros, so every step has the same number of loads
-    tk.load(mine, j0, 0);
-    tv.load(mine + TILE, j0, 0);
     for (; j0 < hi; j0 += WAVES * BN) {
         char *next = mine + (buf ^ 1) * 2 * TILE;
         tk.load(next, j0 + WAVES * BN, 0);
@@ -262,12 +456,7 @@ __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
         for (int e = 1; e < 16; ++e) mx = fmaxf(mx, x[e]);
         mx = both_max(mx) * c;
         if (__builtin_amdgcn_ballot_w64(mx > sm.max + 8.0f)) {
-            const float m = fmaxf(sm.max, mx);
-            const float use = m == -__builtin_inff() ? 0.0f : m;
-            const float f = __builtin_amdgcn_exp2f(sm.max - use);
-            sm.max = m;
-            sm.use = use;
-            sm.sum *= f;
+            const float f = sm.raise(mx);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -383,14 +572,14 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnParams p) {
 }
 
 template <typename E, int DP>
-static void launch_forward(const AttnParams &p, bool few, hipStream_t s) {
-    const int heads = p.n * p.hk;
-    if (few) {
-        attention_few_kernel<E, DP><<<dim3(heads * p.splits), dim3(256), 0, s>>>(p);
-    } else {
-        const int tiles = (p.rows + kAttnTileRows - 1) / kAttnTileRows;
-        attention_tile_kernel<E, DP, kAttnTileRows / 32>
-            <<<dim3(heads * tiles, p.splits), dim3(kAttnTileRows * 2), 0, s>>>(p);
+static void launch_forward(const AttnParams &p, AttnTileKind kind, hipStream_t s) {
+    const int heads = p.n * p.hk, rows = attn_tile(kind).rows;
+    const dim3 grid((uint32_t)(heads * ((p.rows + rows - 1) / rows)), (uint32_t)p.splits), block(512);
+    switch (kind) {
+        case kAttnFew: attention_few_kernel<E, DP><<<dim3(heads * p.splits), dim3(256), 0, s>>>(p); break;
+        case kAttn64: attention_tile_kernel<E, DP, 2, 4, 32><<<grid, block, 0, s>>>(p); break;
+        case kAttn128: attention_tile_kernel<E, DP, 4, 2, 64><<<grid, block, 0, s>>>(p); break;
+        default: attention_phase_kernel<E, DP><<<grid, block, 0, s>>>(p); break;
     }
     if (p.splits > 1) {
         const int64_t count = (int64_t)heads * p.rows;
@@ -399,22 +588,22 @@ static void launch_forward(const AttnParams &p, bool few, hipStream_t s) {
 }
 
 template <typename E>
-static void launch_forward_dim(const AttnParams &p, bool few, hipStream_t s) {
+static void launch_forward_dim(const AttnParams &p, AttnTileKind kind, hipStream_t s) {
     if (p.d <= 32)
-        launch_forward<E, 32>(p, few, s);
+        launch_forward<E, 32>(p, kind, s);
     else if (p.d <= 64)
-        launch_forward<E, 64>(p, few, s);
+        launch_forward<E, 64>(p, kind, s);
     else if (p.d <= 96)
-        launch_forward<E, 96>(p, few, s);
+        launch_forward<E, 96>(p, kind, s);
     else
-        launch_forward<E, 128>(p, few, s);
+        launch_forward<E, 128>(p, kind, s);
 }
 
-hipError_t launch_attention(const AttnParams &p, bool few, hipStream_t s) {
+hipError_t launch_attention(const AttnParams &p, AttnTileKind kind, hipStream_t s) {
     if (p.bf16)
-        launch_forward_dim<__bf16>(p, few, s);
+        launch_forward_dim<__bf16>(p, kind, s);
     else
-        launch_forward_dim<_Float16>(p, few, s);
+        launch_forward_dim<_Float16>(p, kind, s);
     return hipGetLastError();
 }
 

@@ -17,9 +17,9 @@ struct attention_plan_s {
     attention_desc d;
     int64_t qs[3], ks[3], vs[3], os[3];
     bool folds_q, folds_k, folds_v, folds_o;  // strides that put different elements on one address
-    bool few;
+    AttnTileKind kind, kind_q, kind_kv;
     int64_t grid;
-    size_t off_ml, fwd_bytes, off_delta, back_bytes;
+    size_t off_ml, fwd_bytes, off_delta, off_dk, off_dv, back_bytes;
     AttnParams prm;  // pointers filled per call
 };
 
@@ -27,7 +27,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 constexpr int64_t kMaxOffset = (int64_t)1 << 30;
-constexpr int kAttnCUs = 256;
+constexpr int kAttnCUs = 256, kMaxPieces = 128;
 
 conv3d_status attn_strides(const int64_t *given, int64_t tokens, int heads, int dim, const char *what, int64_t *out) {
     if (!given[0] && !given[1] && !given[2]) {
@@ -52,17 +52,79 @@ conv3d_status attn_strides(const int64_t *given, int64_t tokens, int heads, int 
     return CONV3D_OK;
 }
 
-// How many pieces to split the keys into.  `units` workgroups take `steps` steps each.
-int attn_splits(int64_t units, int64_t steps, bool few) {
-    if (const char *v = getenv("CONV3D_ATTENTION_SPLITS")) {
-        const int k = atoi(v);
-        return k < 1 ? 1 : k > steps ? (int)steps : k;
+// ---- which kernel, and how many pieces.  Times in us, from the kernels' measured steps.
+
+// One operator's problem: `heads` independent ones of `rows` rows, each of which walks `most` elements
+// of the other side, `mean` on average.
+struct Problem {
+    int64_t heads, rows;
+    double most, mean;
+    int dim;
+};
+struct Choice {
+    AttnTileKind kind;
+    int pieces;
+    double us;
+};
+
+enum Pass { kForward, kDq, kDkv };
+
+// A step of a workgroup alone on its CU: two waves to a SIMD, each with as many MFMAs (32 cycles)
+// as its product of 32 rows and `keys` / groups needs, or as many vector instructions.
+double step_us(Pass pass, AttnTileKind kind, int dim) {
+    const int dp = (dim + 31) / 32 * 32, sub = kind == kAttn64 || (pass == kDkv && kind == kAttn128) ? 1 : 2;
+    const int products = pass == kForward ? 2 : pass == kDq ? 3 : 4;
+    const double matrix = products * (dp / 16) * 32.0, vector = pass == kForward ? 380.0 : 330.0;
+    return 2.0 * sub * ((matrix > vector ? matrix : vector) + 110.0) / 2200.0 + 0.15;
+}
+
+AttnTileKind forced_kind(AttnTileKind otherwise, bool few) {
+    const char *v = getenv("CONV3D_ATTENTION_TILE");
+    if (!v) return otherwise;
+    for (AttnTileKind k : {kAttnFew, kAttn64, kAttn128, kAttn256})
+        if ((k != kAttnFew || few) && strcmp(v, attn_tile(k).name) == 0) return k;
+    return otherwise;
+}
+int forced_pieces(int otherwise) {
+    const char *v = getenv("CONV3D_ATTENTION_SPLITS");
+    const int k = v ? atoi(v) : 0;
+    return k < 1 ? otherwise : k > kMaxPieces ? kMaxPieces : k;
+}
+
+Choice choose(Pass pass, const Problem &w, bool splits) {
+    Choice best = {kAttn256, 1, -1.0};
+    const bool few = pass == kForward && w.rows <= kAttnFewRows;
+    const AttnTileKind only = forced_kind(few ? kAttnFew : kAttn256, few);
+    const bool forced = getenv("CONV3D_ATTENTION_TILE") != nullptr;
+    for (AttnTileKind kind : {kAttn256, kAttn128, kAttn64, kAttnFew}) {
+        if (kind == kAttnFew && !few) continue;
+        if (forced && kind != only) continue;
+        const AttnTileSize t = attn_tile(kind);
+        const int64_t tiles = w.heads * ((w.rows + t.rows - 1) / t.rows);
+        const double keys = pass == kDkv ? attn_grad_step(kind) : t.keys;
+        for (int z = 1; z <= kMaxPieces; z += z < 8 ? 1 : z < 32 ? 4 : 16) {
+            const int pieces = forced_pieces(z);
+            const double most = std::ceil(std::ceil(w.most / keys) / pieces), mean = w.mean / keys / pieces;
+            if (z > 1 && (!splits || most < 1.5 || tiles * z > 4 * kAttnCUs)) break;
+            const double units = (double)tiles * pieces, rounds = units / kAttnCUs;
+            double us;
+            if (kind == kAttnFew) {
+                // the steps' loads are on their way one step ahead; all of them share the memory's rate
+                const double bytes = 512.0 * w.dim, share = (units < kAttnCUs ? units : kAttnCUs) * bytes / 5.5e6;
+                us = 3.2 + std::ceil(rounds) * most * (share > 0.9 ? share : 0.9);
+            } else {
+                const double c = step_us(pass, kind, w.dim), fixed = 1.2 + (kind == kAttn256 ? 0.0 : 1.0);
+                // equal workgroups run in whole rounds; unequal ones, longest first, fill up
+                const double even = std::ceil(rounds) * (most * c + fixed);
+                const double fill = rounds * (mean * c + fixed) + 0.4 * most * c, longest = most * c + fixed;
+                us = 2.0 + (w.mean > 0.95 * w.most ? even : fill > longest ? fill : longest);
+            }
+            if (pieces > 1) us += 3.0 + (double)w.heads * w.rows * w.dim * pieces * (pass == kDkv ? 16.0 : 8.0) / 4e6;
+            if (best.us < 0.0 || us < best.us) best = {kind, pieces, us};
+            if (pieces != z) break;  // forced
+        }
     }
-    const int64_t least = few ? 2 : 8;  // steps worth a piece
-    int64_t want = units > 0 ? kAttnCUs / units : 1;
-    if (want > steps / least) want = steps / least;
-    if (want > 256) want = 256;
-    return want < 1 ? 1 : (int)want;
+    return best;
 }
 
 // The tensors of a call.
@@ -166,23 +228,40 @@ conv3d_status attention_plan(const attention_desc *d, attention_plan_t *out, siz
     r.scale = d->scale > 0.0f ? d->scale : (float)(1.0 / std::sqrt((double)d->head_dim));
 
     const int64_t heads = (int64_t)d->n * d->heads_k;
-    p->few = r.rows <= kAttnFewRows;
-    const int64_t tiles = p->few ? 1 : (r.rows + kAttnTileRows - 1) / kAttnTileRows;
-    const int64_t units = heads * tiles, key_tiles = heads * (((int64_t)d->tk + 127) / 128);
-    if (units >= (int64_t)1 << 22 || key_tiles >= (int64_t)1 << 22) {
+    // what a query sees of the keys, and a key of the queries: offsets and lengths are the calls', so the
+    // queries are taken as the last tokens of whole samples
+    double most = d->tk, mean = d->tk, back = d->tq, back_mean = d->tq;
+    if (d->frame) {
+        const double offset = d->tk > d->tq ? (double)(d->tk - d->tq) : 0.0, window = (double)d->window * d->frame;
+        if (d->window && window + d->frame < most) most = window + d->frame;
+        mean = offset + 0.5 * (d->tq + (d->frame < d->tq ? d->frame : d->tq));
+        mean = mean < most ? mean : most;
+        if (d->window && window + d->frame < back) back = window + d->frame;
+        back_mean = d->tk ? mean * d->tq / d->tk : 0.0;
+        back_mean = back_mean < back ? back_mean : back;
+    }
+    const Choice fwd = choose(kForward, {heads, r.rows, most, mean, d->head_dim}, true),
+                 dq = choose(kDq, {heads, r.rows, most, mean, d->head_dim}, false),
+                 dkv = choose(kDkv, {heads, d->tk, back * group, back_mean * group, d->head_dim}, true);
+    p->kind = fwd.kind;
+    p->kind_q = dq.kind;
+    p->kind_kv = dkv.kind;
+    const AttnTileSize tile = attn_tile(fwd.kind);
+    const int64_t units = heads * ((r.rows + tile.rows - 1) / tile.rows),
+                  units64 = heads * (((int64_t)(r.rows > d->tk ? r.rows : d->tk) + 63) / 64);
+    if (units64 >= (int64_t)1 << 22) {
         delete p;
         return api_fail(CONV3D_ERR_UNSUPPORTED, "the call has too many tiles");
     }
-    // the keys that one tile's rows see together
+    // all of a row's keys, whatever the call's offset (a range may start inside a step)
     int64_t span = d->tk;
     if (d->window) {
-        const int64_t tokens = p->few ? d->tq : kAttnTileRows / group + 2;
+        const int64_t tokens = tile.rows / group + 2;
         const int64_t seen = ((int64_t)d->window + tokens / d->frame + 1) * d->frame;
         if (seen < span) span = seen;
     }
-    const int step = p->few ? kAttnFewKeys : kAttnTileKeys;
-    const int64_t steps = (span + step - 1) / step + 1;  // one more: a range may start inside a tile
-    r.splits = units ? attn_splits(units, steps, p->few) : 1;
+    const int64_t steps = (span + tile.keys - 1) / tile.keys + 1;
+    r.splits = fwd.pieces < steps ? fwd.pieces : (int32_t)steps;
     r.pieces = (int32_t)((steps + r.splits - 1) / r.splits);
     p->grid = units * r.splits;
     p->off_ml = p->fwd_bytes = 0;
@@ -190,8 +269,22 @@ conv3d_status attention_plan(const attention_desc *d, attention_plan_t *out, siz
         p->off_ml = align256((size_t)r.splits * heads * r.rows * r.d * 4);
         p->fwd_bytes = p->off_ml + (size_t)r.splits * heads * r.rows * 8;
     }
+    // the same for a key's queries: steps of one query head, for all of them
+    const int grad_keys = attn_tile(dkv.kind).rows, grad_step = attn_grad_step(dkv.kind);
+    int64_t back_span = d->tq;
+    if (d->window) {
+        const int64_t seen = ((int64_t)d->window + grad_keys / d->frame + 1) * d->frame;
+        if (seen < back_span) back_span = seen;
+    }
+    const int64_t back_steps = ((back_span + grad_step - 1) / grad_step + 1) * group;
+    r.grad_splits = dkv.pieces < back_steps ? dkv.pieces : (int32_t)back_steps;
+    r.grad_pieces = (int32_t)((back_steps + r.grad_splits - 1) / r.grad_splits);
     p->off_delta = align256((size_t)d->n * d->heads_q * d->tq * 4);
-    p->back_bytes = 2 * p->off_delta;
+    p->off_dk = p->off_dv = p->back_bytes = 2 * p->off_delta;
+    if (r.grad_splits > 1) {
+        p->off_dv = p->off_dk + align256((size_t)r.grad_splits * heads * d->tk * r.d * 4);
+        p->back_bytes = p->off_dv + (size_t)r.grad_splits * heads * d->tk * r.d * 4;
+    }
     *out = p;
     *workspace_bytes = p->fwd_bytes;
     return api_ok();
@@ -200,14 +293,15 @@ conv3d_status attention_plan(const attention_desc *d, attention_plan_t *out, siz
 conv3d_status attention_plan_query(attention_plan_t p, attention_plan_info *info) {
     if (!p || !info) return api_fail(CONV3D_ERR_INVALID_ARG, "plan and info are required");
     memset(info, 0, sizeof(*info));
-    info->tile_rows = p->few ? kAttnFewRows : kAttnTileRows;
-    info->tile_keys = p->few ? kAttnFewKeys : kAttnTileKeys;
-    info->threads = p->few ? 256 : kAttnTileRows * 2;
+    const AttnTileSize t = attn_tile(p->kind);
+    info->tile_rows = t.rows;
+    info->tile_keys = t.keys;
+    info->threads = t.threads;
     info->splits = p->prm.splits;
     info->grid = p->grid;
     info->workspace_bytes = p->fwd_bytes;
     info->backward_workspace_bytes = p->back_bytes;
-    snprintf(info->kernel_name, sizeof(info->kernel_name), "%s", p->few ? "attention_few" : "attention_tile");
+    snprintf(info->kernel_name, sizeof(info->kernel_name), "%s", t.name);
     return api_ok();
 }
 
@@ -251,7 +345,7 @@ conv3d_status attention_forward(attention_plan_t p, const void *q, const void *k
     r.q_offset = q_offset;
     r.part_o = static_cast<float *>(workspace);
     r.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p->off_ml);
-    return launched(launch_attention(r, p->few, static_cast<hipStream_t>(stream)), "attention");
+    return launched(launch_attention(r, p->kind, static_cast<hipStream_t>(stream)), "attention");
 }
 
 size_t attention_backward_workspace(attention_plan_t p) { return p ? p->back_bytes : 0; }
@@ -312,8 +406,11 @@ conv3d_status attention_backward(attention_plan_t p, const void *dout, const voi
     r.lengths = static_cast<const int32_t *>(lengths);
     r.q_offset = q_offset;
     r.nlse = static_cast<float *>(workspace);
-    r.ndelta = reinterpret_cast<float *>(static_cast<char *>(workspace) + p->off_delta);
-    return launched(launch_attention_grad(r, static_cast<hipStream_t>(stream)), "attention_backward");
+    char *ws = static_cast<char *>(workspace);
+    r.ndelta = reinterpret_cast<float *>(ws + p->off_delta);
+    r.part_dk = reinterpret_cast<float *>(ws + p->off_dk);
+    r.part_dv = reinterpret_cast<float *>(ws + p->off_dv);
+    return launched(launch_attention_grad(r, p->kind_q, p->kind_kv, static_cast<hipStream_t>(stream)), "attention_backward");
 }
 
 }  // extern "C"

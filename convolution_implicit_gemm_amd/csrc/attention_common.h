@@ -49,6 +49,16 @@ __device__ __forceinline__ AttnRange attn_range(const AttnParams &p, const AttnS
     return {lo, hi};
 }
 
+// The other way round: the query tokens [lo, hi) that see a key of the sample.
+__device__ __forceinline__ AttnRange attn_seen_by(const AttnParams &p, const AttnSample &s, int key) {
+    if (!p.frame) return {0, s.queries};
+    const int64_t f = (uint32_t)key / (uint32_t)p.frame, q = s.queries;
+    const int64_t from = f * p.frame - s.offset;
+    const int64_t to = p.window ? (f + p.window) * p.frame - s.offset : q;
+    const int lo = (int)(from < 0 ? 0 : from < q ? from : q), hi = (int)(to < 0 ? 0 : to < q ? to : q);
+    return {lo, hi < lo ? lo : hi};
+}
+
 // ---- tiles in LDS: rows of DP elements (the head's, then zeros), 2 DP bytes.
 // 16-byte chunk c of row r sits at chunk c ^ attn_swz(r): the 16 rows that a read of
 // one chunk touches at a time, and the 4 rows x 64 bytes of a transposing read, each
@@ -150,6 +160,22 @@ struct AttnCols {
         off1 = r1 * ROW + ((c ^ attn_swz<DP>(r1)) << 4) + (j & 1) * 8;
     }
     static __device__ __forceinline__ uint32_t group(uint32_t at, int t) { return XOR ? at ^ (t << 6) : at + (t << 6); }
+    // One fragment in the compiler's own form, which it moves and waits for by itself (and for the wave's
+    // loads into LDS too: the caller sees to it that they have had their time).  b0, b1: the
+    // tile's address + off0, off1.
+    template <int S>
+    static __device__ __forceinline__ half8_t fragment(uint32_t b0, uint32_t b1, int t) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        typedef __fp16 v4 __attribute__((__vector_size__(8)));
+        typedef __attribute__((address_space(3))) v4 lds_v4;
+        const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_v4 *)(group(b0, t) + S * 16 * ROW));
+        const auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_v4 *)(group(b1, t) + S * 16 * ROW));
+        return __builtin_shufflevector(__builtin_bit_cast(half4_t, lo), __builtin_bit_cast(half4_t, hi), 0, 1, 2, 3, 4, 5,
+                                       6, 7);
+#else
+        return half8_t{};
+#endif
+    }
     // the fragments of rows [16 S, 16 S + 16) of the tile
     template <int S>
     __device__ __forceinline__ void read(const char *tile, half8_t (&f)[NT]) const {
@@ -214,6 +240,30 @@ __device__ __forceinline__ float both_max(float v) {
 __device__ __forceinline__ float both_sum(float v) {
     const Halves x(v);
     return x.low + x.high;
+}
+
+// One wave's accumulators to another one that holds the same rows and columns, through LDS:
+// 16 bytes per lane at a time, lane by lane.
+template <int NT>
+__device__ __forceinline__ void acc_put(float *to, const f32x16 (&acc)[NT], int lane) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<f32x4 *>(to + ((t * 4 + (e >> 2)) * 64 + lane) * 4) =
+                f32x4{acc[t][e], acc[t][e + 1], acc[t][e + 2], acc[t][e + 3]};
+}
+// acc = acc * own + other * f
+template <int NT>
+__device__ __forceinline__ void acc_join(const float *from, f32x16 (&acc)[NT], float own, float f, int lane) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const f32x4 o = *reinterpret_cast<const f32x4 *>(from + ((t * 4 + (e >> 2)) * 64 + lane) * 4);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) acc[t][e + m] = fmaf(acc[t][e + m], own, o[m] * f);
+        }
 }
 
 // Eight consecutive accumulator registers as an operand's fragment.

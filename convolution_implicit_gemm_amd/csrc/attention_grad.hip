@@ -27,35 +27,39 @@ __device__ __forceinline__ float dot8(half8_t a, half8_t b) {
     return s;
 }
 
-// ---- dq: tiles of WAVES x 32 rows as in the forward pass.  S^T = K Q^T and dP^T = V dout^T
+// ---- dq: tiles of 32 RG rows and BN KG keys as in the forward pass.  S^T = K Q^T and dP^T = V dout^T
 // hold one query per lane; dS^T is, as it stands, the operand of dq^T = K^T dS^T.
-template <typename E, int DP, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void attention_dq_kernel(AttnParams p) {
-    constexpr int BN = kAttnTileKeys, NT = DP / 32, KK = DP / 16, TILE = BN * DP * 2;
+template <typename E, int DP, int RG, int KG, int BN>
+__global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
+    constexpr int NT = DP / 32, KK = DP / 16, XN = BN / 32, STEP = KG * BN, TILE = STEP * DP * 2;
+    static_assert(RG * KG == 8, "eight waves");
     __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];
+    static_assert((KG - 1) * RG * NT * 4096 <= (int)sizeof(smem), "the waves' sums fit the buffers");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rg = wave % RG, kg = wave / RG;
     const int heads = p.n * p.hk, tiles = (int)gridDim.x / heads;
     const int head = blockIdx.x % heads, tile = tiles - 1 - blockIdx.x / heads;
     const int b = head / p.hk, hk = head % p.hk;
     const AttnSample s = attn_sample(p, b);
-    const int r0 = tile * WAVES * 32;
-    const int r = r0 + wave * 32 + (lane & 31);
+    const int r0 = tile * RG * 32, d = p.d, last = s.queries - 1;
+    int lo = 0, hi = 0;
+    if (p.dq) {
+        const int t_first = r0 / p.group, t_last = (r0 + RG * 32 - 1) / p.group;
+        if (t_first <= last) {
+            lo = attn_range(p, s, t_first).lo & ~(BN - 1);
+            hi = attn_range(p, s, t_last < last ? t_last : last).hi;
+        }
+    }
+    const AttnTile<DP, STEP, 8> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane),
+        tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
+    if (lo < hi) {
+        tk.load(smem, lo, wave);
+        tv.load(smem + TILE, lo, wave);
+    }
+    const int r = r0 + rg * 32 + (lane & 31);
     const int i = r / p.group, g = r - i * p.group, h = hk * p.group + g;
     const bool alive = i < s.queries;
-    const int last = s.queries - 1;
-    const AttnRange seen = last < 0 ? AttnRange{0, 0} : attn_range(p, s, i < last ? i : last);
-    const int t_first = r0 / p.group, t_last = (r0 + WAVES * 32 - 1) / p.group;
-    int lo = 0, hi = 0;
-    if (t_first <= last) {
-        lo = attn_range(p, s, t_first).lo;
-        hi = attn_range(p, s, t_last < last ? t_last : last).hi;
-    }
-    lo &= ~(BN - 1);
-    const int wave_lo = __builtin_amdgcn_readfirstlane(seen.lo), wave_hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
-    const int wave_lo_all = __builtin_amdgcn_readlane(seen.lo, 31), wave_hi = __builtin_amdgcn_readlane(seen.hi, 31);
-
-    const int d = p.d;
     half8_t q[KK], go[KK];
     float delta = 0.0f, lse = -__builtin_inff();
     {
@@ -76,13 +80,15 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dq_kernel(AttnParams p) 
         delta = both_sum(delta);
         const int64_t row = ((int64_t)b * p.hq + h) * p.tq + i;
         if (alive) lse = p.lse[row];
-        if (r < p.rows && lane < 32) {
+        if (r < p.rows && lane < 32 && kg == 0) {
             p.nlse[row] = start_of_scores(lse, p.scale);
             p.ndelta[row] = -delta;
         }
     }
     if (!p.dq) return;  // only the rows' sums were asked for
-    const AttnTile<DP, BN, WAVES> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane), tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
+    const AttnRange seen = last < 0 ? AttnRange{0, 0} : attn_range(p, s, i < last ? i : last);
+    const int wave_lo = __builtin_amdgcn_readfirstlane(seen.lo), wave_hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
+    const int wave_lo_all = __builtin_amdgcn_readlane(seen.lo, 31), wave_hi = __builtin_amdgcn_readlane(seen.hi, 31);
     AttnRows<DP> fr;
     AttnCols<DP> fc;
     fr.init(lane);
@@ -90,23 +96,20 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dq_kernel(AttnParams p) 
     const float c = p.scale * kAttnLog2e, lse2 = lse == -__builtin_inff() ? 0.0f : lse * kAttnLog2e;
     f32x16 acc[NT] = {};
     int buf = 0;
-    if (lo < hi) {
-        tk.load(smem, lo, wave);
-        tv.load(smem + TILE, lo, wave);
-    }
-    for (int j0 = lo; j0 < hi; j0 += BN) {
+    for (int at = lo; at < hi; at += STEP) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const char *ks = smem + buf * 2 * TILE;
+        const char *ks = smem + buf * 2 * TILE + kg * BN * DP * 2;
         buf ^= 1;
-        if (j0 + BN < hi) {
+        if (at + STEP < hi) {
             char *next = smem + buf * 2 * TILE;
-            tk.load(next, j0 + BN, wave);
-            tv.load(next + TILE, j0 + BN, wave);
+            tk.load(next, at + STEP, wave);
+            tv.load(next + TILE, at + STEP, wave);
         }
+        const int j0 = at + kg * BN;
         if (j0 + BN <= wave_lo || j0 >= wave_hi) continue;
         const bool edge = j0 < wave_lo_all || j0 + BN > wave_hi_all;
         const uint32_t kr = lds_address(ks) + fr.off;
-        static_for<2>([&](auto sub) {
+        static_for<XN>([&](auto sub) {
             constexpr int T = decltype(sub)::value;
             f32x16 x = {}, y;
 #pragma unroll
@@ -114,7 +117,7 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dq_kernel(AttnParams p) 
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
                 x = mfma_32x32x16<E>(fr.read(kr, 32 * T, kk), q[kk], x);
-                y = mfma_32x32x16<E>(fr.read(kr, BN + 32 * T, kk), go[kk], y);
+                y = mfma_32x32x16<E>(fr.read(kr, STEP + 32 * T, kk), go[kk], y);
             }
             if (edge) {
                 const int from = seen.lo - j0, to = seen.hi - j0;
@@ -136,6 +139,15 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dq_kernel(AttnParams p) 
             });
         });
     }
+    if constexpr (KG > 1) {
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the buffers are free
+        float *sums = reinterpret_cast<float *>(smem);
+        if (kg > 0) acc_put<NT>(sums + ((kg - 1) * RG + rg) * NT * 1024, acc, lane);
+        __syncthreads();
+        if (kg > 0) return;
+#pragma unroll 1
+        for (int o = 0; o < KG - 1; ++o) acc_join<NT>(sums + (o * RG + rg) * NT * 1024, acc, 1.0f, 1.0f, lane);
+    }
     if (r >= p.rows) return;
     if (!alive) {
 #pragma unroll
@@ -146,48 +158,76 @@ __global__ __launch_bounds__(WAVES * 64) void attention_dq_kernel(AttnParams p) 
     for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, acc[t], p.scale, d - 32 * t, lane, true);
 }
 
-// ---- dk, dv: WAVES x 32 keys, wave w holds keys 32 w .. + 31 (one key per lane of every
-// result) and all waves share the tile of 64 query tokens in LDS; the query heads of the
-// key head are taken one after the other.  S = Q K^T and dP = dout V^T; P and dS are,
-// as they stand, the operands of dv^T = dout^T P and dk^T = Q^T dS.
-template <typename E, int DP, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, 2) void attention_dkv_kernel(AttnParams p) {
-    constexpr int BM = 64, NT = DP / 32, KK = DP / 16, TILE = BM * DP * 2, BN = WAVES * 32;
+// ---- dk, dv: tiles of 32 KW keys and BM QG query tokens, 8 waves: wave (kw, qg) holds keys
+// 32 kw .. + 31 (one key per lane of every result) and takes the qg-th BM tokens of each step; the
+// query heads of the key head are taken one after the other.  S = Q K^T and dP = dout V^T; P
+// and dS are, as they stand, the operands of dv^T = dout^T P and dk^T = Q^T dS.  The qg waves of
+// the same keys meet in LDS at the end.
+template <typename E, int DP, int KW, int QG, int BM>
+__global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
+    constexpr int NT = DP / 32, KK = DP / 16, XN = BM / 32, STEP = QG * BM, TILE = STEP * DP * 2, BN = KW * 32;
+    static_assert(KW * QG == 8, "eight waves");
     constexpr bool KLDS = DP > 64;  // k in LDS: with both in registers two waves would not fit a SIMD
     constexpr int KBYTES = KLDS ? BN * DP * 2 : 0;
-    __shared__ __attribute__((aligned(1024))) char smem[KBYTES + 4 * TILE + 4 * BM * 4];
+    __shared__ __attribute__((aligned(1024))) char smem[KBYTES + 4 * TILE + 4 * STEP * 4];
+    static_assert(sizeof(smem) <= 160 * 1024, "LDS is 160 KiB per CU");
+    static_assert((QG - 1) * KW * NT * 4096 <= (int)sizeof(smem), "the waves' sums fit the buffers");
     char *tiles = smem + KBYTES;
-    float *rows_at = reinterpret_cast<float *>(tiles + 4 * TILE);  // [2][nlse, ndelta][BM]
+    float *rows_at = reinterpret_cast<float *>(tiles + 4 * TILE);  // [2][nlse, ndelta][STEP]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kw = wave % KW, qg = wave / KW;
     const int heads = p.n * p.hk;
     const int head = blockIdx.x % heads, tile = blockIdx.x / heads;  // the longest of a masked problem first
     const int b = head / p.hk, hk = head % p.hk;
     const AttnSample s = attn_sample(p, b);
-    const int j0 = tile * BN, j = j0 + wave * 32 + (lane & 31);
+    const int j0 = tile * BN, j = j0 + kw * 32 + (lane & 31), last = s.keys - 1, d = p.d;
     const bool alive = j < s.keys;
-    // the query tokens [lo, hi) that see a key
-    auto seen_by = [&](int key) -> AttnRange {
-        if (!p.frame) return {0, s.queries};
-        const int64_t f = (uint32_t)key / (uint32_t)p.frame;
-        const int64_t from = f * p.frame - s.offset;
-        const int64_t to = p.window ? (f + p.window) * p.frame - s.offset : (int64_t)s.queries;
-        const int64_t q = s.queries;
-        const int a = (int)(from < 0 ? 0 : from < q ? from : q), z = (int)(to < 0 ? 0 : to < q ? to : q);
-        return {a, z < a ? a : z};
-    };
-    const int last = s.keys - 1;
-    // keys past the sample's last take that one's place
-    const AttnRange seen = last < 0 ? AttnRange{0, 0} : seen_by(j < last ? j : last);
+    // the sequence of steps: the tokens that see the tile's keys, for one query head after the other
     int lo = 0, hi = 0;
     if (j0 <= last) {
-        lo = seen_by(j0).lo & ~(BM - 1);
-        const int jl = j0 + BN - 1;
-        hi = seen_by(jl < last ? jl : last).hi;
+        lo = attn_seen_by(p, s, j0).lo & ~(BM - 1);
+        hi = attn_seen_by(p, s, j0 + BN - 1 < last ? j0 + BN - 1 : last).hi;
     }
-    const int wave_lo = __builtin_amdgcn_readfirstlane(seen.lo), wave_hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
-    const int wave_lo_all = __builtin_amdgcn_readlane(seen.lo, 31), wave_hi = __builtin_amdgcn_readlane(seen.hi, 31);
-    const int d = p.d;
+    const int steps = hi > lo ? (hi - lo + STEP - 1) / STEP : 0;
+    int first = 0, total = steps * p.group;
+    if (p.grad_splits > 1) {
+        first = blockIdx.y * p.grad_pieces;
+        if (first >= total && blockIdx.y) return;  // the join counts the pieces the same way
+        total = total < first + p.grad_pieces ? total : first + p.grad_pieces;
+    }
+    int load_g = steps ? first / steps : 0, load_step = first - load_g * steps;
+    int step = load_step;
+    if constexpr (KLDS) {
+        const AttnTile<DP, BN, 8> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane);
+        tk.load(smem, j0, wave);
+    }
+    AttnTile<DP, STEP, 8> tq(nullptr, p.qs[1], s.queries, d, wave, lane), tg(nullptr, p.os[1], s.queries, d, wave, lane);
+    auto load = [&](int at) {  // the next step of the sequence
+        const int h = hk * p.group + load_g, i0 = lo + load_step * STEP;
+        char *to = tiles + at * 2 * TILE;
+        tq.base = p.q + b * p.qs[0] + h * p.qs[2];
+        tg.base = p.dout + b * p.os[0] + h * p.os[2];
+        tq.load(to, i0, wave);
+        tg.load(to + TILE, i0, wave);
+        // a row's two numbers: one row per lane of the first waves
+        constexpr int WAVES = STEP / 64;
+        if (wave < 2 * WAVES) {
+            const int part = wave % WAVES * 64, which = wave / WAVES;
+            const float *from = (which ? p.ndelta : p.nlse) + ((int64_t)b * p.hq + h) * p.tq + i0 + part;
+            const int left = s.queries - i0 - part;
+            const buf_rsrc rs = make_rsrc(from, left > 0 ? (uint32_t)(left < 64 ? left : 64) * 4u : 0u);
+#if defined(__HIP_DEVICE_COMPILE__)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(rows_at + (at * 2 + which) * STEP + part), 4, lane * 4,
+                                                     0, 0, 0);
+#endif
+        }
+        if (++load_step == steps) {
+            load_step = 0;
+            ++load_g;
+        }
+    };
+    if (first < total) load(0);
     half8_t k[KLDS ? 1 : KK], v[KK];
     {
         const _Float16 *rk = p.k + b * p.ks[0] + j * p.ks[1] + hk * p.ks[2];
@@ -200,61 +240,36 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attention_dkv_kernel(AttnParams
             v[kk] = alive && e < d ? *reinterpret_cast<const half8_t *>(rv + e) : z;
         }
     }
-    if constexpr (KLDS) {
-        const AttnTile<DP, BN, WAVES> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane);
-        tk.load(smem, j0, wave);
-    }
+    // keys past the sample's last take that one's place
+    const AttnRange seen = last < 0 ? AttnRange{0, 0} : attn_seen_by(p, s, j < last ? j : last);
+    const int wave_lo = __builtin_amdgcn_readfirstlane(seen.lo), wave_hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
+    const int wave_lo_all = __builtin_amdgcn_readlane(seen.lo, 31), wave_hi = __builtin_amdgcn_readlane(seen.hi, 31);
     AttnRows<DP> fr;
     AttnCols<DP> fc;
     fr.init(lane);
     fc.init(lane);
     const float c = p.scale * kAttnLog2e;
     f32x16 ak[NT] = {}, av[NT] = {};
-    AttnTile<DP, BM, WAVES> tq(nullptr, p.qs[1], s.queries, d, wave, lane), tg(nullptr, p.os[1], s.queries, d, wave, lane);
-    const int steps = hi > lo ? (hi - lo + BM - 1) / BM : 0, total = steps * p.group;
-    int load_g = 0, load_step = 0;
-    auto load = [&](int at) {  // the next tile of the sequence
-        const int h = hk * p.group + load_g, i0 = lo + load_step * BM;
-        char *to = tiles + at * 2 * TILE;
-        tq.base = p.q + b * p.qs[0] + h * p.qs[2];
-        tg.base = p.dout + b * p.os[0] + h * p.os[2];
-        tq.load(to, i0, wave);
-        tg.load(to + TILE, i0, wave);
-        // a row's two numbers: waves 0 and 1, one row per lane
-        if (wave < 2) {
-            const float *from = (wave ? p.ndelta : p.nlse) + ((int64_t)b * p.hq + h) * p.tq + i0;
-            const int left = s.queries - i0;
-            const buf_rsrc rs = make_rsrc(from, left > 0 ? (uint32_t)(left < BM ? left : BM) * 4u : 0u);
-#if defined(__HIP_DEVICE_COMPILE__)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(rows_at + (at * 2 + wave) * BM), 4, lane * 4, 0, 0, 0);
-#endif
-        }
-        if (++load_step == steps) {
-            load_step = 0;
-            ++load_g;
-        }
-    };
-    int buf = 0, step = 0;
-    if (total) load(0);
-    for (int n = 0; n < total; ++n) {
+    int buf = 0;
+    for (int n = first; n < total; ++n) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const char *qs = tiles + buf * 2 * TILE, *gs = qs + TILE;
-        const float *starts = rows_at + buf * 2 * BM;
-        const int i0 = lo + step * BM;
+        const char *qs = tiles + buf * 2 * TILE + qg * BM * DP * 2, *gs = qs + TILE;
+        const float *starts = rows_at + buf * 2 * STEP + qg * BM;
+        const int i0 = lo + step * STEP + qg * BM;
         buf ^= 1;
         if (++step == steps) step = 0;
         if (n + 1 < total) load(buf);
         if (i0 + BM <= wave_lo || i0 >= wave_hi) continue;
         const bool edge = i0 < wave_lo_all || i0 + BM > wave_hi_all;
         const uint32_t qr = lds_address(qs) + fr.off;
-        const uint32_t kr = opaque(lds_address(smem) + wave * 32 * DP * 2 + fr.off);
-        static_for<2>([&](auto sub) {
+        const uint32_t kr = opaque(lds_address(smem) + kw * 32 * DP * 2 + fr.off);
+        static_for<XN>([&](auto sub) {
             constexpr int T = decltype(sub)::value;
             f32x16 x, y;
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
                 const f32x4 sx = *reinterpret_cast<const f32x4 *>(starts + 32 * T + acc_row(e, lane >> 5));
-                const f32x4 sy = *reinterpret_cast<const f32x4 *>(starts + BM + 32 * T + acc_row(e, lane >> 5));
+                const f32x4 sy = *reinterpret_cast<const f32x4 *>(starts + STEP + 32 * T + acc_row(e, lane >> 5));
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     x[e + m] = sx[m];
@@ -267,7 +282,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attention_dkv_kernel(AttnParams
                     x = mfma_32x32x16<E>(fr.read(qr, 32 * T, kk), fr.read(kr, 0, kk), x);
                 else
                     x = mfma_32x32x16<E>(fr.read(qr, 32 * T, kk), k[kk], x);
-                y = mfma_32x32x16<E>(fr.read(qr, BM + 32 * T, kk), v[kk], y);
+                y = mfma_32x32x16<E>(fr.read(qr, STEP + 32 * T, kk), v[kk], y);
             }
             if (edge) {
                 const int from = seen.lo - i0, to = seen.hi - i0;
@@ -296,7 +311,37 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attention_dkv_kernel(AttnParams
             });
         });
     }
+    // without a step, k is still on its way into LDS
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if constexpr (QG > 1) {
+        float *sums = reinterpret_cast<float *>(smem);
+        static_for<2>([&](auto w) {
+            auto &acc = decltype(w)::value ? av : ak;
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the buffers are free
+            if (qg > 0) acc_put<NT>(sums + ((qg - 1) * KW + kw) * NT * 1024, acc, lane);
+            __syncthreads();
+            if (qg == 0) {
+#pragma unroll 1
+                for (int o = 0; o < QG - 1; ++o) acc_join<NT>(sums + (o * KW + kw) * NT * 1024, acc, 1.0f, 1.0f, lane);
+            }
+        });
+        if (qg > 0) return;
+    }
     if (j >= p.tk) return;
+    if (p.grad_splits > 1) {
+        const int64_t at = (((int64_t)blockIdx.y * heads + head) * p.tk + j) * d;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const int e0 = 32 * t + acc_row(e, lane >> 5);
+                if (e0 < d) {
+                    *reinterpret_cast<f32x4 *>(p.part_dk + at + e0) = f32x4{ak[t][e], ak[t][e + 1], ak[t][e + 2], ak[t][e + 3]};
+                    *reinterpret_cast<f32x4 *>(p.part_dv + at + e0) = f32x4{av[t][e], av[t][e + 1], av[t][e + 2], av[t][e + 3]};
+                }
+            }
+        return;
+    }
     if (!alive) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) ak[t] = av[t] = f32x16{};
@@ -313,34 +358,89 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attention_dkv_kernel(AttnParams
     }
 }
 
-template <typename E, int DP>
-static void launch_grad(const AttnParams &p, hipStream_t s) {
-    const int heads = p.n * p.hk;
-    if (p.tq > 0) {
-        const int tiles = (p.rows + kAttnTileRows - 1) / kAttnTileRows;
-        attention_dq_kernel<E, DP, kAttnTileRows / 32><<<dim3(heads * tiles), dim3(kAttnTileRows * 2), 0, s>>>(p);
+// The pieces of each key's steps added in their order: four elements per lane.
+template <typename E>
+__global__ __launch_bounds__(256) void attention_dkv_join_kernel(AttnParams p, int tile_keys, int tile_tokens, int align) {
+    const int heads = p.n * p.hk, quads = p.d >> 2;
+    const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x, keys = (int64_t)heads * p.tk;
+    if (unit >= keys * quads) return;
+    const int64_t key = unit / quads;
+    const int e = (int)(unit - key * quads) * 4, head = (int)(key / p.tk), j = (int)(key - (int64_t)head * p.tk);
+    const int b = head / p.hk, hk = head - b * p.hk;
+    const AttnSample s = attn_sample(p, b);
+    int pieces = 0;  // of this key's tile
+    if (j < s.keys) {
+        const int j0 = j / tile_keys * tile_keys, jl = j0 + tile_keys - 1;
+        const int lo = attn_seen_by(p, s, j0).lo & ~(align - 1), hi = attn_seen_by(p, s, jl < s.keys ? jl : s.keys - 1).hi;
+        const int total = hi > lo ? (hi - lo + tile_tokens - 1) / tile_tokens * p.group : 0;
+        pieces = (total + p.grad_pieces - 1) / p.grad_pieces;
     }
-    if (p.tk > 0 && (p.dk || p.dv))
-        attention_dkv_kernel<E, DP, 8><<<dim3(heads * ((p.tk + 255) / 256)), dim3(512), 0, s>>>(p);
+    f32x4 ak = {}, av = {};
+    for (int z = 0; z < pieces; ++z) {
+        const int64_t at = (z * keys + key) * p.d + e;
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(p.part_dk + at), c = *reinterpret_cast<const f32x4 *>(p.part_dv + at);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            ak[m] += a[m];
+            av[m] += c[m];
+        }
+    }
+    half4_t ok, ov;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        ok[m] = from_f32<E>(ak[m] * p.scale);
+        ov[m] = from_f32<E>(av[m]);
+    }
+    if (p.dk) *reinterpret_cast<half4_t *>(p.dk + b * p.ks[0] + j * p.ks[1] + hk * p.ks[2] + e) = ok;
+    if (p.dv) *reinterpret_cast<half4_t *>(p.dv + b * p.vs[0] + j * p.vs[1] + hk * p.vs[2] + e) = ov;
+}
+
+template <typename E, int DP>
+static void launch_grad(const AttnParams &p, AttnTileKind kq, AttnTileKind kkv, hipStream_t s) {
+    const int heads = p.n * p.hk;
+    const dim3 block(512);
+    if (p.tq > 0) {
+        const int rows = attn_tile(kq).rows;
+        const dim3 grid((uint32_t)(heads * ((p.rows + rows - 1) / rows)));
+        switch (kq) {
+            case kAttn64: attention_dq_kernel<E, DP, 2, 4, 32><<<grid, block, 0, s>>>(p); break;
+            case kAttn128: attention_dq_kernel<E, DP, 4, 2, 64><<<grid, block, 0, s>>>(p); break;
+            default: attention_dq_kernel<E, DP, 8, 1, 64><<<grid, block, 0, s>>>(p); break;
+        }
+    }
+    if (p.tk > 0 && (p.dk || p.dv)) {
+        const int keys = attn_tile(kkv).rows;
+        const dim3 grid((uint32_t)(heads * ((p.tk + keys - 1) / keys)), (uint32_t)p.grad_splits);
+        switch (kkv) {
+            case kAttn64: attention_dkv_kernel<E, DP, 2, 4, 32><<<grid, block, 0, s>>>(p); break;
+            case kAttn128: attention_dkv_kernel<E, DP, 4, 2, 32><<<grid, block, 0, s>>>(p); break;
+            default: attention_dkv_kernel<E, DP, 8, 1, 64><<<grid, block, 0, s>>>(p); break;
+        }
+        if (p.grad_splits > 1) {
+            const int64_t count = (int64_t)heads * p.tk * (p.d / 4);
+            attention_dkv_join_kernel<E><<<dim3((uint32_t)((count + 255) / 256)), dim3(256), 0, s>>>(
+                p, keys, attn_grad_step(kkv), kkv == kAttn256 ? 64 : 32);
+        }
+    }
 }
 
 template <typename E>
-static void launch_grad_dim(const AttnParams &p, hipStream_t s) {
+static void launch_grad_dim(const AttnParams &p, AttnTileKind kq, AttnTileKind kkv, hipStream_t s) {
     if (p.d <= 32)
-        launch_grad<E, 32>(p, s);
+        launch_grad<E, 32>(p, kq, kkv, s);
     else if (p.d <= 64)
-        launch_grad<E, 64>(p, s);
+        launch_grad<E, 64>(p, kq, kkv, s);
     else if (p.d <= 96)
-        launch_grad<E, 96>(p, s);
+        launch_grad<E, 96>(p, kq, kkv, s);
     else
-        launch_grad<E, 128>(p, s);
+        launch_grad<E, 128>(p, kq, kkv, s);
 }
 
-hipError_t launch_attention_grad(const AttnParams &p, hipStream_t s) {
+hipError_t launch_attention_grad(const AttnParams &p, AttnTileKind kq, AttnTileKind kkv, hipStream_t s) {
     if (p.bf16)
-        launch_grad_dim<__bf16>(p, s);
+        launch_grad_dim<__bf16>(p, kq, kkv, s);
     else
-        launch_grad_dim<_Float16>(p, s);
+        launch_grad_dim<_Float16>(p, kq, kkv, s);
     return hipGetLastError();
 }
 

@@ -143,7 +143,7 @@ struct RopeParams {
 hipError_t launch_rope3d(const RopeParams &p, hipStream_t s);
 
 // ---- attention
-constexpr int kAttnMaxDim = 128;
+constexpr int kAttnMaxDim = 128, kAttnFewRows = 32;
 struct AttnParams {
     const _Float16 *q, *k, *v;
     _Float16 *o;                 // backward: read
@@ -162,16 +162,30 @@ struct AttnParams {
     // backward
     const _Float16 *dout;
     _Float16 *dq, *dk, *dv;
-    float *nlse, *ndelta;        // [n * hk][rows] in the workspace
+    float *nlse, *ndelta;        // [n][hq][tq] in the workspace: see attention_grad.hip
+    // dk and dv: `grad_splits` pieces of each key tile's steps, of grad_pieces steps each; more than
+    // one leave partials, [grad_splits][n * hk][tk][d]
+    int32_t grad_splits, grad_pieces;
+    float *part_dk, *part_dv;
 };
-struct AttnKernel {
+// Tiles of the kernels: rows (query tokens times the query heads of a key head) and
+// keys of a step.  kAttnFew: all rows of a key head in one tile.
+enum AttnTileKind { kAttnFew = 0, kAttn64 = 1, kAttn128 = 2, kAttn256 = 3 };
+struct AttnTileSize {
     const char *name;
-    int rows, keys, threads;     // of a workgroup's tile
+    int rows, keys, threads;
 };
-// few: all rows of a key head in one tile of kAttnFewRows
-constexpr int kAttnFewRows = 32, kAttnFewKeys = 128, kAttnTileRows = 256, kAttnTileKeys = 64;
-hipError_t launch_attention(const AttnParams &p, bool few, hipStream_t s);
-hipError_t launch_attention_grad(const AttnParams &p, hipStream_t s);
+constexpr AttnTileSize attn_tile(AttnTileKind k) {
+    return k == kAttnFew ? AttnTileSize{"attention_few", 32, 128, 256}
+         : k == kAttn64  ? AttnTileSize{"attention_64x128", 64, 128, 512}
+         : k == kAttn128 ? AttnTileSize{"attention_128x128", 128, 128, 512}
+                         : AttnTileSize{"attention_256x64", 256, 64, 512};
+}
+hipError_t launch_attention(const AttnParams &p, AttnTileKind kind, hipStream_t s);
+// dq by tiles of kind_q; dk and dv by tiles of as many keys as kind_kv has rows, and 64
+// query tokens (kAttn64: 128) to a step.
+constexpr int attn_grad_step(AttnTileKind kind) { return kind == kAttn64 ? 128 : 64; }
+hipError_t launch_attention_grad(const AttnParams &p, AttnTileKind kind_q, AttnTileKind kind_kv, hipStream_t s);
 
 // ---- adamw
 constexpr int kAdamwBlock = 128;    // elements that share a scale

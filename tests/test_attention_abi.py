@@ -119,8 +119,8 @@ def test_fused_projections_are_told_apart():
 def test_workspace_sizes_and_kernels():
     one = c3d.attention_plan(desc(tq=1))
     many = c3d.attention_plan(desc(tq=1000))
-    assert one.info().kernel_name == b"attention_few" and many.info().kernel_name == b"attention_tile"
-    assert one.info().tile_rows == 32
+    assert one.info().kernel_name == b"attention_few" and one.info().tile_rows == 32
+    assert many.info().kernel_name in (b"attention_64x128", b"attention_128x128", b"attention_256x64")
     assert many.info().backward_workspace_bytes == c3d.attention_backward_workspace(many) >= 2 * 4 * 2 * 4 * 1000
     assert c3d.attention_plan(desc(n=0)).workspace_bytes == 0
     assert c3d.attention_plan(desc(tk=0)).workspace_bytes == 0

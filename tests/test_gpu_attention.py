@@ -198,6 +198,19 @@ def ident(c):
     return "-".join("%s=%s" % (k, v if k != "lengths" else "given") for k, v in c.items())
 
 
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("tile", ["attention_64x128", "attention_128x128", "attention_256x64"])
+@pytest.mark.parametrize("case", [c for c in CASES if c.get("tq", 64) > 1 and c.get("tk", 64) > 40], ids=ident)
+def test_every_tile_and_pieces(case, tile, splits, monkeypatch):
+    monkeypatch.setenv("CONV3D_ATTENTION_TILE", tile)
+    monkeypatch.setenv("CONV3D_ATTENTION_SPLITS", str(splits))
+    c = Case(**case)
+    assert c.plan.info().kernel_name.decode() == tile
+    c.forward()
+    c.check_forward()
+    c.check_backward(c.backward())
+
+
 @pytest.mark.parametrize("case", CASES, ids=ident)
 def test_forward_and_gradients(case):
     c = Case(**case)
