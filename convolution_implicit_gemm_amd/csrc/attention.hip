@@ -110,19 +110,25 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_tile_kernel(A
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         const char *ks = smem + buf * 2 * TILE + kg * BN * DP * 2, *vs = ks + TILE;
         buf ^= 1;
-        if (at + STEP < hi) {
-            char *next = smem + buf * 2 * TILE;
-            tk.load(next, at + STEP, wave);
-            tv.load(next + TILE, at + STEP, wave);
-        }
+        auto next = [&]() {
+            if (at + STEP < hi) {
+                char *to = smem + buf * 2 * TILE;
+                tk.load(to, at + STEP, wave);
+                tv.load(to + TILE, at + STEP, wave);
+            }
+        };
         const int j0 = at + kg * BN;
-        if (j0 + BN <= wave_lo || j0 >= wave_hi) continue;
+        if (j0 + BN <= wave_lo || j0 >= wave_hi) {
+            next();
+            continue;
+        }
         const uint32_t kr = lds_address(ks) + fk.off;
         f32x16 x[XN] = {};
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
             for (int t = 0; t < XN; ++t) x[t] = mfma_32x32x16<E>(fk.read(kr, 32 * t, kk), q[kk], x[t]);
+        next();  // behind the products, which it then does not hold up
         if (j0 < wave_lo_all || j0 + BN > wave_hi_all) {
             const int from = seen.lo - j0, to = seen.hi - j0;
 #pragma unroll

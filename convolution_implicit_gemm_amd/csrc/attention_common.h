@@ -80,13 +80,14 @@ __device__ __forceinline__ int opaque(int v) {
     return v;
 }
 
-// Rows of a tensor straight into LDS tiles of ROWS rows, by WAVES waves.
-template <int DP, int ROWS, int WAVES>
+// Rows of a tensor straight into LDS tiles of ROWS rows, by WAVES waves.  LEAN: one offset
+// for all of a lane's loads, each with a resource of its own (a dozen scalar instructions), where
+// the rows between them swizzle alike: for kernels short of registers.
+template <int DP, int ROWS, int WAVES, bool LEAN = false>
 struct AttnTile {
     static constexpr int CH = DP / 8, LOADS = ROWS * CH / 64, NI = (LOADS + WAVES - 1) / WAVES;
     static constexpr int STEP = WAVES * 64 / CH;  // rows from one of a lane's loads to the next
-    // where these rows swizzle alike one offset does for all loads, each with a resource of its own
-    static constexpr bool ONE = WAVES * 64 % CH == 0 && STEP % 16 == 0;
+    static constexpr bool ONE = LEAN && WAVES * 64 % CH == 0 && STEP % 16 == 0;
     const _Float16 *base;  // row 0
     int64_t stride;
     int rows, dim;

@@ -100,13 +100,18 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         const char *ks = smem + buf * 2 * TILE + kg * BN * DP * 2;
         buf ^= 1;
-        if (at + STEP < hi) {
-            char *next = smem + buf * 2 * TILE;
-            tk.load(next, at + STEP, wave);
-            tv.load(next + TILE, at + STEP, wave);
-        }
+        auto next = [&]() {
+            if (at + STEP < hi) {
+                char *to = smem + buf * 2 * TILE;
+                tk.load(to, at + STEP, wave);
+                tv.load(to + TILE, at + STEP, wave);
+            }
+        };
         const int j0 = at + kg * BN;
-        if (j0 + BN <= wave_lo || j0 >= wave_hi) continue;
+        if (j0 + BN <= wave_lo || j0 >= wave_hi) {
+            next();
+            continue;
+        }
         const bool edge = j0 < wave_lo_all || j0 + BN > wave_hi_all;
         const uint32_t kr = lds_address(ks) + fr.off;
         static_for<XN>([&](auto sub) {
@@ -119,6 +124,7 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
                 x = mfma_32x32x16<E>(fr.read(kr, 32 * T, kk), q[kk], x);
                 y = mfma_32x32x16<E>(fr.read(kr, STEP + 32 * T, kk), go[kk], y);
             }
+            if constexpr (T == 0) next();  // behind the products, which it then does not hold up
             if (edge) {
                 const int from = seen.lo - j0, to = seen.hi - j0;
 #pragma unroll
@@ -202,7 +208,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
         const AttnTile<DP, BN, 8> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane);
         tk.load(smem, j0, wave);
     }
-    AttnTile<DP, STEP, 8> tq(nullptr, p.qs[1], s.queries, d, wave, lane), tg(nullptr, p.os[1], s.queries, d, wave, lane);
+    AttnTile<DP, STEP, 8, true> tq(nullptr, p.qs[1], s.queries, d, wave, lane), tg(nullptr, p.os[1], s.queries, d, wave, lane);
     auto load = [&](int at) {  // the next step of the sequence
         const int h = hk * p.group + load_g, i0 = lo + load_step * STEP;
         char *to = tiles + at * 2 * TILE;
@@ -258,8 +264,10 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
         const int i0 = lo + step * STEP + qg * BM;
         buf ^= 1;
         if (++step == steps) step = 0;
-        if (n + 1 < total) load(buf);
-        if (i0 + BM <= wave_lo || i0 >= wave_hi) continue;
+        if (i0 + BM <= wave_lo || i0 >= wave_hi) {
+            if (n + 1 < total) load(buf);
+            continue;
+        }
         const bool edge = i0 < wave_lo_all || i0 + BM > wave_hi_all;
         const uint32_t qr = lds_address(qs) + fr.off;
         const uint32_t kr = opaque(lds_address(smem) + kw * 32 * DP * 2 + fr.off);
@@ -283,6 +291,9 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
                 else
                     x = mfma_32x32x16<E>(fr.read(qr, 32 * T, kk), k[kk], x);
                 y = mfma_32x32x16<E>(fr.read(qr, STEP + 32 * T, kk), v[kk], y);
+            }
+            if constexpr (T == 0) {
+                if (n + 1 < total) load(buf);  // behind the products, which it then does not hold up
             }
             if (edge) {
                 const int from = seen.lo - i0, to = seen.hi - i0;
