@@ -535,45 +535,60 @@ __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
     }
 }
 
-// The pieces of each row's keys joined, in their order: a wave per row, two elements
-// per lane.
-template <typename E>
+// The pieces of each row's keys joined, in a fixed order: a workgroup per row, LANES lanes of four
+// elements to a piece, the pieces in turn over the workgroup, whose sums meet in LDS.
+template <typename E, int LANES>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnParams p) {
-    const int heads = p.n * p.hk, lane = threadIdx.x & 63;
-    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), count = (int64_t)heads * p.rows;
-    if (unit >= count) return;
+    constexpr int SETS = 256 / LANES;
+    __shared__ __attribute__((aligned(16))) float sums[256 * 4];
+    __shared__ float2 ml[SETS];
+    const int heads = p.n * p.hk, set = threadIdx.x / LANES, l = threadIdx.x % LANES, e = 4 * l;
+    const int64_t unit = blockIdx.x, count = (int64_t)heads * p.rows;
     const int head = (int)(unit / p.rows), row = (int)(unit - (int64_t)head * p.rows);
+    float m = -__builtin_inff(), sum = 0.0f;
+    f32x4 v = {};
+#pragma unroll 2
+    for (int k = set; k < p.splits; k += SETS) {
+        const float2 x = p.part_ml[k * count + unit];
+        f32x4 a = {};
+        if (e < p.d) a = *reinterpret_cast<const f32x4 *>(p.part_o + (k * count + unit) * p.d + e);
+        const float top = fmaxf(m, x.x), use = top == -__builtin_inff() ? 0.0f : top;
+        const float own = __builtin_amdgcn_exp2f(m - use), f = __builtin_amdgcn_exp2f(x.x - use);
+        m = top;
+        sum = fmaf(sum, own, x.y * f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = fmaf(v[c], own, a[c] * f);
+    }
+    *reinterpret_cast<f32x4 *>(sums + threadIdx.x * 4) = v;
+    if (l == 0) ml[set] = make_float2(m, sum);
+    __syncthreads();
+    if (set > 0) return;
+#pragma unroll
+    for (int k = 1; k < SETS; ++k) m = fmaxf(m, ml[k].x);
+    const float use = m == -__builtin_inff() ? 0.0f : m;
+    v = f32x4{};
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < SETS; ++k) {
+        const float2 x = ml[k];
+        const float f = __builtin_amdgcn_exp2f(x.x - use);
+        sum = fmaf(x.y, f, sum);
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(sums + (k * LANES + l) * 4);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = fmaf(a[c], f, v[c]);
+    }
     const int b = head / p.hk, hk = head - b * p.hk;
     const int ti = row / p.group, h = hk * p.group + row - ti * p.group;
     const bool live = ti < attn_sample(p, b).queries;
-    float m = -__builtin_inff();
-    for (int k = lane; k < p.splits; k += 64) m = fmaxf(m, p.part_ml[k * count + unit].x);
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
-    const float use = m == -__builtin_inff() ? 0.0f : m;
-    const int e = 2 * lane;
-    float sum = 0.0f, v0 = 0.0f, v1 = 0.0f;
-#pragma unroll 4
-    for (int k = 0; k < p.splits; ++k) {
-        const float2 x = p.part_ml[k * count + unit];
-        const float f = __builtin_amdgcn_exp2f(x.x - use);
-        sum = fmaf(x.y, f, sum);
-        if (e < p.d) {
-            const float2 a = *reinterpret_cast<const float2 *>(p.part_o + (k * count + unit) * p.d + e);
-            v0 = fmaf(a.x, f, v0);
-            v1 = fmaf(a.y, f, v1);
-        }
-    }
     const float inv = attn_inverse(sum);
-    if (lane == 0 && p.lse)
+    if (l == 0 && p.lse)
         p.lse[((int64_t)b * p.hq + h) * p.tq + ti] =
             live ? (use + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -__builtin_inff();
     if (e < p.d) {
-        typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-        h2 o;
-        o[0] = live ? from_f32<E>(v0 * inv) : (_Float16)0.0f;
-        o[1] = live ? from_f32<E>(v1 * inv) : (_Float16)0.0f;
-        *reinterpret_cast<h2 *>(p.o + b * p.os[0] + ti * p.os[1] + h * p.os[2] + e) = o;
+        half4_t o;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = live ? from_f32<E>(v[c] * inv) : (_Float16)0.0f;
+        *reinterpret_cast<half4_t *>(p.o + b * p.os[0] + ti * p.os[1] + h * p.os[2] + e) = o;
     }
 }
 
@@ -588,8 +603,7 @@ static void launch_forward(const AttnParams &p, AttnTileKind kind, hipStream_t s
         default: attention_phase_kernel<E, DP><<<grid, block, 0, s>>>(p); break;
     }
     if (p.splits > 1) {
-        const int64_t count = (int64_t)heads * p.rows;
-        attention_join_kernel<E><<<dim3((uint32_t)((count + 3) / 4)), dim3(256), 0, s>>>(p);
+        attention_join_kernel<E, (DP > 64 ? 32 : DP / 4)><<<dim3((uint32_t)(heads * p.rows)), dim3(256), 0, s>>>(p);
     }
 }
 

@@ -69,14 +69,23 @@ struct Choice {
 
 enum Pass { kForward, kDq, kDkv };
 
-// A step of a workgroup alone on its CU: two waves to a SIMD, each with as many MFMAs (32 cycles)
-// as its product of 32 rows and `keys` / groups needs, or as many vector instructions.
-double step_us(Pass pass, AttnTileKind kind, int dim) {
-    const int dp = (dim + 31) / 32 * 32, sub = kind == kAttn64 || (pass == kDkv && kind == kAttn128) ? 1 : 2;
-    const int products = pass == kForward ? 2 : pass == kDq ? 3 : 4;
-    const double matrix = products * (dp / 16) * 32.0, vector = pass == kForward ? 380.0 : 330.0;
-    return 2.0 * sub * ((matrix > vector ? matrix : vector) + 110.0) / 2200.0 + 0.15;
-}
+// Fitted to 3700 measured calls (heads of 32, 64, 96 and 128, 64 to 9216 tokens, 2 to 48 heads, with and
+// without a mask, 1 to 16 pieces): the choice is then 1 to 3% off the fastest kernel on average.
+// Per pass: the time of a call besides its steps (kDkv: with that of the row sums), of a
+// workgroup besides its steps, what joining the waves adds to that, the share of the longest workgroup
+// that the end of unequal ones waits for, a second launch to join pieces, and the partials' us per 2^20 or so values.
+struct PassCost {
+    double call, group, joined, tail, join, part;
+};
+constexpr PassCost kPass[3] = {
+    {4.6, 1.4, 0.0, 0.29, 3.9, 2.4}, {1.0, 4.5, 2.0, 0.2, 3.0, 2.0}, {9.7, 0.0, 1.4, 0.28, 3.4, 2.7}};
+// A step of a workgroup by pass, tile (64, 128, 256 rows) and padded head (32, 64, 96, 128).
+constexpr double kStepUs[3][3][4] = {
+    {{0.48, 0.73, 1.26, 1.47}, {0.89, 1.20, 1.60, 2.00}, {1.02, 1.17, 1.43, 1.53}},
+    {{0.33, 0.84, 1.40, 1.70}, {0.92, 1.48, 2.07, 2.63}, {1.02, 1.50, 1.93, 2.27}},
+    {{0.69, 1.49, 2.03, 3.05}, {0.72, 1.21, 1.71, 2.21}, {1.45, 2.03, 2.81, 3.95}}};
+// Pieces are taken where they save a tenth: their join is a launch more.
+constexpr double kPieceMargin = 1.1;
 
 AttnTileKind forced_kind(AttnTileKind otherwise, bool few) {
     const char *v = getenv("CONV3D_ATTENTION_TILE");
@@ -97,29 +106,35 @@ Choice choose(Pass pass, const Problem &w, bool splits) {
     const AttnTileKind only = forced_kind(few ? kAttnFew : kAttn256, few);
     const bool forced = getenv("CONV3D_ATTENTION_TILE") != nullptr;
     for (AttnTileKind kind : {kAttn256, kAttn128, kAttn64, kAttnFew}) {
-        if (kind == kAttnFew && !few) continue;
-        if (forced && kind != only) continue;
+        if (forced ? kind != only : (kind == kAttnFew) != few) continue;
         const AttnTileSize t = attn_tile(kind);
         const int64_t tiles = w.heads * ((w.rows + t.rows - 1) / t.rows);
         const double keys = pass == kDkv ? attn_grad_step(kind) : t.keys;
-        for (int z = 1; z <= kMaxPieces; z += z < 8 ? 1 : z < 32 ? 4 : 16) {
+        for (int z = 1; z <= kMaxPieces; z += z < 8 ? 1 : z < 16 ? 2 : z < 32 ? 4 : 16) {
             const int pieces = forced_pieces(z);
             const double most = std::ceil(std::ceil(w.most / keys) / pieces), mean = w.mean / keys / pieces;
-            if (z > 1 && (!splits || most < 1.5 || tiles * z > 4 * kAttnCUs)) break;
+            if (z > 1 && (!splits || z > w.most / keys || tiles * z > (few ? 1 : 4) * kAttnCUs)) break;
             const double units = (double)tiles * pieces, rounds = units / kAttnCUs;
             double us;
             if (kind == kAttnFew) {
-                // the steps' loads are on their way one step ahead; all of them share the memory's rate
-                const double bytes = 512.0 * w.dim, share = (units < kAttnCUs ? units : kAttnCUs) * bytes / 5.5e6;
-                us = 3.2 + std::ceil(rounds) * most * (share > 0.9 ? share : 0.9);
+                // a step's latency (from the last-level cache or from memory), the first ones' longer, or all
+                // workgroups' shares of the memory's rate
+                const bool cached = 4.0 * w.heads * w.most * w.dim < 2e8;
+                const double least = w.dim > 64 ? (cached ? 0.87 : 1.45) : (cached ? 0.61 : 0.8);
+                const double share = (units < kAttnCUs ? units : kAttnCUs) * 512.0 * w.dim / 5.8e6;
+                const double step = std::sqrt(std::hypot(least * least, share * share));
+                us = 3.6 + std::ceil(rounds) * most * step + 0.4 * least * (most < 5 ? most : 5) +
+                     (pieces > 1 ? 2.2 + 0.02 * pieces : 0.0);
             } else {
-                const double c = step_us(pass, kind, w.dim), fixed = 1.2 + (kind == kAttn256 ? 0.0 : 1.0);
+                const PassCost &k = kPass[pass];
+                const double c = kStepUs[pass][kind - kAttn64][(w.dim - 1) / 32], fixed = k.group + (kind == kAttn256 ? 0.0 : k.joined);
                 // equal workgroups run in whole rounds; unequal ones, longest first, fill up
                 const double even = std::ceil(rounds) * (most * c + fixed);
-                const double fill = rounds * (mean * c + fixed) + 0.4 * most * c, longest = most * c + fixed;
-                us = 2.0 + (w.mean > 0.95 * w.most ? even : fill > longest ? fill : longest);
+                const double fill = rounds * (mean * c + fixed) + k.tail * most * c, longest = most * c + fixed;
+                us = k.call + (w.mean > 0.95 * w.most ? even : fill > longest ? fill : longest);
             }
-            if (pieces > 1) us += 3.0 + (double)w.heads * w.rows * w.dim * pieces * (pass == kDkv ? 16.0 : 8.0) / 4e6;
+            if (pieces > 1 && kind != kAttnFew)
+                us = kPieceMargin * (us + kPass[pass].join + (double)w.heads * w.rows * w.dim * pieces * kPass[pass].part / 1e6);
             if (best.us < 0.0 || us < best.us) best = {kind, pieces, us};
             if (pieces != z) break;  // forced
         }
