@@ -8,10 +8,9 @@
 namespace c3d {
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-// The largest of 16 adjacent lanes' values, to all of them.
-__device__ __forceinline__ float max16(float v) {
+// The largest of the values of lanes 32 h .. 32 h + 31, to all of them.
+__device__ __forceinline__ float max32(float v) {
 #if defined(__HIP_DEVICE_COMPILE__)
     const auto step = [&](auto ctrl) {
         const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, false);
@@ -21,213 +20,244 @@ __device__ __forceinline__ float max16(float v) {
     step(std::integral_constant<int, 0x4E>{});   // quad_perm [2,3,0,1]
     step(std::integral_constant<int, 0x141>{});  // row_half_mirror
     step(std::integral_constant<int, 0x140>{});  // row_mirror
+    uint32_t x = __builtin_bit_cast(uint32_t, v), y = x;
+    asm("" : "+v"(y));  // a swap of one value with itself: the compiler takes both results for the same
+    const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    v = fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
 #endif
     return v;
 }
 
 __device__ __forceinline__ float power_of_two(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
 
-// 8 codes -> values times `unit`
-__device__ __forceinline__ void decode8(u32x2_t c, float unit, float (&x)[8]) {
+// 4 codes -> values times `unit`
+__device__ __forceinline__ void decode4(uint32_t c, float unit, float (&x)[4]) {
 #if defined(__HIP_DEVICE_COMPILE__)
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[w], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[w], true);
-        x[4 * w] = a[0] * unit;
-        x[4 * w + 1] = a[1] * unit;
-        x[4 * w + 2] = b[0] * unit;
-        x[4 * w + 3] = b[1] * unit;
-    }
+    const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
+    x[0] = a[0] * unit;
+    x[1] = a[1] * unit;
+    x[2] = b[0] * unit;
+    x[3] = b[1] * unit;
 #endif
 }
 
 // The block's power e: the least from -126 on with its largest finite value at most
-// 448 * 2^e (448 = 7/8 * 2^9, the largest e4m3 number).  The block is 16 lanes' 8 values.
-__device__ __forceinline__ int block_power(const float (&x)[8]) {
+// 448 * 2^e (448 = 7/8 * 2^9, the largest e4m3 number).  The block is 32 lanes' 4 values.
+__device__ __forceinline__ int block_power(const float (&x)[4]) {
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const float a = fabsf(x[i]);
         top = fmaxf(top, a < __builtin_inff() ? a : 0.0f);
     }
-    top = max16(top);
-    const uint32_t bits = __builtin_bit_cast(uint32_t, top);
+    const uint32_t bits = __builtin_bit_cast(uint32_t, max32(top));
     const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);  // 1.75 * 2^8 = 448
     return e < -126 ? -126 : e;
 }
 template <bool ROOT>
-__device__ __forceinline__ u32x2_t encode8(const float (&x)[8], int e) {
-    u32x2_t c = {};
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], int e) {
 #if defined(__HIP_DEVICE_COMPILE__)
     const float inv = power_of_two(-e);
-    float y[8];
+    float y[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         y[i] = x[i] * inv;
         if (ROOT) y[i] = x[i] > 0.0f ? fmaxf(y[i], 0x1p-9f) : y[i];  // the least code but 0
     }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * w], y[4 * w + 1], 0, false);
-        v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * w + 2], y[4 * w + 3], v, true);
-        c[w] = (uint32_t)v;
-    }
+    const int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], v, true);
+#else
+    return 0;
 #endif
-    return c;
 }
 
-// 8 elements, or the `left` first of them, as vectors or one by one.
-template <typename T>
-__device__ __forceinline__ void load_f32(const T *p, int left, float (&x)[8]) {
-    if (left >= 8) {
+// FAR: past the caches, for steps whose tensors would only push each other out.
+template <bool FAR, typename T>
+__device__ __forceinline__ T load_of(const void *p) {
+    if constexpr (FAR)
+        return __builtin_nontemporal_load(static_cast<const T *>(p));
+    else
+        return *static_cast<const T *>(p);
+}
+template <bool FAR, typename T>
+__device__ __forceinline__ void store_to(void *p, T v) {
+    if constexpr (FAR)
+        __builtin_nontemporal_store(v, static_cast<T *>(p));
+    else
+        *static_cast<T *>(p) = v;
+}
+
+// 4 elements, or the `left` first of them, as vectors or one by one.
+template <bool FAR>
+__device__ __forceinline__ void load_f32(const float *p, int left, float (&x)[4]) {
+    if (left >= 4) {
+        const f32x4_t v = load_of<FAR, f32x4_t>(p);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const f32x4_t v = *reinterpret_cast<const f32x4_t *>(p + 4 * h);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[4 * h + i] = v[i];
-        }
+        for (int i = 0; i < 4; ++i) x[i] = v[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < left ? p[i] : 0.0f;
+        for (int i = 0; i < 4; ++i) x[i] = i < left ? p[i] : 0.0f;
     }
 }
-__device__ __forceinline__ void store_f32(float *p, int left, const float (&x)[8]) {
-    if (left >= 8) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<f32x4_t *>(p + 4 * h) = f32x4_t{x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]};
+template <bool FAR>
+__device__ __forceinline__ void store_f32(float *p, int left, const float (&x)[4]) {
+    if (left >= 4) {
+        store_to<FAR>(p, f32x4_t{x[0], x[1], x[2], x[3]});
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
             if (i < left) p[i] = x[i];
     }
 }
-template <typename E>
-__device__ __forceinline__ void load_16(const _Float16 *p, int left, float (&x)[8]) {
-    if (left >= 8) {
-        const e16x8_t v = *reinterpret_cast<const e16x8_t *>(p);
+template <typename E, bool FAR>
+__device__ __forceinline__ void load_16(const _Float16 *p, int left, float (&x)[4]) {
+    if (left >= 4) {
+        const e16x4_t v = load_of<FAR, e16x4_t>(p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_f32<E>(v[i]);
+        for (int i = 0; i < 4; ++i) x[i] = to_f32<E>(v[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < left ? to_f32<E>(p[i]) : 0.0f;
+        for (int i = 0; i < 4; ++i) x[i] = i < left ? to_f32<E>(p[i]) : 0.0f;
     }
 }
-template <typename E>
-__device__ __forceinline__ void store_16(_Float16 *p, int left, const float (&x)[8]) {
-    if (left >= 8) {
-        e16x8_t v;
+template <typename E, bool FAR>
+__device__ __forceinline__ void store_16(_Float16 *p, int left, const float (&x)[4]) {
+    if (left >= 4) {
+        e16x4_t v;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = from_f32<E>(x[i]);
-        *reinterpret_cast<e16x8_t *>(p) = v;
+        for (int i = 0; i < 4; ++i) v[i] = from_f32<E>(x[i]);
+        store_to<FAR>(p, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
             if (i < left) p[i] = from_f32<E>(x[i]);
     }
 }
-__device__ __forceinline__ u32x2_t load_codes(const uint8_t *p, int left) {
-    if (left >= 8) return *reinterpret_cast<const u32x2_t *>(p);
-    u32x2_t c = {};
+template <bool FAR>
+__device__ __forceinline__ uint32_t load_codes(const uint8_t *p, int left) {
+    if (left >= 4) return load_of<FAR, uint32_t>(p);
+    uint32_t c = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < left) c[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    for (int i = 0; i < 4; ++i)
+        if (i < left) c |= (uint32_t)p[i] << (8 * i);
     return c;
 }
-__device__ __forceinline__ void store_codes(uint8_t *p, int left, u32x2_t c) {
-    if (left >= 8) {
-        *reinterpret_cast<u32x2_t *>(p) = c;
+template <bool FAR>
+__device__ __forceinline__ void store_codes(uint8_t *p, int left, uint32_t c) {
+    if (left >= 4) {
+        store_to<FAR>(p, c);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < left) p[i] = (uint8_t)(c[i >> 2] >> (8 * (i & 3)));
+    for (int i = 0; i < 4; ++i)
+        if (i < left) p[i] = (uint8_t)(c >> (8 * i));
 }
 
-// A lane takes 8 elements at a time, 16 lanes a block of 128, whose scale they find by
-// themselves; a workgroup p.units times 2048 elements of one tensor.
-template <typename E, bool STATE8, bool GRAD32>
+// sqrt within an ulp, of denormal numbers too.
+__device__ __forceinline__ float root_of(float v) {
+    const bool tiny = v < 0x1p-96f;
+    const float s = __builtin_amdgcn_sqrtf(tiny ? v * 0x1p+64f : v);
+    return tiny ? s * 0x1p-32f : s;
+}
+
+// A lane takes 4 adjacent elements at a time (one access of up to 16 bytes to each array, whole
+// lines of it to a wave), half a wave a block of 128, whose scale it finds by itself; a
+// workgroup adamw_unit() adjacent elements of one tensor, all of them on their way at once, so that
+// workgroups that run together read and write adjacent memory (201 million weights, 8-bit
+// states: 595 us; with 24 times the elements to a workgroup, one after the other, 706 us).
+template <typename E, bool STATE8, bool GRAD32, bool FAR>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamwParams p) {
+    constexpr int PARTS = adamw_unit(FAR) / 1024;
     const int lane = threadIdx.x & 63;
     // the tensor: the last one whose first workgroup is not behind this one
     const int mine = lane < kAdamwTensors ? p.first[lane] : INT_MAX;
-    const int at = __popcll(__builtin_amdgcn_ballot_w64(mine <= (int)blockIdx.x)) - 1;
-    const AdamwTensor &t = p.t[__builtin_amdgcn_readfirstlane(at)];
+    const int at = __builtin_amdgcn_readfirstlane(__popcll(__builtin_amdgcn_ballot_w64(mine <= (int)blockIdx.x)) - 1);
+    const AdamwTensor &t = p.t[at];
     const AdamwHyper h = p.device_hyper ? *p.device_hyper : p.hyper;
     const float keep = 1.0f - h.lr_decay * t.decay;
-    const int64_t first = (int64_t)((int)blockIdx.x - p.first[__builtin_amdgcn_readfirstlane(at)]) * p.units * kAdamwUnit;
-    for (int u = 0; u < p.units; ++u) {
-        const int64_t base = first + (int64_t)u * kAdamwUnit + threadIdx.x * 8;
-        if (first + (int64_t)u * kAdamwUnit >= t.count) break;
-        const int64_t rest = t.count - base;
-        const int left = rest <= 0 ? 0 : rest < 8 ? (int)rest : 8;
-        float g[8], m[8], v[8], w[8];
-        const int64_t block = base / kAdamwBlock;
-        const bool scaled = left > 0;
+    const int64_t unit = (int64_t)((int)blockIdx.x - p.first[at]) * adamw_unit(FAR);
+    float g[PARTS][4], m[PARTS][4], v[PARTS][4], w[PARTS][4];
+    uint32_t cm[PARTS], cv[PARTS];
+    int em[PARTS], ev[PARTS], left[PARTS];
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+        const int64_t base = unit + k * 1024 + threadIdx.x * 4, rest = t.count - base;
+        left[k] = rest <= 0 ? 0 : rest < 4 ? (int)rest : 4;
         if (GRAD32)
-            load_f32(static_cast<const float *>(t.grad) + base, left, g);
+            load_f32<FAR>(static_cast<const float *>(t.grad) + base, left[k], g[k]);
         else
-            load_16<E>(static_cast<const _Float16 *>(t.grad) + base, left, g);
+            load_16<E, FAR>(static_cast<const _Float16 *>(t.grad) + base, left[k], g[k]);
         if (t.master)
-            load_f32(t.master + base, left, w);
+            load_f32<FAR>(t.master + base, left[k], w[k]);
         else
-            load_16<E>(t.param + base, left, w);
+            load_16<E, FAR>(t.param + base, left[k], w[k]);
         if constexpr (STATE8) {
-            const u32x2_t cm = load_codes(static_cast<const uint8_t *>(t.m) + base, left);
-            const u32x2_t cv = load_codes(static_cast<const uint8_t *>(t.v) + base, left);
-            const int em = scaled ? t.m_scale[block] : 0, ev = scaled ? t.v_scale[block] : 0;
-            decode8(cm, ldexpf(1.0f, em - 127), m);
-            decode8(cv, ldexpf(1.0f, ev - 127), v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= v[i];
+            cm[k] = load_codes<FAR>(static_cast<const uint8_t *>(t.m) + base, left[k]);
+            cv[k] = load_codes<FAR>(static_cast<const uint8_t *>(t.v) + base, left[k]);
+            em[k] = left[k] ? t.m_scale[base / kAdamwBlock] : 0;
+            ev[k] = left[k] ? t.v_scale[base / kAdamwBlock] : 0;
         } else {
-            load_f32(static_cast<const float *>(t.m) + base, left, m);
-            load_f32(static_cast<const float *>(t.v) + base, left, v);
+            load_f32<FAR>(static_cast<const float *>(t.m) + base, left[k], m[k]);
+            load_f32<FAR>(static_cast<const float *>(t.v) + base, left[k], v[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+        const int64_t base = unit + k * 1024 + threadIdx.x * 4;
+        if constexpr (STATE8) {
+            decode4(cm[k], ldexpf(1.0f, em[k] - 127), m[k]);
+            decode4(cv[k], ldexpf(1.0f, ev[k] - 127), v[k]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[k][i] *= v[k][i];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = g[i] * h.grad_scale;
-            m[i] = fmaf(m[i], h.beta1, x * h.rest1);
-            v[i] = fmaf(v[i], h.beta2, x * x * h.rest2);
-            const float root = sqrtf(v[i]);
-            w[i] = fmaf(w[i], keep, -h.lr1 * (m[i] / fmaf(root, h.root2, h.eps)));
-            if (STATE8) v[i] = root;
+        for (int i = 0; i < 4; ++i) {
+            const float x = g[k][i] * h.grad_scale;
+            m[k][i] = fmaf(m[k][i], h.beta1, x * h.rest1);
+            v[k][i] = fmaf(v[k][i], h.beta2, x * x * h.rest2);
+            const float root = root_of(v[k][i]);
+            w[k][i] = fmaf(w[k][i], keep, -h.lr1 * (m[k][i] / fmaf(root, h.root2, h.eps)));
+            if (STATE8) v[k][i] = root;
         }
-        if (t.master) store_f32(t.master + base, left, w);
-        if (t.param) store_16<E>(t.param + base, left, w);
+        if (t.master) store_f32<FAR>(t.master + base, left[k], w[k]);
+        if (t.param) store_16<E, FAR>(t.param + base, left[k], w[k]);
         if constexpr (STATE8) {
-            const int em = block_power(m), ev = block_power(v);
-            store_codes(static_cast<uint8_t *>(t.m) + base, left, encode8<false>(m, em));
-            store_codes(static_cast<uint8_t *>(t.v) + base, left, encode8<true>(v, ev));
-            if (scaled && (threadIdx.x & 15) == 0) {
-                t.m_scale[block] = (uint8_t)(em + 127);
-                t.v_scale[block] = (uint8_t)(ev + 127);
+            const int pm = block_power(m[k]), pv = block_power(v[k]);
+            store_codes<FAR>(static_cast<uint8_t *>(t.m) + base, left[k], encode4<false>(m[k], pm));
+            store_codes<FAR>(static_cast<uint8_t *>(t.v) + base, left[k], encode4<true>(v[k], pv));
+            if (left[k] && (threadIdx.x & 31) == 0) {
+                t.m_scale[base / kAdamwBlock] = (uint8_t)(pm + 127);
+                t.v_scale[base / kAdamwBlock] = (uint8_t)(pv + 127);
             }
         } else {
-            store_f32(static_cast<float *>(t.m) + base, left, m);
-            store_f32(static_cast<float *>(t.v) + base, left, v);
+            store_f32<FAR>(static_cast<float *>(t.m) + base, left[k], m[k]);
+            store_f32<FAR>(static_cast<float *>(t.v) + base, left[k], v[k]);
         }
     }
 }
 
-template <typename E>
+template <typename E, bool FAR>
 static void launch(const AdamwParams &p, int64_t blocks, bool state8, bool grad32, hipStream_t s) {
     const dim3 g((uint32_t)blocks), b(256);
     if (state8 && grad32)
-        adamw_kernel<E, true, true><<<g, b, 0, s>>>(p);
+        adamw_kernel<E, true, true, FAR><<<g, b, 0, s>>>(p);
     else if (state8)
-        adamw_kernel<E, true, false><<<g, b, 0, s>>>(p);
+        adamw_kernel<E, true, false, FAR><<<g, b, 0, s>>>(p);
     else if (grad32)
-        adamw_kernel<E, false, true><<<g, b, 0, s>>>(p);
+        adamw_kernel<E, false, true, FAR><<<g, b, 0, s>>>(p);
     else
-        adamw_kernel<E, false, false><<<g, b, 0, s>>>(p);
+        adamw_kernel<E, false, false, FAR><<<g, b, 0, s>>>(p);
 }
 
-hipError_t launch_adamw(const AdamwParams &p, int64_t blocks, bool bf16, bool state8, bool grad32, hipStream_t s) {
-    if (bf16)
-        launch<__bf16>(p, blocks, state8, grad32, s);
+hipError_t launch_adamw(const AdamwParams &p, int64_t blocks, bool far, bool bf16, bool state8, bool grad32, hipStream_t s) {
+    if (bf16 && far)
+        launch<__bf16, true>(p, blocks, state8, grad32, s);
+    else if (bf16)
+        launch<__bf16, false>(p, blocks, state8, grad32, s);
+    else if (far)
+        launch<_Float16, true>(p, blocks, state8, grad32, s);
     else
-        launch<_Float16>(p, blocks, state8, grad32, s);
+        launch<_Float16, false>(p, blocks, state8, grad32, s);
     return hipGetLastError();
 }
 

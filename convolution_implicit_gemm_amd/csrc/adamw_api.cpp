@@ -21,6 +21,7 @@ struct adamw_plan_s {
     std::vector<Launch> launches;
     std::vector<std::pair<uintptr_t, uintptr_t>> written;  // in order, disjoint
     uint32_t flags;
+    bool far;
 };
 
 namespace {
@@ -99,16 +100,14 @@ conv3d_status build(const adamw_tensor *tensors, int32_t count, uint32_t flags, 
         }
     }
     p->flags = flags;
+    int64_t bytes = 0;
+    for (const Range &r : all) bytes += (int64_t)(r.hi - r.lo);
+    p->far = bytes > kAdamwCached;
+    const int64_t unit = adamw_unit(p->far);
     for (size_t at = 0; at < used.size();) {
         p->launches.push_back({});
         adamw_plan_s::Launch &l = p->launches.back();
         const size_t end = std::min(used.size(), at + kAdamwTensors);
-        int64_t units = 0;
-        for (size_t i = at; i < end; ++i) units += (used[i]->count + kAdamwUnit - 1) / kAdamwUnit;
-        // enough workgroups to fill the card several times over, then several units each
-        int64_t each = units / 4096;
-        each = each < 1 ? 1 : each > 1024 ? 1024 : each;
-        l.prm.units = (int32_t)each;
         int64_t block = 0;
         for (size_t i = at; i < end; ++i) {
             const adamw_tensor &t = *used[i];
@@ -123,10 +122,10 @@ conv3d_status build(const adamw_tensor *tensors, int32_t count, uint32_t flags, 
             d.count = t.count;
             d.decay = t.decay;
             l.prm.first[i - at] = (int32_t)block;
-            block += (t.count + kAdamwUnit * each - 1) / (kAdamwUnit * each);
+            block += (t.count + unit - 1) / unit;
+            if (block >= (int64_t)1 << 22) return api_fail(CONV3D_ERR_UNSUPPORTED, "too many elements in one launch");
         }
         for (size_t i = end - at; i < (size_t)kAdamwTensors; ++i) l.prm.first[i] = INT_MAX;
-        if (block >= (int64_t)1 << 23) return api_fail(CONV3D_ERR_UNSUPPORTED, "too many elements in one launch");
         l.blocks = block;
         at = end;
     }
@@ -192,7 +191,7 @@ conv3d_status adamw_step(adamw_plan_t p, const adamw_hyper *hyper, const void *d
         AdamwParams q = l.prm;
         q.hyper = h;
         q.device_hyper = static_cast<const AdamwHyper *>(device_hyper);
-        const hipError_t e = launch_adamw(q, l.blocks, (p->flags & CONV3D_F_BF16) != 0, (p->flags & CONV3D_F_STATE8) != 0,
+        const hipError_t e = launch_adamw(q, l.blocks, p->far, (p->flags & CONV3D_F_BF16) != 0, (p->flags & CONV3D_F_STATE8) != 0,
                                           (p->flags & CONV3D_F_GRAD32) != 0, static_cast<hipStream_t>(stream));
         if (e != hipSuccess) return launched(e, "adamw_step");
     }

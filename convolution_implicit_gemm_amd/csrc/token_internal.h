@@ -190,7 +190,11 @@ hipError_t launch_attention_grad(const AttnParams &p, AttnTileKind kind_q, AttnT
 // ---- adamw
 constexpr int kAdamwBlock = 128;    // elements that share a scale
 constexpr int kAdamwTensors = 48;   // of a launch: their table travels in the kernel's arguments (4 KiB)
-constexpr int kAdamwUnit = 2048;    // elements that a workgroup takes at a time
+// Elements of a workgroup.  far: the step's tensors are larger than the last-level cache (256 MB)
+// and go past the caches: 201 million weights, 8-bit states, 3.2 GB: 526 us, through
+// them 595 us; 14 million in 61 tensors, 133 MB: 39 us, through them 34 us.
+constexpr int adamw_unit(bool far) { return far ? 2048 : 1024; }
+constexpr int64_t kAdamwCached = (int64_t)256 << 20;
 struct AdamwTensor {
     _Float16 *param;
     float *master;
@@ -211,9 +215,8 @@ struct AdamwParams {
     int32_t first[kAdamwTensors];  // of each tensor's workgroups; INT32_MAX behind the last tensor
     const AdamwHyper *device_hyper;
     AdamwHyper hyper;
-    int32_t units;     // of kAdamwUnit elements to a workgroup
 };
 static_assert(sizeof(AdamwParams) <= 4096, "kernel arguments");
-hipError_t launch_adamw(const AdamwParams &p, int64_t blocks, bool bf16, bool state8, bool grad32, hipStream_t s);
+hipError_t launch_adamw(const AdamwParams &p, int64_t blocks, bool far, bool bf16, bool state8, bool grad32, hipStream_t s);
 
 }  // namespace c3d

@@ -603,7 +603,8 @@ typedef struct adamw_plan_s *adamw_plan_t;
 /*
  * Errors: INVALID_ARG for null pointers, count < 0, neither param nor master, a decay that
  * is negative or not finite, misaligned pointers (16 bytes, scales 1), unknown flags, or
- * tensors that overlap (gradients may overlap each other); UNSUPPORTED for 2^40 elements or more.
+ * tensors that overlap (gradients may overlap each other); UNSUPPORTED for 2^33 elements or more in
+ * 48 tensors that follow each other.
  */
 conv3d_status adamw_plan(const adamw_tensor *tensors, int32_t count, uint32_t flags, adamw_plan_t *out);
 void adamw_plan_destroy(adamw_plan_t p);
