@@ -218,9 +218,6 @@ struct AttnCols {
 };
 #undef C3D_TR
 
-// Row (of a 32 x 32 accumulator) that register i of a lane in half h holds.
-__device__ __forceinline__ constexpr int acc_row(int i, int h) { return (i & 3) + 8 * (i >> 2) + 4 * h; }
-
 // The values that lanes l % 32 and l % 32 + 32 hold, to both.
 struct Halves {
     float low, high;
@@ -234,6 +231,57 @@ struct Halves {
 #endif
     }
 };
+// fp16 has 5 bits of exponent: in the gradients, probabilities (at most 1, 5e-5 in even rows of 20000
+// keys) are 2^15 times as large as operands, so that they stay normal numbers, and what is
+// summed of them is divided by that at the end.  (The forward pass divides by a row's own sum at the
+// end: next to its largest exponential, 1 or more, what the small ones lose does not count.)
+template <typename E>
+constexpr float kLift = std::is_same_v<E, __bf16> ? 0.0f : 15.0f;
+template <typename E>
+constexpr float kDrop = std::is_same_v<E, __bf16> ? 1.0f : 0x1p-15f;
+
+template <int NT>
+__device__ __forceinline__ void acc_scale(f32x16 (&acc)[NT], float f) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[t][e] *= f;
+}
+
+// dS = P (dP - delta) is as large as the gradients make it.  Lifted with P it may not fit fp16: then
+// its column (a query in dq, a key in dk: one per lane, sums and all) is scaled down by a power
+// of two, for good.  bf16 has fp32's exponents and needs none of this.
+template <typename E>
+struct ColumnScale {
+    float f = 1.0f;
+    // the column's 16 new values here and its 16 in the other half of the wave, and its sums so far
+    template <int NT>
+    __device__ __forceinline__ void apply(f32x16 &x, f32x16 (&acc)[NT]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        if constexpr (!std::is_same_v<E, __bf16>) {
+            float top = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
+            if (__builtin_amdgcn_ballot_w64(top * f > 32768.0f)) {
+                const Halves h(top);
+                const float most = fmaxf(h.low, h.high);
+                // the power of two that brings the largest value to 2^13 .. 2^14
+                const int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127;
+                const float to = __builtin_bit_cast(float, (uint32_t)(13 - e + 127) << 23);
+                const float now = most * f > 32768.0f ? to : f, by = now / f;
+                f = now;
+                acc_scale<NT>(acc, by);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] *= f;
+        }
+#endif
+    }
+};
+
+// Row (of a 32 x 32 accumulator) that register i of a lane in half h holds.
+__device__ __forceinline__ constexpr int acc_row(int i, int h) { return (i & 3) + 8 * (i >> 2) + 4 * h; }
+
 __device__ __forceinline__ float both_max(float v) {
     const Halves x(v);
     return fmaxf(x.low, x.high);

@@ -93,8 +93,9 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
     AttnCols<DP> fc;
     fr.init(lane);
     fc.init(lane);
-    const float c = p.scale * kAttnLog2e, lse2 = lse == -__builtin_inff() ? 0.0f : lse * kAttnLog2e;
+    const float c = p.scale * kAttnLog2e, lse2 = (lse == -__builtin_inff() ? 0.0f : lse * kAttnLog2e) - kLift<E>;
     f32x16 acc[NT] = {};
+    ColumnScale<E> scale;
     int buf = 0;
     for (int at = lo; at < hi; at += STEP) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -135,6 +136,7 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], c, -lse2)) * y[e];
+            scale.template apply<NT>(x, acc);
             static_for<2>([&](auto step) {
                 constexpr int S = decltype(step)::value;
                 half8_t f[NT];
@@ -148,6 +150,8 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
     if constexpr (KG > 1) {
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the buffers are free
         float *sums = reinterpret_cast<float *>(smem);
+        if constexpr (!std::is_same_v<E, __bf16>) acc_scale<NT>(acc, 1.0f / scale.f);
+        scale.f = 1.0f;
         if (kg > 0) acc_put<NT>(sums + ((kg - 1) * RG + rg) * NT * 1024, acc, lane);
         __syncthreads();
         if (kg > 0) return;
@@ -161,7 +165,7 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
     }
     _Float16 *out = p.dq + b * p.qs[0] + i * p.qs[1] + h * p.qs[2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, acc[t], p.scale, d - 32 * t, lane, true);
+    for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, acc[t], p.scale * kDrop<E> / scale.f, d - 32 * t, lane, true);
 }
 
 // ---- dk, dv: tiles of 32 KW keys and BM QG query tokens, 8 waves: wave (kw, qg) holds keys
@@ -256,6 +260,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
     fc.init(lane);
     const float c = p.scale * kAttnLog2e;
     f32x16 ak[NT] = {}, av[NT] = {};
+    ColumnScale<E> scale;
     int buf = 0;
     for (int n = first; n < total; ++n) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -305,16 +310,17 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                x[e] = __builtin_amdgcn_exp2f(x[e] * c);
+                x[e] = __builtin_amdgcn_exp2f(kLift<E> == 0.0f ? x[e] * c : fmaf(x[e], c, kLift<E>));
                 y[e] *= x[e];
             }
+            const half8_t w[2] = {pack8<E>(x, 0), pack8<E>(x, 8)};
+            scale.template apply<NT>(y, ak);
             static_for<2>([&](auto half) {
                 constexpr int S = decltype(half)::value;
                 half8_t f[NT];
                 fc.template read<2 * T + S>(gs, f);
-                const half8_t w = pack8<E>(x, S * 8);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) av[t] = mfma_32x32x16<E>(f[t], w, av[t]);
+                for (int t = 0; t < NT; ++t) av[t] = mfma_32x32x16<E>(f[t], w[S], av[t]);
                 fc.template read<2 * T + S>(qs, f);
                 const half8_t u = pack8<E>(y, S * 8);
 #pragma unroll
@@ -324,6 +330,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
     }
     // without a step, k is still on its way into LDS
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if constexpr (!std::is_same_v<E, __bf16>) acc_scale<NT>(ak, 1.0f / scale.f);
     if constexpr (QG > 1) {
         float *sums = reinterpret_cast<float *>(smem);
         static_for<2>([&](auto w) {
@@ -360,12 +367,12 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
     if (p.dk) {
         _Float16 *out = p.dk + b * p.ks[0] + j * p.ks[1] + hk * p.ks[2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, ak[t], p.scale, d - 32 * t, lane, true);
+        for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, ak[t], p.scale * kDrop<E>, d - 32 * t, lane, true);
     }
     if (p.dv) {
         _Float16 *out = p.dv + b * p.vs[0] + j * p.vs[1] + hk * p.vs[2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, av[t], 1.0f, d - 32 * t, lane, true);
+        for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, av[t], kDrop<E>, d - 32 * t, lane, true);
     }
 }
 
@@ -399,8 +406,8 @@ __global__ __launch_bounds__(256) void attention_dkv_join_kernel(AttnParams p, i
     half4_t ok, ov;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-        ok[m] = from_f32<E>(ak[m] * p.scale);
-        ov[m] = from_f32<E>(av[m]);
+        ok[m] = from_f32<E>(ak[m] * (p.scale * kDrop<E>));
+        ov[m] = from_f32<E>(av[m] * kDrop<E>);
     }
     if (p.dk) *reinterpret_cast<half4_t *>(p.dk + b * p.ks[0] + j * p.ks[1] + hk * p.ks[2] + e) = ok;
     if (p.dv) *reinterpret_cast<half4_t *>(p.dv + b * p.vs[0] + j * p.vs[1] + hk * p.vs[2] + e) = ov;

@@ -1,15 +1,13 @@
 """The token path of a video transformer over the VAE decoder's latent grid.
 
 One pre-norm transformer block runs on the voxels of a latent video (one token
-per voxel), forward and backward, through the library's token operators, and
-the decoder's first causal convolution takes the result:
+per voxel), forward and backward, through the library's token operators, an
+AdamW step updates its weights, and the decoder's first causal convolution takes the result:
 
     layernorm -> q, k, v projection -> rope3d -> attention -> out projection + x
     layernorm -> up projection + GELU -> down projection + x -> conv3d
 
-Attention is not one of the library's operators: the block takes it as a
-function (forward and backward); the one below attends within each frame, in
-plain fp32 torch.  Run it on a GPU:
+Each frame attends to itself.  Run it on a GPU:
 
     python examples/latent_block.py [--frames 5] [--size 16] [--channels 256] [--heads 4]
 
@@ -68,38 +66,34 @@ class LatentBlock:
         self.rope = c3d.rope3d_plan(c3d.make_rope3d_desc(
             1, t, h, w, heads, heads, self.d, (self.d - 2 * rest, rest, rest), flags=c3d.CONV3D_F_BF16,
             q_stride=stride, k_stride=stride, q_out_stride=stride, k_out_stride=stride))
+        # the frames are told apart by a mask over all tokens, one frame wide
+        self.attention = c3d.attention_plan(c3d.make_attention_desc(
+            1, m, m, heads, heads, self.d, frame=h * w, window=1, flags=c3d.CONV3D_F_BF16, q_stride=stride,
+            k_stride=stride, v_stride=stride))
         need = max([p.workspace_bytes for p in self.plans.values()] +
                    [c3d.linear_backward_workspace(p) for p in self.plans.values()] +
-                   [c3d.layernorm_backward_workspace(m, c)])
+                   [self.attention.workspace_bytes, c3d.attention_backward_workspace(self.attention),
+                    c3d.layernorm_backward_workspace(m, c)])
         self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
 
     def rows(self, n, dtype=torch.bfloat16):
         return torch.empty((self.m, n), dtype=dtype, device="cuda")
 
-    def _qk(self, qkv):
-        v = qkv.view(1, self.m, 3 * self.heads, self.d)
-        return v[:, :, :self.heads], v[:, :, self.heads:2 * self.heads]
-
-    def _attend(self, qkv):
-        t, h, w = self.grid
-        f = qkv.view(t, h * w, 3, self.heads, self.d).float().requires_grad_(True)
-        with torch.enable_grad():
-            o = frame_attention(f[:, :, 0], f[:, :, 1], f[:, :, 2])
-        return f, o
+    def _qkv(self, qkv):
+        return qkv.view(1, self.m, 3 * self.heads, self.d).split(self.heads, 2)
 
     def forward(self, x):
         """y, and what the backward pass needs."""
         m, c, p, ws = self.m, self.c, self.p, self.ws
         s = {"x": x, "n1": self.rows(c), "st1": self.rows(2, torch.float32), "qkv": self.rows(3 * c),
-             "x1": self.rows(c), "n2": self.rows(c), "st2": self.rows(2, torch.float32), "up": self.rows(4 * c),
+             "o": self.rows(c), "lse": torch.empty((1, self.heads, m), device="cuda"), "x1": self.rows(c), "n2": self.rows(c), "st2": self.rows(2, torch.float32), "up": self.rows(4 * c),
              "z": self.rows(4 * c)}
         y = self.rows(c)
         c3d.layernorm_bf16(x, p["g1"], p["b1"], s["n1"], s["st1"], m, c, EPS)
         c3d.linear_forward(self.plans["qkv"], s["n1"], p["qkv"], p["qkv_b"], None, s["qkv"], None, ws)
-        q, k = self._qk(s["qkv"])
+        q, k, v = self._qkv(s["qkv"])
         c3d.rope3d_forward(self.rope, q, k, q, k)
-        s["attn"] = self._attend(s["qkv"])
-        s["o"] = s["attn"][1].detach().reshape(m, c).to(torch.bfloat16)
+        c3d.attention_forward(self.attention, q, k, v, s["o"], s["lse"], workspace=ws)
         c3d.linear_forward(self.plans["out"], s["o"], p["out"], p["out_b"], x, s["x1"], None, ws)
         c3d.layernorm_bf16(s["x1"], p["g2"], p["b2"], s["n2"], s["st2"], m, c, EPS)
         c3d.linear_forward(self.plans["up"], s["n2"], p["up"], p["up_b"], None, s["up"], s["z"], ws)
@@ -117,14 +111,27 @@ class LatentBlock:
         c3d.layernorm_backward_bf16(d_n, s["x1"], p["g2"], s["st2"], dy, d_x1, g["g2"], g["b2"], m, c, ws)
         d_o, d_x = self.rows(c), self.rows(c)
         c3d.linear_backward(self.plans["out"], d_x1, s["o"], p["out"], None, d_o, g["out"], g["out_b"], ws)
-        f, o = s["attn"]
-        d_f, = torch.autograd.grad(o, f, d_o.view(o.shape).float())
-        d_qkv = d_f.reshape(m, 3 * c).to(torch.bfloat16)
-        dq, dk = self._qk(d_qkv)
+        d_qkv = self.rows(3 * c)
+        dq, dk, dv = self._qkv(d_qkv)
+        c3d.attention_backward(self.attention, d_o, *self._qkv(s["qkv"]), s["o"], s["lse"], dq, dk, dv, workspace=ws)
         c3d.rope3d_backward(self.rope, dq, dk, dq, dk)
         c3d.linear_backward(self.plans["qkv"], d_qkv, s["n1"], p["qkv"], None, d_n, g["qkv"], g["qkv_b"], ws)
         c3d.layernorm_backward_bf16(d_n, s["x"], p["g1"], s["st1"], d_x1, d_x, g["g1"], g["b1"], m, c, ws)
         return d_x, g
+
+    def optimizer(self, grads):
+        """What steps over the block's weights need: fp32 copies of them and 8-bit states."""
+        names = list(self.p)
+        blocks = [-(-self.p[n].numel() // c3d.ADAMW_BLOCK) for n in names]
+
+        def zeros(sizes):
+            return [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in sizes]
+
+        sizes = [self.p[n].numel() for n in names]
+        master = [self.p[n].float() for n in names]
+        return master, c3d.adamw_list([self.p[n] for n in names], [grads[n] for n in names], zeros(sizes), zeros(sizes),
+                                      master=master, m_scale=zeros(blocks), v_scale=zeros(blocks),
+                                      decay=[float(self.p[n].dim() > 1) for n in names])
 
 
 def decode_first_conv(tokens, grid, seed=1):
@@ -188,7 +195,18 @@ def run(frames=5, size=16, channels=256, heads=4):
     def err(a, b):
         return float((a.double() - b).norm() / b.norm())
 
-    return dict({"y": err(y, ry), "dx": err(dx, rdx)}, **{n: err(grads[n], rg[n]) for n in grads})
+    errors = dict({"y": err(y, ry), "dx": err(dx, rdx)}, **{n: err(grads[n], rg[n]) for n in grads})
+    # the first step on these gradients, against the formula: with new states m / (1 - beta1) = g, v / (1 - beta2) = g^2
+    before = {n: v.double() for n, v in block.p.items()}
+    master, tensors = block.optimizer(grads)
+    hyper = c3d.make_adamw_hyper(1e-3, weight_decay=0.1)
+    c3d.adamw_step(tensors, hyper)
+    torch.cuda.synchronize()
+    for w, (n, old) in zip(master, before.items()):
+        gr = grads[n].double()
+        want = old - hyper.lr * (hyper.weight_decay * (old.dim() > 1) * old + gr / (gr.abs() + hyper.eps))
+        errors["step " + n] = err(w, want)
+    return errors
 
 
 if __name__ == "__main__":

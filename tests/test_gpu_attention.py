@@ -218,3 +218,52 @@ def test_forward_and_gradients(case):
     c.check_forward()
     outs = c.backward()
     c.check_backward(outs)
+
+
+def l2(a, b):
+    """Relative, beyond what the result's own rounding below fp16's normal numbers allows: half of 2^-24 for each
+    element (dk of the first case below is 1e-5, where fp16's steps are 2^-24 = 6e-8)."""
+    return max(0.0, float((a.double() - b).norm()) - 2.0 ** -25 * a.numel() ** 0.5) / float(b.norm())
+
+
+@pytest.mark.parametrize("tile", ["attention_64x128", "attention_128x128", "attention_256x64"])
+@pytest.mark.parametrize("dout,vs,ks", [(0.05, 0.05, 8.0), (200.0, 4.0, 1.0), (0.05, 1.0, 1.0)])
+def test_fp16_gradients_of_any_size_keep_their_digits(dout, vs, ks, tile, monkeypatch):
+    # dS between 1e-7 (below fp16's normal numbers) and 1e4 (their products' scales overflow them): P and dS round
+    # once each, and the result once; three roundings of at most 2^-11
+    monkeypatch.setenv("CONV3D_ATTENTION_TILE", tile)
+    c = Case(tq=4096, tk=4096, hq=1, hk=1, d=64, dtype="fp16", seed=5)
+    g = gen(77)
+    c.k, c.v, c.do = (normal(g, x.shape, c.dt, s) for x, s in ((c.k, ks), (c.v, vs), (c.do, dout)))
+    c.q = normal(g, c.q.shape, c.dt, 1.0 / ks)
+    c.forward()
+    dq, dk, dv = c.backward()
+    q, k, v, do, m, p, lse, err = c.one(0, 0)
+    dp = do @ v.t()
+    ds = p * (dp - (p * dp).sum(1, keepdim=True))
+    want = c.s * (ds @ k), c.s * (ds.t() @ q), p.t() @ do
+    for name, got, ref in zip(("dq", "dk", "dv"), (dq, dk, dv), want):
+        ref = torch.where(ref.abs() > 65504.0, torch.full_like(ref, math.inf) * ref.sign(), ref)
+        fits = torch.isfinite(ref)
+        assert l2(got[0, :, 0][fits], ref[fits]) < 3 * 2.0 ** -11, name
+
+
+def test_fp16_gradients_whose_size_grows_on_the_way():
+    # the last keys' and queries' dS are 2^20 times the first ones': sums so far are scaled down, nothing overflows
+    c = Case(tq=700, tk=900, hq=2, hk=1, d=64, dtype="fp16", seed=6)
+    ramp = torch.exp2(torch.arange(900, device="cuda:0") / 900 * 10).half()
+    c.v = (c.v * ramp[None, :, None, None]).contiguous()
+    c.do = (c.do * 0.1 * ramp[None, :700, None, None]).contiguous()
+    c.forward()
+    dq, dk, dv = c.backward()
+    sums = [0.0] * 2
+    for h in range(2):
+        q, k, v, do, m, p, lse, err = c.one(0, h)
+        dp = do @ v.t()
+        ds = p * (dp - (p * dp).sum(1, keepdim=True))
+        # row by row: each has a scale of its own
+        ref = c.s * (ds @ k)
+        assert float(((dq[0, :, h].double() - ref).norm(dim=1) / ref.norm(dim=1)).max()) < 2.0 ** -7
+        sums[0] = sums[0] + c.s * (ds.t() @ q)
+        sums[1] = sums[1] + p.t() @ do
+    assert l2(dk[0, :, 0], sums[0]) < 4 * 2.0 ** -11 and l2(dv[0, :, 0], sums[1]) < 3 * 2.0 ** -11
