@@ -29,6 +29,13 @@ __device__ __forceinline__ float dot8(half8_t a, half8_t b) {
 
 // ---- dq: tiles of 32 RG rows and BN KG keys as in the forward pass.  S^T = K Q^T and dP^T = V dout^T
 // hold one query per lane; dS^T is, as it stands, the operand of dq^T = K^T dS^T.
+//
+// delta_i = sum_j P_ij dP_ij is dout_i . o_i, but o is rounded, and where a query sees few keys
+// that rounding is as large as those of dS and dq together (one key: dS is 0, and would be
+// nothing but it).  Tiles whose first query sees fewer than kFewKeys keys therefore take the
+// sum itself, in a pass over the keys of its own, as long as there are at most kFewSpan of them: for 64
+// tokens, causal, the error of dq falls from 1.72 to 1.43 times that of the plain form.
+constexpr int kFewKeys = 160, kFewSpan = 512;
 template <typename E, int DP, int RG, int KG, int BN>
 __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
     constexpr int NT = DP / 32, KK = DP / 16, XN = BN / 32, STEP = KG * BN, TILE = STEP * DP * 2;
@@ -44,12 +51,16 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
     const AttnSample s = attn_sample(p, b);
     const int r0 = tile * RG * 32, d = p.d, last = s.queries - 1;
     int lo = 0, hi = 0;
-    if (p.dq) {
+    bool few = false;
+    {
         const int t_first = r0 / p.group, t_last = (r0 + RG * 32 - 1) / p.group;
         if (t_first <= last) {
-            lo = attn_range(p, s, t_first).lo & ~(BN - 1);
+            const AttnRange first = attn_range(p, s, t_first);
+            lo = first.lo & ~(BN - 1);
             hi = attn_range(p, s, t_last < last ? t_last : last).hi;
+            few = first.hi - first.lo < kFewKeys && hi - lo <= kFewSpan;
         }
+        if (!p.dq && !few) hi = lo;  // the rows' sums alone are asked for
     }
     const AttnTile<DP, STEP, 8> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane),
         tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
@@ -78,14 +89,8 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
             delta += dot8<E>(go[kk], o);
         }
         delta = both_sum(delta);
-        const int64_t row = ((int64_t)b * p.hq + h) * p.tq + i;
-        if (alive) lse = p.lse[row];
-        if (r < p.rows && lane < 32 && kg == 0) {
-            p.nlse[row] = start_of_scores(lse, p.scale);
-            p.ndelta[row] = -delta;
-        }
+        if (alive) lse = p.lse[((int64_t)b * p.hq + h) * p.tq + i];
     }
-    if (!p.dq) return;  // only the rows' sums were asked for
     const AttnRange seen = last < 0 ? AttnRange{0, 0} : attn_range(p, s, i < last ? i : last);
     const int wave_lo = __builtin_amdgcn_readfirstlane(seen.lo), wave_hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
     const int wave_lo_all = __builtin_amdgcn_readlane(seen.lo, 31), wave_hi = __builtin_amdgcn_readlane(seen.hi, 31);
@@ -96,57 +101,94 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
     const float c = p.scale * kAttnLog2e, lse2 = (lse == -__builtin_inff() ? 0.0f : lse * kAttnLog2e) - kLift<E>;
     f32x16 acc[NT] = {};
     ColumnScale<E> scale;
+    float sum = 0.0f;  // of P dP, this lane's keys
     int buf = 0;
-    for (int at = lo; at < hi; at += STEP) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const char *ks = smem + buf * 2 * TILE + kg * BN * DP * 2;
-        buf ^= 1;
-        auto next = [&]() {
-            if (at + STEP < hi) {
-                char *to = smem + buf * 2 * TILE;
-                tk.load(to, at + STEP, wave);
-                tv.load(to + TILE, at + STEP, wave);
-            }
-        };
-        const int j0 = at + kg * BN;
-        if (j0 + BN <= wave_lo || j0 >= wave_hi) {
-            next();
-            continue;
-        }
-        const bool edge = j0 < wave_lo_all || j0 + BN > wave_hi_all;
-        const uint32_t kr = lds_address(ks) + fr.off;
-        static_for<XN>([&](auto sub) {
-            constexpr int T = decltype(sub)::value;
-            f32x16 x = {}, y;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = -delta;
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                x = mfma_32x32x16<E>(fr.read(kr, 32 * T, kk), q[kk], x);
-                y = mfma_32x32x16<E>(fr.read(kr, STEP + 32 * T, kk), go[kk], y);
-            }
-            if constexpr (T == 0) next();  // behind the products, which it then does not hold up
-            if (edge) {
-                const int from = seen.lo - j0, to = seen.hi - j0;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int j = 32 * T + acc_row(e, lane >> 5);
-                    x[e] = j >= from && j < to ? x[e] : -__builtin_inff();
+    // one pass over the keys: the sum of P dP (SUM), or dq; the first step's tiles are on their way
+    auto pass = [&](auto which) {
+        constexpr bool SUM = decltype(which)::value;
+        for (int at = lo; at < hi; at += STEP) {
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            const char *ks = smem + buf * 2 * TILE + kg * BN * DP * 2;
+            buf ^= 1;
+            auto next = [&]() {
+                if (at + STEP < hi) {
+                    char *to = smem + buf * 2 * TILE;
+                    tk.load(to, at + STEP, wave);
+                    tv.load(to + TILE, at + STEP, wave);
                 }
+            };
+            const int j0 = at + kg * BN;
+            if (j0 + BN <= wave_lo || j0 >= wave_hi) {
+                next();
+                continue;
             }
+            const bool edge = j0 < wave_lo_all || j0 + BN > wave_hi_all;
+            const uint32_t kr = lds_address(ks) + fr.off;
+            static_for<XN>([&](auto sub) {
+                constexpr int T = decltype(sub)::value;
+                f32x16 x = {}, y;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], c, -lse2)) * y[e];
-            scale.template apply<NT>(x, acc);
-            static_for<2>([&](auto step) {
-                constexpr int S = decltype(step)::value;
-                half8_t f[NT];
-                fc.template read<2 * T + S>(ks, f);
-                const half8_t w = pack8<E>(x, S * 8);
+                for (int e = 0; e < 16; ++e) y[e] = SUM ? 0.0f : -delta;
 #pragma unroll
-                for (int t = 0; t < NT; ++t) acc[t] = mfma_32x32x16<E>(f[t], w, acc[t]);
+                for (int kk = 0; kk < KK; ++kk) {
+                    x = mfma_32x32x16<E>(fr.read(kr, 32 * T, kk), q[kk], x);
+                    y = mfma_32x32x16<E>(fr.read(kr, STEP + 32 * T, kk), go[kk], y);
+                }
+                if constexpr (T == 0) next();  // behind the products, which it then does not hold up
+                if (edge) {
+                    const int from = seen.lo - j0, to = seen.hi - j0;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int j = 32 * T + acc_row(e, lane >> 5);
+                        x[e] = j >= from && j < to ? x[e] : -__builtin_inff();
+                    }
+                }
+                if constexpr (SUM) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        sum = fmaf(__builtin_amdgcn_exp2f(fmaf(x[e], c, -lse2 - kLift<E>)), y[e], sum);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], c, -lse2)) * y[e];
+                    scale.template apply<NT>(x, acc);
+                    static_for<2>([&](auto step) {
+                        constexpr int S = decltype(step)::value;
+                        half8_t f[NT];
+                        fc.template read<2 * T + S>(ks, f);
+                        const half8_t w = pack8<E>(x, S * 8);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) acc[t] = mfma_32x32x16<E>(f[t], w, acc[t]);
+                    });
+                }
             });
-        });
+        }
+    };
+    if (few) {
+        pass(std::true_type{});
+        sum = both_sum(sum);
+        if constexpr (KG > 1) {
+            __shared__ float parts[512];
+            parts[threadIdx.x] = sum;
+            __syncthreads();
+            sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KG; ++k) sum += parts[(k * RG + rg) * 64 + lane];
+        }
+        delta = sum;
+        buf = 0;
+        if (p.dq && hi - lo > STEP) {  // a single step is still there
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the buffers are free
+            tk.load(smem, lo, wave);
+            tv.load(smem + TILE, lo, wave);
+        }
     }
+    if (r < p.rows && lane < 32 && kg == 0) {
+        const int64_t row = ((int64_t)b * p.hq + h) * p.tq + i;
+        p.nlse[row] = start_of_scores(lse, p.scale);
+        p.ndelta[row] = alive ? -delta : 0.0f;
+    }
+    if (!p.dq) return;
+    pass(std::false_type{});
     if constexpr (KG > 1) {
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the buffers are free
         float *sums = reinterpret_cast<float *>(smem);
