@@ -28,8 +28,6 @@ __device__ __forceinline__ float max32(float v) {
     return v;
 }
 
-__device__ __forceinline__ float power_of_two(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
-
 // 4 codes -> values times `unit`
 __device__ __forceinline__ void decode4(uint32_t c, float unit, float (&x)[4]) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -54,10 +52,37 @@ __device__ __forceinline__ int block_power(const float (&x)[4]) {
     const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);  // 1.75 * 2^8 = 448
     return e < -126 ? -126 : e;
 }
-template <bool ROOT>
-__device__ __forceinline__ uint32_t encode4(const float (&x)[4], int e) {
+// 2^-e of N blocks to a half wave, whose lanes all hold them: the first wave of the workgroup works
+// out those of all.  By powf, as a program that scales its states elementwise (ldexp of a tensor
+// is a product with its powf) takes it: powf is half an ulp off for a sixth of the powers, which decides
+// where values between two codes go that lie exactly on the border, and with gradients of
+// 8 bits and betas of few digits one in 250 does.  Codes are then that program's to the bit.
+template <int N>
+__device__ __forceinline__ void inverse_powers(const int (&e)[N], float (&inv)[N]) {
+    static_assert(8 * N <= 64, "one wave for all");
+    __shared__ int powers[8 * N];
+    __shared__ float inverses[8 * N];
+    const auto meet = [] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+    const int half = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) powers[half * N + k] = e[k];
+    }
+    meet();
+    if (threadIdx.x < 8 * N) {
+        float two = 2.0f;
 #if defined(__HIP_DEVICE_COMPILE__)
-    const float inv = power_of_two(-e);
+        asm("" : "+v"(two));
+#endif
+        inverses[threadIdx.x] = powf(two, (float)-powers[threadIdx.x]);
+    }
+    meet();
+#pragma unroll
+    for (int k = 0; k < N; ++k) inv[k] = inverses[half * N + k];
+}
+template <bool ROOT>
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], float inv) {
+#if defined(__HIP_DEVICE_COMPILE__)
     float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -153,18 +178,23 @@ __device__ __forceinline__ void store_codes(uint8_t *p, int left, uint32_t c) {
         if (i < left) p[i] = (uint8_t)(c >> (8 * i));
 }
 
-// sqrt within an ulp, of denormal numbers too.
-__device__ __forceinline__ float root_of(float v) {
-    const bool tiny = v < 0x1p-96f;
-    const float s = __builtin_amdgcn_sqrtf(tiny ? v * 0x1p+64f : v);
-    return tiny ? s * 0x1p-32f : s;
+// m and v as the formulas read, each product and sum rounded by itself, and v's root to the nearest: a
+// program that evaluates them in fp32 gets the same bits, so that 8-bit codes next to a border between
+// two of them do not differ between the two (contracted, one in 10^6 did, and their weights by
+// up to a step's size one step later).
+__device__ __forceinline__ void new_states(const AdamwHyper &h, float x, float &m, float &v, float &root) {
+#pragma clang fp contract(off)
+    m = m * h.beta1 + x * h.rest1;
+    v = v * h.beta2 + (x * x) * h.rest2;
+    root = sqrtf(v);
 }
 
 // A lane takes 4 adjacent elements at a time (one access of up to 16 bytes to each array, whole
 // lines of it to a wave), half a wave a block of 128, whose scale it finds by itself; a
 // workgroup adamw_unit() adjacent elements of one tensor, all of them on their way at once, so that
-// workgroups that run together read and write adjacent memory (201 million weights, 8-bit
-// states: 595 us; with 24 times the elements to a workgroup, one after the other, 706 us).
+// workgroups that run together read and write adjacent memory: 201 million weights, 8-bit
+// states 548 us, 5.9 TB/s, bound by memory (with 24 times the elements to a workgroup, one after the
+// other, a fifth more).
 template <typename E, bool STATE8, bool GRAD32, bool FAR>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamwParams p) {
     constexpr int PARTS = adamw_unit(FAR) / 1024;
@@ -213,25 +243,36 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float x = g[k][i] * h.grad_scale;
-            m[k][i] = fmaf(m[k][i], h.beta1, x * h.rest1);
-            v[k][i] = fmaf(v[k][i], h.beta2, x * x * h.rest2);
-            const float root = root_of(v[k][i]);
+            float root;
+            new_states(h, x, m[k][i], v[k][i], root);
             w[k][i] = fmaf(w[k][i], keep, -h.lr1 * (m[k][i] / fmaf(root, h.root2, h.eps)));
             if (STATE8) v[k][i] = root;
         }
         if (t.master) store_f32<FAR>(t.master + base, left[k], w[k]);
         if (t.param) store_16<E, FAR>(t.param + base, left[k], w[k]);
-        if constexpr (STATE8) {
-            const int pm = block_power(m[k]), pv = block_power(v[k]);
-            store_codes<FAR>(static_cast<uint8_t *>(t.m) + base, left[k], encode4<false>(m[k], pm));
-            store_codes<FAR>(static_cast<uint8_t *>(t.v) + base, left[k], encode4<true>(v[k], pv));
-            if (left[k] && (threadIdx.x & 31) == 0) {
-                t.m_scale[base / kAdamwBlock] = (uint8_t)(pm + 127);
-                t.v_scale[base / kAdamwBlock] = (uint8_t)(pv + 127);
-            }
-        } else {
+        if constexpr (!STATE8) {
             store_f32<FAR>(static_cast<float *>(t.m) + base, left[k], m[k]);
             store_f32<FAR>(static_cast<float *>(t.v) + base, left[k], v[k]);
+        }
+    }
+    if constexpr (STATE8) {
+        int e[2 * PARTS];
+        float inv[2 * PARTS];
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            e[2 * k] = block_power(m[k]);
+            e[2 * k + 1] = block_power(v[k]);
+        }
+        inverse_powers<2 * PARTS>(e, inv);
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            const int64_t base = unit + k * 1024 + threadIdx.x * 4;
+            store_codes<FAR>(static_cast<uint8_t *>(t.m) + base, left[k], encode4<false>(m[k], inv[2 * k]));
+            store_codes<FAR>(static_cast<uint8_t *>(t.v) + base, left[k], encode4<true>(v[k], inv[2 * k + 1]));
+            if (left[k] && (threadIdx.x & 31) == 0) {
+                t.m_scale[base / kAdamwBlock] = (uint8_t)(e[2 * k] + 127);
+                t.v_scale[base / kAdamwBlock] = (uint8_t)(e[2 * k + 1] + 127);
+            }
         }
     }
 }

@@ -525,15 +525,18 @@ typedef struct {
 /*
  * Validate *d and choose the kernels.  Host only.  *workspace_bytes: device workspace
  * of attention_forward (0 if none).
- * Errors: INVALID_ARG for null pointers, negative n, tq, tk, frame or window, heads_q
- * not a positive multiple of heads_k, head_dim < 1, a scale that is negative or not
+ * Errors: INVALID_ARG for null pointers, negative n, tq, tk, frame or window, a window
+ * without a frame, heads_q not a positive multiple of heads_k, head_dim < 1, a scale that is negative or not
  * finite, unknown flags, or strides that are negative, not a multiple of 8, or
  * (between tokens, with more than one) shorter than a head; UNSUPPORTED for head_dim
  * not a multiple of 8 or above 128, more than 16384 heads, 2^30 tokens or more (of a sample, times
  * heads_q / heads_k for queries), token strides above 2^20, others of 2^40 or more, a tensor of 2^48
  * elements or more from its first to its last, or more than 2^31 threads' work.
  * Few rows against many keys split the keys over workgroups, which leave fp32
- * partials in the workspace that a second small kernel joins in a fixed order.
+ * partials in the workspace that a second small kernel joins in a fixed order; few
+ * keys against many queries split the queries in the backward pass the same way.
+ * The environment variables CONV3D_ATTENTION_TILE=<name> and CONV3D_ATTENTION_SPLITS=<n>
+ * force a kernel (where it can run the call) and a number of pieces.
  */
 conv3d_status attention_plan(const attention_desc *d, attention_plan_t *out, size_t *workspace_bytes);
 conv3d_status attention_plan_query(attention_plan_t p, attention_plan_info *info);
@@ -579,8 +582,8 @@ conv3d_status attention_backward(attention_plan_t p, const void *dout, const voi
  *          block of 128 elements (the last one may be shorter): uint8 [(count + 127) / 128]
  * In 8 bits a block's byte s and codes c stand for m = c 2^(s - 127) and sqrt(v) =
  * c 2^(s - 127), s - 127 the least power (from -126 on) at which the block's largest value is
- * 448 or less; values are rounded to nearest, and a positive sqrt(v) never to 0, so that no step divides
- * by a state that vanished.  Zero bytes are the states before the first step.  The step itself
+ * 448 or less; the product with powf(2, 127 - s) is rounded to nearest, and a positive
+ * sqrt(v) never to 0, so that no step divides by a state that vanished.  Zero bytes are the states before the first step.  The step itself
  * uses the states before they are rounded.  A value that is not finite becomes a NaN code and
  * does not count for its block's scale.
  */

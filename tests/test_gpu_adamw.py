@@ -219,3 +219,32 @@ def test_hyperparameters_on_the_device_and_replays():
         torch.cuda.synchronize()
         for x, y in zip(a.params + a.master + a.m + a.v, b.params + b.master + b.m + b.v):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("state8", [False, True])
+def test_states_have_the_bits_of_the_formula_in_fp32(state8):
+    # products, sums and the root rounded one by one, as elementwise operations in fp32 round them
+    t = Tensors([300000], state8=state8, grad32=True, seed=8)
+    h = c3d.make_adamw_hyper(1e-3, 0.9, 0.98, 1e-8, 0.1, 5, grad_scale=0.3)
+    x = t.grads[0] * h.grad_scale
+    if state8:
+        m, root = decode(t.m[0], t.ms[0]).float(), decode(t.v[0], t.vs[0]).float()
+        v = root * root
+    else:
+        m, v = t.m[0].clone(), t.v[0].clone()
+    m = m * h.beta1 + x * (1.0 - h.beta1)
+    v = v * h.beta2 + x * x * (1.0 - h.beta2)
+    c3d.adamw_step(t.list(), h)
+    if not state8:
+        assert torch.equal(t.m[0], m) and torch.equal(t.v[0], v)
+        return
+    for codes, scale, want in ((t.m[0], t.ms[0], m), (t.v[0], t.vs[0], torch.sqrt(v))):
+        pad = torch.nn.functional.pad(want, (0, -len(want) % B)).view(-1, B)
+        f, e = torch.frexp(pad.abs().amax(1))
+        e = (e - 9 + (f > 0.875).int()).clamp(min=-126)  # 448 = 0.875 * 2^9
+        assert torch.equal(scale.int(), e + 127)
+        y = torch.ldexp(pad, -e[:, None]).flatten()[:len(want)]
+        code = y.to(torch.float8_e4m3fn).float()
+        if want is not m:
+            code = torch.where((code == 0) & (y > 0), torch.full_like(code, 2.0 ** -9), code)
+        assert torch.equal(codes.view(torch.float8_e4m3fn).float(), code)
