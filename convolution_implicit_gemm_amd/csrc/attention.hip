@@ -128,7 +128,12 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_tile_kernel(A
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
             for (int t = 0; t < XN; ++t) x[t] = mfma_32x32x16<E>(fk.read(kr, 32 * t, kk), q[kk], x[t]);
-        next();  // behind the products, which it then does not hold up
+        // behind the products, which these then do not hold up: the next step's loads, and the first of v's
+        // fragments, whose wait the products cover
+        half8_t ahead[2][NT];
+        fv.template read<0>(vs, ahead[0]);
+        fv.template read<1>(vs, ahead[1]);
+        next();
         if (j0 < wave_lo_all || j0 + BN > wave_hi_all) {
             const int from = seen.lo - j0, to = seen.hi - j0;
 #pragma unroll
@@ -164,10 +169,10 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_tile_kernel(A
         static_for<2 * XN>([&](auto step) {
             constexpr int S = decltype(step)::value;
             half8_t f[NT];
-            fv.template read<S>(vs, f);
+            if constexpr (S > 1) fv.template read<S>(vs, f);
             const half8_t w = pack8<E>(x[S / 2], (S & 1) * 8);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) acc[t] = mfma_32x32x16<E>(f[t], w, acc[t]);
+            for (int t = 0; t < NT; ++t) acc[t] = mfma_32x32x16<E>(S > 1 ? f[t] : ahead[S & 1][t], w, acc[t]);
         });
     }
     if constexpr (KG > 1) {
