@@ -17,7 +17,8 @@ struct attention_plan_s {
     attention_desc d;
     int64_t qs[3], ks[3], vs[3], os[3];
     bool folds_q, folds_k, folds_v, folds_o;  // strides that put different elements on one address
-    AttnTileKind kind, kind_q, kind_kv;
+    AttnTileKind kind;
+    AttnGradKinds grad;
     int64_t grid;
     size_t off_ml, fwd_bytes, off_delta, off_dk, off_dv, back_bytes;
     AttnParams prm;  // pointers filled per call
@@ -142,6 +143,30 @@ Choice choose(Pass pass, const Problem &w, bool splits) {
     return best;
 }
 
+// dq beside dk and dv in one launch of tiles of one kind, after a launch for the rows' numbers.  That is
+// worth it where either alone leaves CUs idle: 1024 tokens, 8 heads of 128 46 -> 35 us, 256
+// tokens 26 -> 22; 2048 tokens, 256 workgroups each, 81 and 82.
+double together_us(AttnTileKind kind, const Problem &q, const Problem &kv, int pieces) {
+    const PassCost &kq = kPass[kDq], &kk = kPass[kDkv];
+    const int rows = attn_tile(kind).rows, column = (q.dim - 1) / 32;
+    const double cq = kStepUs[kDq][kind - kAttn64][column], ck = kStepUs[kDkv][kind - kAttn64][column];
+    const double units_q = (double)q.heads * ((q.rows + rows - 1) / rows),
+                 units_k = (double)kv.heads * ((kv.rows + rows - 1) / rows) * pieces;
+    const double keys = attn_tile(kind).keys, tokens = attn_grad_step(kind);
+    const double fq = kq.group + kq.joined, fk = kk.group + kk.joined;
+    const double longest_q = std::ceil(q.most / keys) * cq + fq, longest_k = std::ceil(std::ceil(kv.most / tokens) / pieces) * ck + fk;
+    const double longest = longest_q > longest_k ? longest_q : longest_k;
+    const double share = (units_q * (q.mean / keys * cq + fq) + units_k * (kv.mean / tokens / pieces * ck + fk)) / kAttnCUs;
+    const double work = units_q + units_k <= kAttnCUs ? longest : share + 0.3 * longest;
+    // four waves to a row meet at the end of the 64-row tiles, two in the others: 64 tokens, heads of 64 and
+    // 128, 13.7 and 20.6 us against 11.4 and 15.9
+    double us = 5.5 + (work > longest ? work : longest) + (kind == kAttn64 ? 0.037 * q.dim : 0.0);
+    if (pieces > 1) us += kk.join + (double)kv.heads * kv.rows * kv.dim * pieces * kk.part / 1e6;
+    return us;
+}
+// Of kPass[kDkv].call, the launch for the rows' numbers that dk and dv were timed with.
+constexpr double kRowsUs = 5.0;
+
 // The tensors of a call.
 struct Tensors {
     const attention_plan_s &p;
@@ -255,12 +280,30 @@ conv3d_status attention_plan(const attention_desc *d, attention_plan_t *out, siz
         back_mean = d->tk ? mean * d->tq / d->tk : 0.0;
         back_mean = back_mean < back ? back_mean : back;
     }
-    const Choice fwd = choose(kForward, {heads, r.rows, most, mean, d->head_dim}, true),
-                 dq = choose(kDq, {heads, r.rows, most, mean, d->head_dim}, false),
-                 dkv = choose(kDkv, {heads, d->tk, back * group, back_mean * group, d->head_dim}, true);
+    const Problem of_q = {heads, r.rows, most, mean, d->head_dim},
+                  of_kv = {heads, d->tk, back * group, back_mean * group, d->head_dim};
+    const Choice fwd = choose(kForward, of_q, true), dq = choose(kDq, of_q, false);
+    Choice dkv = choose(kDkv, of_kv, true);
     p->kind = fwd.kind;
-    p->kind_q = dq.kind;
-    p->kind_kv = dkv.kind;
+    p->grad = {dq.kind, dkv.kind, false};
+    if (heads > 0 && d->tq > 0 && d->tk > 0) {
+        const char *force = getenv("CONV3D_ATTENTION_TOGETHER");
+        double us = dq.us + dkv.us - kRowsUs;
+        for (AttnTileKind kind : {kAttn64, kAttn128}) {
+            if (forced_kind(kind, false) != kind) continue;
+            const int pieces = forced_pieces(dkv.kind == kind ? dkv.pieces : 1);
+            double both = together_us(kind, of_q, of_kv, pieces);
+            // unequal tiles fill the card well enough by themselves, and their first ones see few keys, whose
+            // numbers take a pass of their own
+            if (mean < 0.95 * most) both = 1.1 * both + 3.0;
+            if (force ? force[0] == '1' : both < us) {
+                us = both;
+                p->grad = {kind, kind, true};
+                dkv.kind = kind;
+                dkv.pieces = pieces;
+            }
+        }
+    }
     const AttnTileSize tile = attn_tile(fwd.kind);
     const int64_t units = heads * ((r.rows + tile.rows - 1) / tile.rows),
                   units64 = heads * (((int64_t)(r.rows > d->tk ? r.rows : d->tk) + 63) / 64);
@@ -425,7 +468,7 @@ conv3d_status attention_backward(attention_plan_t p, const void *dout, const voi
     r.ndelta = reinterpret_cast<float *>(ws + p->off_delta);
     r.part_dk = reinterpret_cast<float *>(ws + p->off_dk);
     r.part_dv = reinterpret_cast<float *>(ws + p->off_dv);
-    return launched(launch_attention_grad(r, p->kind_q, p->kind_kv, static_cast<hipStream_t>(stream)), "attention_backward");
+    return launched(launch_attention_grad(r, p->grad, static_cast<hipStream_t>(stream)), "attention_backward");
 }
 
 }  // extern "C"

@@ -36,17 +36,22 @@ __device__ __forceinline__ float dot8(half8_t a, half8_t b) {
 // sum itself, in a pass over the keys of its own, as long as there are at most kFewSpan of them: for 64
 // tokens, causal, the error of dq falls from 1.72 to 1.43 times that of the plain form.
 constexpr int kFewKeys = 160, kFewSpan = 512;
-template <typename E, int DP, int RG, int KG, int BN>
-__global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
-    constexpr int NT = DP / 32, KK = DP / 16, XN = BN / 32, STEP = KG * BN, TILE = STEP * DP * 2;
+//
+// READY: nlse and ndelta are there, from a launch of this kernel without dq.
+template <int DP, int RG, int KG, int BN>
+constexpr int dq_lds() {
     static_assert(RG * KG == 8, "eight waves");
-    __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];
-    static_assert((KG - 1) * RG * NT * 4096 <= (int)sizeof(smem), "the waves' sums fit the buffers");
+    static_assert((KG - 1) * RG * (DP / 32) * 4096 <= 4 * KG * BN * DP * 2, "the waves' sums fit the buffers");
+    return 4 * KG * BN * DP * 2 + (KG > 1 ? 2048 : 0);
+}
+template <typename E, int DP, int RG, int KG, int BN, bool READY>
+__device__ __forceinline__ void dq_tile(const AttnParams &p, int block, int tiles, char *smem) {
+    constexpr int NT = DP / 32, KK = DP / 16, XN = BN / 32, STEP = KG * BN, TILE = STEP * DP * 2;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rg = wave % RG, kg = wave / RG;
-    const int heads = p.n * p.hk, tiles = (int)gridDim.x / heads;
-    const int head = blockIdx.x % heads, tile = tiles - 1 - blockIdx.x / heads;
+    const int heads = p.n * p.hk;
+    const int head = block % heads, tile = tiles - 1 - block / heads;
     const int b = head / p.hk, hk = head % p.hk;
     const AttnSample s = attn_sample(p, b);
     const int r0 = tile * RG * 32, d = p.d, last = s.queries - 1;
@@ -58,7 +63,7 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
             const AttnRange first = attn_range(p, s, t_first);
             lo = first.lo & ~(BN - 1);
             hi = attn_range(p, s, t_last < last ? t_last : last).hi;
-            few = first.hi - first.lo < kFewKeys && hi - lo <= kFewSpan;
+            few = !READY && first.hi - first.lo < kFewKeys && hi - lo <= kFewSpan;
         }
         if (!p.dq && !few) hi = lo;  // the rows' sums alone are asked for
     }
@@ -84,12 +89,14 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
             if (alive && e < d) {
                 q[kk] = *reinterpret_cast<const half8_t *>(rq + e);
                 go[kk] = *reinterpret_cast<const half8_t *>(p.dout + at + e);
-                o = *reinterpret_cast<const half8_t *>(p.o + at + e);
+                if (!READY) o = *reinterpret_cast<const half8_t *>(p.o + at + e);
             }
-            delta += dot8<E>(go[kk], o);
+            if (!READY) delta += dot8<E>(go[kk], o);
         }
-        delta = both_sum(delta);
-        if (alive) lse = p.lse[((int64_t)b * p.hq + h) * p.tq + i];
+        if (!READY) delta = both_sum(delta);
+        const int64_t row = ((int64_t)b * p.hq + h) * p.tq + i;
+        if (alive) lse = p.lse[row];
+        if (READY && alive) delta = -p.ndelta[row];
     }
     const AttnRange seen = last < 0 ? AttnRange{0, 0} : attn_range(p, s, i < last ? i : last);
     const int wave_lo = __builtin_amdgcn_readfirstlane(seen.lo), wave_hi_all = __builtin_amdgcn_readfirstlane(seen.hi);
@@ -167,7 +174,7 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
         pass(std::true_type{});
         sum = both_sum(sum);
         if constexpr (KG > 1) {
-            __shared__ float parts[512];
+            float *parts = reinterpret_cast<float *>(smem + 4 * TILE);
             parts[threadIdx.x] = sum;
             __syncthreads();
             sum = 0.0f;
@@ -182,7 +189,7 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
             tv.load(smem + TILE, lo, wave);
         }
     }
-    if (r < p.rows && lane < 32 && kg == 0) {
+    if (!READY && r < p.rows && lane < 32 && kg == 0) {
         const int64_t row = ((int64_t)b * p.hq + h) * p.tq + i;
         p.nlse[row] = start_of_scores(lse, p.scale);
         p.ndelta[row] = alive ? -delta : 0.0f;
@@ -209,28 +216,37 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, acc[t], p.scale * kDrop<E> / scale.f, d - 32 * t, lane, true);
 }
+template <typename E, int DP, int RG, int KG, int BN>
+__global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
+    __shared__ __attribute__((aligned(1024))) char smem[dq_lds<DP, RG, KG, BN>()];
+    dq_tile<E, DP, RG, KG, BN, false>(p, blockIdx.x, (int)gridDim.x / (p.n * p.hk), smem);
+}
 
 // ---- dk, dv: tiles of 32 KW keys and BM QG query tokens, 8 waves: wave (kw, qg) holds keys
 // 32 kw .. + 31 (one key per lane of every result) and takes the qg-th BM tokens of each step; the
 // query heads of the key head are taken one after the other.  S = Q K^T and dP = dout V^T; P
 // and dS are, as they stand, the operands of dv^T = dout^T P and dk^T = Q^T dS.  The qg waves of
 // the same keys meet in LDS at the end.
-template <typename E, int DP, int KW, int QG, int BM>
-__global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
-    constexpr int NT = DP / 32, KK = DP / 16, XN = BM / 32, STEP = QG * BM, TILE = STEP * DP * 2, BN = KW * 32;
+template <int DP, int KW, int QG, int BM>
+constexpr int dkv_lds() {
+    constexpr int bytes = (DP > 64 ? KW * 32 * DP * 2 : 0) + 4 * QG * BM * DP * 2 + 4 * QG * BM * 4;
     static_assert(KW * QG == 8, "eight waves");
+    static_assert(bytes <= 160 * 1024, "LDS is 160 KiB per CU");
+    static_assert((QG - 1) * KW * (DP / 32) * 4096 <= bytes, "the waves' sums fit the buffers");
+    return bytes;
+}
+template <typename E, int DP, int KW, int QG, int BM>
+__device__ __forceinline__ void dkv_tile(const AttnParams &p, int block, int piece, char *smem) {
+    constexpr int NT = DP / 32, KK = DP / 16, XN = BM / 32, STEP = QG * BM, TILE = STEP * DP * 2, BN = KW * 32;
     constexpr bool KLDS = DP > 64;  // k in LDS: with both in registers two waves would not fit a SIMD
     constexpr int KBYTES = KLDS ? BN * DP * 2 : 0;
-    __shared__ __attribute__((aligned(1024))) char smem[KBYTES + 4 * TILE + 4 * STEP * 4];
-    static_assert(sizeof(smem) <= 160 * 1024, "LDS is 160 KiB per CU");
-    static_assert((QG - 1) * KW * NT * 4096 <= (int)sizeof(smem), "the waves' sums fit the buffers");
     char *tiles = smem + KBYTES;
     float *rows_at = reinterpret_cast<float *>(tiles + 4 * TILE);  // [2][nlse, ndelta][STEP]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kw = wave % KW, qg = wave / KW;
     const int heads = p.n * p.hk;
-    const int head = blockIdx.x % heads, tile = blockIdx.x / heads;  // the longest of a masked problem first
+    const int head = block % heads, tile = block / heads;  // the longest of a masked problem first
     const int b = head / p.hk, hk = head % p.hk;
     const AttnSample s = attn_sample(p, b);
     const int j0 = tile * BN, j = j0 + kw * 32 + (lane & 31), last = s.keys - 1, d = p.d;
@@ -244,8 +260,8 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
     const int steps = hi > lo ? (hi - lo + STEP - 1) / STEP : 0;
     int first = 0, total = steps * p.group;
     if (p.grad_splits > 1) {
-        first = blockIdx.y * p.grad_pieces;
-        if (first >= total && blockIdx.y) return;  // the join counts the pieces the same way
+        first = piece * p.grad_pieces;
+        if (first >= total && piece) return;  // the join counts the pieces the same way
         total = total < first + p.grad_pieces ? total : first + p.grad_pieces;
     }
     int load_g = steps ? first / steps : 0, load_step = first - load_g * steps;
@@ -389,7 +405,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
     }
     if (j >= p.tk) return;
     if (p.grad_splits > 1) {
-        const int64_t at = (((int64_t)blockIdx.y * heads + head) * p.tk + j) * d;
+        const int64_t at = (((int64_t)piece * heads + head) * p.tk + j) * d;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -416,6 +432,24 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, av[t], kDrop<E>, d - 32 * t, lane, true);
     }
+}
+template <typename E, int DP, int KW, int QG, int BM>
+__global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
+    __shared__ __attribute__((aligned(1024))) char smem[dkv_lds<DP, KW, QG, BM>()];
+    dkv_tile<E, DP, KW, QG, BM>(p, blockIdx.x, blockIdx.y, smem);
+}
+
+// Both in one launch, where neither fills the card: blocks [0, kv_units) dk and dv, piece by piece, the
+// others dq, with the rows' numbers from a launch before.
+template <typename E, int DP, int W, int G, int BN, int BM>
+__global__ __launch_bounds__(512, 2) void attention_grads_kernel(AttnParams p, int kv_units, int kv_tiles, int q_tiles) {
+    constexpr int A = dq_lds<DP, W, G, BN>(), B = dkv_lds<DP, W, G, BM>();
+    __shared__ __attribute__((aligned(1024))) char smem[A > B ? A : B];
+    const int b = blockIdx.x;
+    if (b < kv_units)
+        dkv_tile<E, DP, W, G, BM>(p, b % kv_tiles, b / kv_tiles, smem);
+    else
+        dq_tile<E, DP, W, G, BN, true>(p, b - kv_units, q_tiles, smem);
 }
 
 // The pieces of each key's steps added in their order: four elements per lane.
@@ -456,51 +490,61 @@ __global__ __launch_bounds__(256) void attention_dkv_join_kernel(AttnParams p, i
 }
 
 template <typename E, int DP>
-static void launch_grad(const AttnParams &p, AttnTileKind kq, AttnTileKind kkv, hipStream_t s) {
-    const int heads = p.n * p.hk;
+static void launch_grad(const AttnParams &p, const AttnGradKinds &k, hipStream_t s) {
+    const int heads = p.n * p.hk, rows = attn_tile(k.q).rows, keys = attn_tile(k.kv).rows;
+    const int q_tiles = (p.rows + rows - 1) / rows, kv_tiles = heads * ((p.tk + keys - 1) / keys);
     const dim3 block(512);
+    const bool kv = p.tk > 0 && (p.dk || p.dv), together = k.together && kv && p.dq && p.tq > 0;
     if (p.tq > 0) {
-        const int rows = attn_tile(kq).rows;
-        const dim3 grid((uint32_t)(heads * ((p.rows + rows - 1) / rows)));
-        switch (kq) {
-            case kAttn64: attention_dq_kernel<E, DP, 2, 4, 32><<<grid, block, 0, s>>>(p); break;
-            case kAttn128: attention_dq_kernel<E, DP, 4, 2, 64><<<grid, block, 0, s>>>(p); break;
-            default: attention_dq_kernel<E, DP, 8, 1, 64><<<grid, block, 0, s>>>(p); break;
+        AttnParams r = p;
+        if (together) r.dq = nullptr;  // the rows' numbers alone
+        const dim3 grid((uint32_t)(heads * q_tiles));
+        switch (k.q) {
+            case kAttn64: attention_dq_kernel<E, DP, 2, 4, 32><<<grid, block, 0, s>>>(r); break;
+            case kAttn128: attention_dq_kernel<E, DP, 4, 2, 64><<<grid, block, 0, s>>>(r); break;
+            default: attention_dq_kernel<E, DP, 8, 1, 64><<<grid, block, 0, s>>>(r); break;
         }
     }
-    if (p.tk > 0 && (p.dk || p.dv)) {
-        const int keys = attn_tile(kkv).rows;
-        const dim3 grid((uint32_t)(heads * ((p.tk + keys - 1) / keys)), (uint32_t)p.grad_splits);
-        switch (kkv) {
+    if (!kv) return;
+    if (together) {
+        const int kv_units = kv_tiles * p.grad_splits;
+        const dim3 grid((uint32_t)(kv_units + heads * q_tiles));
+        if (k.kv == kAttn64)
+            attention_grads_kernel<E, DP, 2, 4, 32, 32><<<grid, block, 0, s>>>(p, kv_units, kv_tiles, q_tiles);
+        else
+            attention_grads_kernel<E, DP, 4, 2, 64, 32><<<grid, block, 0, s>>>(p, kv_units, kv_tiles, q_tiles);
+    } else {
+        const dim3 grid((uint32_t)kv_tiles, (uint32_t)p.grad_splits);
+        switch (k.kv) {
             case kAttn64: attention_dkv_kernel<E, DP, 2, 4, 32><<<grid, block, 0, s>>>(p); break;
             case kAttn128: attention_dkv_kernel<E, DP, 4, 2, 32><<<grid, block, 0, s>>>(p); break;
             default: attention_dkv_kernel<E, DP, 8, 1, 64><<<grid, block, 0, s>>>(p); break;
         }
-        if (p.grad_splits > 1) {
-            const int64_t count = (int64_t)heads * p.tk * (p.d / 4);
-            attention_dkv_join_kernel<E><<<dim3((uint32_t)((count + 255) / 256)), dim3(256), 0, s>>>(
-                p, keys, attn_grad_step(kkv), kkv == kAttn256 ? 64 : 32);
-        }
+    }
+    if (p.grad_splits > 1) {
+        const int64_t count = (int64_t)heads * p.tk * (p.d / 4);
+        attention_dkv_join_kernel<E><<<dim3((uint32_t)((count + 255) / 256)), dim3(256), 0, s>>>(
+            p, keys, attn_grad_step(k.kv), k.kv == kAttn256 ? 64 : 32);
     }
 }
 
 template <typename E>
-static void launch_grad_dim(const AttnParams &p, AttnTileKind kq, AttnTileKind kkv, hipStream_t s) {
+static void launch_grad_dim(const AttnParams &p, const AttnGradKinds &k, hipStream_t s) {
     if (p.d <= 32)
-        launch_grad<E, 32>(p, kq, kkv, s);
+        launch_grad<E, 32>(p, k, s);
     else if (p.d <= 64)
-        launch_grad<E, 64>(p, kq, kkv, s);
+        launch_grad<E, 64>(p, k, s);
     else if (p.d <= 96)
-        launch_grad<E, 96>(p, kq, kkv, s);
+        launch_grad<E, 96>(p, k, s);
     else
-        launch_grad<E, 128>(p, kq, kkv, s);
+        launch_grad<E, 128>(p, k, s);
 }
 
-hipError_t launch_attention_grad(const AttnParams &p, AttnTileKind kq, AttnTileKind kkv, hipStream_t s) {
+hipError_t launch_attention_grad(const AttnParams &p, const AttnGradKinds &k, hipStream_t s) {
     if (p.bf16)
-        launch_grad_dim<__bf16>(p, kq, kkv, s);
+        launch_grad_dim<__bf16>(p, k, s);
     else
-        launch_grad_dim<_Float16>(p, kq, kkv, s);
+        launch_grad_dim<_Float16>(p, k, s);
     return hipGetLastError();
 }
 

@@ -185,7 +185,11 @@ hipError_t launch_attention(const AttnParams &p, AttnTileKind kind, hipStream_t 
 // dq by tiles of kind_q; dk and dv by tiles of as many keys as kind_kv has rows, and 64
 // query tokens (kAttn64: 128) to a step.
 constexpr int attn_grad_step(AttnTileKind kind) { return kind == kAttn64 ? 128 : 64; }
-hipError_t launch_attention_grad(const AttnParams &p, AttnTileKind kind_q, AttnTileKind kind_kv, hipStream_t s);
+struct AttnGradKinds {
+    AttnTileKind q, kv;
+    bool together;  // in one launch: both kAttn64 or both kAttn128
+};
+hipError_t launch_attention_grad(const AttnParams &p, const AttnGradKinds &k, hipStream_t s);
 
 // ---- adamw
 constexpr int kAdamwBlock = 128;    // elements that share a scale

@@ -536,7 +536,8 @@ typedef struct {
  * partials in the workspace that a second small kernel joins in a fixed order; few
  * keys against many queries split the queries in the backward pass the same way.
  * The environment variables CONV3D_ATTENTION_TILE=<name> and CONV3D_ATTENTION_SPLITS=<n>
- * force a kernel (where it can run the call) and a number of pieces.
+ * force a kernel (where it can run the call) and a number of pieces,
+ * CONV3D_ATTENTION_TOGETHER=1 or 0 whether a backward pass takes dq, dk and dv in one launch.
  */
 conv3d_status attention_plan(const attention_desc *d, attention_plan_t *out, size_t *workspace_bytes);
 conv3d_status attention_plan_query(attention_plan_t p, attention_plan_info *info);

@@ -198,10 +198,11 @@ def ident(c):
     return "-".join("%s=%s" % (k, v if k != "lengths" else "given") for k, v in c.items())
 
 
-@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("splits,together", [(1, 0), (3, 0), (1, 1), (4, 1)])
 @pytest.mark.parametrize("tile", ["attention_64x128", "attention_128x128", "attention_256x64"])
 @pytest.mark.parametrize("case", [c for c in CASES if c.get("tq", 64) > 1 and c.get("tk", 64) > 40], ids=ident)
-def test_every_tile_and_pieces(case, tile, splits, monkeypatch):
+def test_every_tile_and_pieces(case, tile, splits, together, monkeypatch):
+    monkeypatch.setenv("CONV3D_ATTENTION_TOGETHER", str(together))
     monkeypatch.setenv("CONV3D_ATTENTION_TILE", tile)
     monkeypatch.setenv("CONV3D_ATTENTION_SPLITS", str(splits))
     c = Case(**case)
