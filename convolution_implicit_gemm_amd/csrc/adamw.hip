@@ -42,11 +42,11 @@ __device__ __forceinline__ void decode4(uint32_t c, float unit, float (&x)[4]) {
 // The block's power e: the least from -126 on with its largest finite value at most
 // 448 * 2^e (448 = 7/8 * 2^9, the largest e4m3 number).  The block is 32 lanes' 4 values.
 __device__ __forceinline__ int block_power(const float (&x)[4]) {
-    float top = 0.0f;
+    float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    if (!(top < __builtin_inff())) {  // rare: infinities, and NaN in all four
+        top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float a = fabsf(x[i]);
-        top = fmaxf(top, a < __builtin_inff() ? a : 0.0f);
+        for (int i = 0; i < 4; ++i) top = fabsf(x[i]) < __builtin_inff() ? fmaxf(top, fabsf(x[i])) : top;
     }
     const uint32_t bits = __builtin_bit_cast(uint32_t, max32(top));
     const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);  // 1.75 * 2^8 = 448
@@ -83,14 +83,15 @@ __device__ __forceinline__ void inverse_powers(const int (&e)[N], float (&inv)[N
 template <bool ROOT>
 __device__ __forceinline__ uint32_t encode4(const float (&x)[4], float inv) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    float y[4];
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * inv, x[1] * inv, 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * inv, x[3] * inv, v, true);
+    uint32_t c = (uint32_t)v;
+    if (ROOT && ((c - 0x01010101u) & ~c & 0x80808080u)) {  // a byte of 0: the least code but 0 for what is not 0
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        y[i] = x[i] * inv;
-        if (ROOT) y[i] = x[i] > 0.0f ? fmaxf(y[i], 0x1p-9f) : y[i];  // the least code but 0
+        for (int i = 0; i < 4; ++i)
+            if (!(c >> (8 * i) & 0xffu) && x[i] > 0.0f) c |= 1u << (8 * i);
     }
-    const int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], v, true);
+    return c;
 #else
     return 0;
 #endif
@@ -193,7 +194,7 @@ __device__ __forceinline__ void new_states(const AdamwHyper &h, float x, float &
 // lines of it to a wave), half a wave a block of 128, whose scale it finds by itself; a
 // workgroup adamw_unit() adjacent elements of one tensor, all of them on their way at once, so that
 // workgroups that run together read and write adjacent memory: 201 million weights, 8-bit
-// states 548 us, 5.9 TB/s, bound by memory (with 24 times the elements to a workgroup, one after the
+// states 538 us, 6.0 TB/s, bound by memory (with 24 times the elements to a workgroup, one after the
 // other, a fifth more).
 template <typename E, bool STATE8, bool GRAD32, bool FAR>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamwParams p) {
@@ -245,7 +246,9 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwParams p) {
             const float x = g[k][i] * h.grad_scale;
             float root;
             new_states(h, x, m[k][i], v[k][i], root);
-            w[k][i] = fmaf(w[k][i], keep, -h.lr1 * (m[k][i] / fmaf(root, h.root2, h.eps)));
+            // the instruction's reciprocal, an ulp off at most: 2^-23 of the step, not of the weight; the
+            // denominator is at least a root of 2^-149, never a subnormal, unless eps is one
+            w[k][i] = fmaf(w[k][i], keep, -h.lr1 * m[k][i] * __builtin_amdgcn_rcpf(fmaf(root, h.root2, h.eps)));
             if (STATE8) v[k][i] = root;
         }
         if (t.master) store_f32<FAR>(t.master + base, left[k], w[k]);
