@@ -43,7 +43,10 @@ __device__ __forceinline__ float attn_inverse(float sum) { return sum == 0.0f ? 
 // every lane one of them, and takes the kg-th BN keys of each step; the kg waves of the same rows
 // meet in LDS at the end.  Two steps' K and V are in LDS in turn, loaded straight into it while
 // the step before is computed.  More rows to a tile read K and V less often, more waves to a
-// row shorten the way through its keys: where the rows alone do not fill the card.
+// row shorten the way through its keys: where the rows alone do not fill the card.  What is left
+// is the latency of a step: score products, softmax and output products of a wave depend on each other, and
+// the other wave of its SIMD fills only part of the gaps (9 frames of 1024 tokens, 16 heads of 128: 103-109 us,
+// 710-750 TFLOP/s, matrix cores busy 48%).  Deeper rings do not help: 3 and 4 steps in LDS were level to slower.
 template <typename E, int DP, int RG, int KG, int BN>
 __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_tile_kernel(AttnParams p) {
     constexpr int NT = DP / 32, KK = DP / 16, XN = BN / 32, STEP = KG * BN, TILE = STEP * DP * 2;
@@ -233,6 +236,10 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_tile_kernel(A
 // softmax of step t a wave issues its share of K(t + 2) and V(t + 1), which take the places of
 // K(t - 1) and V(t - 2), whose last readers were one phase and two phases ago, and sees that they have landed
 // at the end of the products that follow; the other group's first reads of them are two phases later.
+// 20480 tokens causal by frames of 4096, 16 heads of 128: 1709-1760 us, 1170-1205 TFLOP/s (the tile kernel 1904),
+// matrix cores busy 65% at the 1.7-1.8 GHz that power leaves.  At heads of 64 the vector units bound it: a
+// score costs as many of their cycles as at 128 for half the products (4096 rows on 20480 keys 392-405 us,
+// 850-880 TFLOP/s, vector units busy 63%, matrix cores 40%; two workgroups per CU were level).
 template <typename E, int DP>
 __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_phase_kernel(AttnParams p) {
     constexpr int BN = 64, NT = DP / 32, KK = DP / 16, TILE = BN * DP * 2;
@@ -393,7 +400,8 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_phase_kernel(
 // ---- few rows (at most 32 to a key head: single tokens): the time is that of reading
 // K and V once.  Every wave takes 32 keys at a time, in turn with the other waves, through
 // LDS buffers of its own, so that no barrier ties the waves' loads together; their sums
-// meet in LDS at the end.
+// meet in LDS at the end.  16 samples of one token, 16 heads over 4 key heads of 128, up to 36864
+// keys: 170 us and 4.3 for the join, 5.5 TB/s, bound by memory (matrix cores busy 10%).
 template <typename E, int DP>
 __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
     constexpr int WAVES = 4, BN = 32, NT = DP / 32, KK = DP / 16, TILE = BN * DP * 2, NL = 2 * AttnTile<DP, BN, 1>::LOADS;
@@ -541,7 +549,8 @@ __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
 }
 
 // The pieces of each row's keys joined, in a fixed order: a workgroup per row, LANES lanes of four
-// elements to a piece, the pieces in turn over the workgroup, whose sums meet in LDS.
+// elements to a piece, the pieces in turn over the workgroup, whose sums meet in LDS.  (With a wave per
+// row, one token of 16 heads on 36864 keys of 4 key heads, 128 pieces, took 38 us instead of 20.)
 template <typename E, int LANES>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnParams p) {
     constexpr int SETS = 256 / LANES;

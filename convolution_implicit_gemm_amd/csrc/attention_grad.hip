@@ -37,6 +37,11 @@ __device__ __forceinline__ float dot8(half8_t a, half8_t b) {
 // tokens, causal, the error of dq falls from 1.72 to 1.43 times that of the plain form.
 constexpr int kFewKeys = 160, kFewSpan = 512;
 //
+// Three products for two of the forward pass, and the exponentials once more; K and V of a step are in LDS,
+// read as they lie and transposed.  20480 tokens causal by frames of 4096, 16 heads of 128: 2502 us, 1236 TFLOP/s,
+// matrix cores busy 65%, power-bound as the forward pass; 3 samples of 1543 tokens, 12 heads of 80: 38 us, busy 27%, the
+// latency of its steps.
+//
 // READY: nlse and ndelta are there, from a launch of this kernel without dq.
 template <int DP, int RG, int KG, int BN>
 constexpr int dq_lds() {
@@ -227,6 +232,11 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
 // query heads of the key head are taken one after the other.  S = Q K^T and dP = dout V^T; P
 // and dS are, as they stand, the operands of dv^T = dout^T P and dk^T = Q^T dS.  The qg waves of
 // the same keys meet in LDS at the end.
+//
+// 20480 tokens causal by frames of 4096, 16 heads of 128: 3566 us, 1155 TFLOP/s over its four products, matrix cores
+// busy 55%, LDS 41%: a SIMD's two waves hold 256 accumulators, and what a wave reads of Q and dout
+// feeds only its 32 keys.  One wave per SIMD with 64 keys, its steps pipelined, reads half of that
+// and took 4686 us: nothing fills its softmax.  3 samples of 1543 tokens, 12 heads of 80 on 4: 50 us and 6 for the join.
 template <int DP, int KW, int QG, int BM>
 constexpr int dkv_lds() {
     constexpr int bytes = (DP > 64 ? KW * 32 * DP * 2 : 0) + 4 * QG * BM * DP * 2 + 4 * QG * BM * 4;
@@ -440,7 +450,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(AttnParams p) {
 }
 
 // Both in one launch, where neither fills the card: blocks [0, kv_units) dk and dv, piece by piece, the
-// others dq, with the rows' numbers from a launch before.
+// others dq, with the rows' numbers from a launch before.  1024 tokens, 8 heads of 128: all gradients 46 -> 35 us.
 template <typename E, int DP, int W, int G, int BN, int BM>
 __global__ __launch_bounds__(512, 2) void attention_grads_kernel(AttnParams p, int kv_units, int kv_tiles, int q_tiles) {
     constexpr int A = dq_lds<DP, W, G, BN>(), B = dkv_lds<DP, W, G, BM>();
