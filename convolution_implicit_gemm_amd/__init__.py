@@ -803,6 +803,7 @@ def adamw_list(params, grads, m, v, master=None, m_scale=None, v_scale=None, dec
     decay for each tensor (1).  The tensors have to stay where they are as long as the list is used."""
     _elem_dtype(False)
     import torch
+    grads = list(grads)
     count = len(grads)
     none = [None] * count
 
@@ -816,7 +817,10 @@ def adamw_list(params, grads, m, v, master=None, m_scale=None, v_scale=None, dec
     kinds = {t.dtype for t in lists[0] if t is not None}
     if len(kinds) > 1 or not kinds <= {_F16, _BF16}:
         bad("params are %s, all fp16 or all bf16 expected" % sorted(map(str, kinds)))
-    grad_kinds = {t.dtype for t in grads}
+    for i, t in enumerate(lists[2]):
+        if t is None:
+            bad("grads[%d] is missing" % i)
+    grad_kinds = {t.dtype for t in lists[2]}
     if len(grad_kinds) > 1:
         bad("grads are of different types")
     grad32 = grad_kinds == {_F32}

@@ -76,8 +76,9 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_tile_kernel(A
         const int end = lo + p.pieces * STEP;
         hi = hi < end ? hi : end;
     }
-    const AttnTile<DP, STEP, 8> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane),
-        tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
+    // keys behind hi come as zeros, whatever a cache holds there
+    const AttnTile<DP, STEP, 8> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], hi, d, wave, lane),
+        tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], hi, d, wave, lane);
     if (lo < hi) {
         tk.load(smem, lo, wave);
         tv.load(smem + TILE, lo, wave);
@@ -264,8 +265,8 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_phase_kernel(
         const int end = lo + p.pieces * BN;
         hi = hi < end ? hi : end;
     }
-    const AttnTile<DP, BN, 8> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, wave, lane),
-        tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, wave, lane);
+    const AttnTile<DP, BN, 8> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], hi, d, wave, lane),
+        tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], hi, d, wave, lane);
     char *const vbuf = smem + 3 * TILE;
     const bool any = lo < hi;
     if (any) {
@@ -426,7 +427,8 @@ __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
         hi = hi < end ? hi : end;
     }
     const int d = p.d;
-    const AttnTile<DP, BN, 1> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], s.keys, d, 0, lane), tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], s.keys, d, 0, lane);
+    const AttnTile<DP, BN, 1> tk(p.k + b * p.ks[0] + hk * p.ks[2], p.ks[1], hi, d, 0, lane),
+        tv(p.v + b * p.vs[0] + hk * p.vs[2], p.vs[1], hi, d, 0, lane);
     char *mine = smem + wave * 4 * TILE;
     int buf = 0;
     int j0 = lo + wave * BN;

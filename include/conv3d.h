@@ -498,9 +498,11 @@ conv3d_status rope3d_backward(rope3d_plan_t p, const void *dq_out, const void *d
  * o = 0, lse = -inf and no part in any gradient.
  * Arithmetic is fp32, o is rounded once; probabilities (and in the backward pass their
  * gradients) are rounded to the element type as operands of the second products.
- * Tokens that a query does not see do not reach it as long as they are finite: an
- * infinite or NaN v in a sample may reach all queries of that sample, and an infinite or
- * NaN k, v, q or dout all of its gradients.
+ * The forward pass never reads keys behind the last one that a query of the call sees, so a
+ * cache may hold anything behind the tokens written so far.  Other tokens that a query does not
+ * see do not reach it as long as they are finite: an infinite or NaN v that one query sees, or that
+ * lies before its window, may reach all queries of that sample, and an infinite or NaN k, v, q or
+ * dout anywhere in a sample all of its gradients.
  */
 typedef struct {
     int32_t n, heads_q, heads_k, head_dim;

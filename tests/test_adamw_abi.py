@@ -106,3 +106,5 @@ def test_binding_checks_the_lists():
                  (None, [f], [f], [f])):
         with pytest.raises(c3d.Conv3dError):
             c3d.adamw_list(*args, master=[f])
+    with pytest.raises(c3d.Conv3dError, match=r"grads\[1\] is missing"):
+        c3d.adamw_list(None, [f, None], [f, f], [f, f], master=[f, f])

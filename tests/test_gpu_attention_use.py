@@ -132,6 +132,27 @@ def test_ragged_cache_buffers_longer_than_their_samples():
             assert float((o[b, 0, h].double() - ref).abs().max()) <= 3 * 2.0 ** -11 * float(vv.abs().max())
 
 
+@pytest.mark.parametrize("frame, window", [(1, 0), (1, 40), (7, 0)])
+@pytest.mark.parametrize("kind", ["", "attention_64x128", "attention_128x128", "attention_256x64"])
+@pytest.mark.parametrize("tq, room, at", [(1, 300, 0), (1, 3000, 1777), (5, 300, 41), (70, 517, 130), (300, 700, 100)])
+def test_caches_hold_anything_behind_what_the_call_sees(tq, room, at, kind, frame, window, monkeypatch):
+    if kind:
+        monkeypatch.setenv("CONV3D_ATTENTION_TILE", kind)
+    hq, hk, d = 4, 2, 64
+    seen = min(((at + tq - 1) // frame + 1) * frame, room)
+    g = gen(13)
+    q, k, v = (normal(g, (1, t, h, d), torch.bfloat16) for t, h in ((tq, hq), (room, hk), (room, hk)))
+    desc = c3d.make_attention_desc(1, tq, room, hq, hk, d, frame=frame, window=window, flags=c3d.CONV3D_F_BF16)
+    p = c3d.attention_plan(desc)
+    outs = []
+    for fill in (0.0, float("nan"), float("inf")):
+        k[:, seen:] = v[:, seen:] = fill
+        outs.append(torch.empty_like(q))
+        c3d.attention_forward(p, q, k, v, outs[-1], q_offset=at, workspace=scratch(p.workspace_bytes))
+    assert not torch.isnan(outs[0]).any()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
 def test_outputs_leave_what_lies_around_them():
     n, t, hq, hk, d = 2, 70, 3, 1, 40
     g = gen(5)
