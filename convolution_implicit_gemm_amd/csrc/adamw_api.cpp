@@ -51,6 +51,8 @@ conv3d_status hyper_of(const adamw_hyper *h, AdamwHyper *out) {
     out->root2 = (float)(1.0 / std::sqrt(rest(h->beta2)));
     out->eps = (float)h->eps;
     out->lr_decay = (float)(h->lr * h->weight_decay);
+    for (float x : {out->grad_scale, out->lr1, out->root2, out->eps, out->lr_decay})
+        if (!std::isfinite(x)) return api_fail(CONV3D_ERR_INVALID_ARG, "a hyperparameter is past the range of fp32");
     return CONV3D_OK;
 }
 static_assert(sizeof(AdamwHyper) == ADAMW_DEVICE_HYPER * sizeof(float), "the numbers in device memory");

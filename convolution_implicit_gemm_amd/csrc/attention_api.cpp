@@ -211,6 +211,9 @@ conv3d_status attention_plan(const attention_desc *d, attention_plan_t *out, siz
     if (d->head_dim < 1) return api_fail(CONV3D_ERR_INVALID_ARG, "head_dim must be positive");
     if (!(d->scale >= 0.0f) || !std::isfinite(d->scale))
         return api_fail(CONV3D_ERR_INVALID_ARG, "scale must be positive and finite, or 0");
+    // the backward pass starts its scores from -lse / scale
+    if (d->scale > 0.0f && (d->scale < 0x1p-64f || d->scale > 0x1p64f))
+        return api_fail(CONV3D_ERR_UNSUPPORTED, "scale is outside 2^-64 .. 2^64");
     const uint32_t known = CONV3D_F_BF16 | CONV3D_F_LENGTHS | CONV3D_F_TAIL;
     if (d->flags & ~known) return api_fail(CONV3D_ERR_INVALID_ARG, "unknown flag bits 0x%x", d->flags & ~known);
     if (d->head_dim % 8 || d->head_dim > kAttnMaxDim)

@@ -531,7 +531,7 @@ typedef struct {
  * without a frame, heads_q not a positive multiple of heads_k, head_dim < 1, a scale that is negative or not
  * finite, unknown flags, or strides that are negative, not a multiple of 8, or
  * (between tokens, with more than one) shorter than a head; UNSUPPORTED for head_dim
- * not a multiple of 8 or above 128, more than 16384 heads, 2^30 tokens or more (of a sample, times
+ * not a multiple of 8 or above 128, a scale (but 0) outside 2^-64 .. 2^64, more than 16384 heads, 2^30 tokens or more (of a sample, times
  * heads_q / heads_k for queries), token strides above 2^20, others of 2^40 or more, a tensor of 2^48
  * elements or more from its first to its last, or more than 2^31 threads' work.
  * Few rows against many keys split the keys over workgroups, which leave fp32
@@ -619,7 +619,7 @@ void adamw_plan_destroy(adamw_plan_t p);
 /* The numbers that the kernels take, as fp32 (computed in 64 bits). */
 enum { ADAMW_DEVICE_HYPER = 9 };
 /* INVALID_ARG for lr, eps or weight_decay negative or not finite, betas outside [0, 1), a
- * grad_scale that is not finite, or step < 1. */
+ * grad_scale that is not finite, numbers past the range of fp32, or step < 1. */
 conv3d_status adamw_hyper_pack(const adamw_hyper *h, float *out);
 
 /*

@@ -83,6 +83,14 @@ def test_hyperparameters_are_checked(bad):
     assert e.value.status == BAD
 
 
+@pytest.mark.parametrize("bad", [dict(lr=1e39), dict(lr=1e38, beta1=0.999), dict(eps=1e39), dict(grad_scale=-1e39),
+                                 dict(lr=1e20, weight_decay=1e20)])
+def test_hyperparameters_past_fp32(bad):
+    with pytest.raises(c3d.Conv3dError) as e:
+        c3d.adamw_hyper_pack(c3d.make_adamw_hyper(**dict(dict(lr=1e-3), **bad)))
+    assert e.value.status == BAD
+
+
 def test_packed_numbers():
     h = c3d.make_adamw_hyper(1e-3, 0.9, 0.999, 1e-8, 0.1, 10, 0.5)
     want = [0.5, 0.9, 0.1, 0.999, 0.001, 1e-3 / (1 - 0.9 ** 10), (1 - 0.999 ** 10) ** -0.5, 1e-8, 1e-4]

@@ -42,6 +42,15 @@ def test_plan_refuses(bad, want):
     assert status(c3d.attention_plan, desc(**bad)) == want
 
 
+@pytest.mark.parametrize("scale,ok", [(2.0 ** -64, True), (2.0 ** 64, True), (0.0, True), (2.0 ** -66, False), (1e-39, False),
+                                      (2.0 ** 65, False)])
+def test_scales_that_lse_can_be_divided_by(scale, ok):
+    if ok:
+        c3d.attention_plan(desc(scale=scale))
+    else:
+        assert status(c3d.attention_plan, desc(scale=scale)) == UNSUP
+
+
 def test_null_pointers():
     lib = c3d.load_library()
     h, ws, d = ctypes.c_void_p(), ctypes.c_size_t(), desc()

@@ -221,6 +221,15 @@ def test_forward_and_gradients(case):
     c.check_backward(outs)
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -64, 2.0 ** -10, 2.0])
+@pytest.mark.parametrize("d,tk", [(64, 90), (128, 300)])
+def test_scales_far_from_the_usual(d, tk, scale):
+    c = Case(tq=80, tk=tk, hq=4, hk=2, d=d, scale=scale)
+    c.forward()
+    c.check_forward()
+    c.check_backward(c.backward())
+
+
 def l2(a, b):
     """Relative, beyond what the result's own rounding below fp16's normal numbers allows: half of 2^-24 for each
     element (dk of the first case below is 1e-5, where fp16's steps are 2^-24 = 6e-8)."""
