@@ -86,8 +86,8 @@ class LatentBlock:
         """y, and what the backward pass needs."""
         m, c, p, ws = self.m, self.c, self.p, self.ws
         s = {"x": x, "n1": self.rows(c), "st1": self.rows(2, torch.float32), "qkv": self.rows(3 * c),
-             "o": self.rows(c), "lse": torch.empty((1, self.heads, m), device="cuda"), "x1": self.rows(c), "n2": self.rows(c), "st2": self.rows(2, torch.float32), "up": self.rows(4 * c),
-             "z": self.rows(4 * c)}
+             "o": self.rows(c), "lse": torch.empty((1, self.heads, m), device="cuda"), "x1": self.rows(c), "n2": self.rows(c),
+             "st2": self.rows(2, torch.float32), "up": self.rows(4 * c), "z": self.rows(4 * c)}
         y = self.rows(c)
         c3d.layernorm_bf16(x, p["g1"], p["b1"], s["n1"], s["st1"], m, c, EPS)
         c3d.linear_forward(self.plans["qkv"], s["n1"], p["qkv"], p["qkv_b"], None, s["qkv"], None, ws)
