@@ -8,17 +8,31 @@
 // rescaling of a query's output are a lane's own business (one exchange between
 // the halves of the wave for the maximum), and its registers are, as they stand, the operand
 // P^T of O^T = V^T P^T.  Probabilities are rounded to the element type for that
-// product (one rounding of each, half an ulp, as the tensors themselves have); their sum
-// is taken of the fp32 values.
+// product, one rounding of each, half an ulp as the tensors themselves have; their sum is taken
+// of the fp32 values.  fp16 has few exponents for that: there they are lifted (kAttnLift), so that only
+// those below 2^-25 of a row's largest are held in fewer bits, in steps of 2^-35.
 #include "attention_common.h"
 
 namespace c3d {
 
 constexpr float kAttnLog2e = 1.44269504088896341f, kAttnLn2 = 0.693147180559945309f;
 
+// Exponentials are taken against the running maximum less kAttnLift, in units of log2, and the maximum
+// follows a step only where it would be passed by more than kAttnRise: they are then at most 2^15 in
+// fp16, which has few exponents and could not hold small ones otherwise.  Where many weak keys
+// stand beside a strong one whose value is next to nothing, the weak ones are the result: 36863 of
+// them 17.5 nats below lost a third of it without a lift, and lose at most 6e-4 with 2^11.  A maximum that follows at once
+// (lifts of 12 to 14) rescales the sums more often: 613 keys in heads of 80 7 to 8% more time, this rise 2%,
+// a rise of 8 (a lift of 7) none; 20480 keys in heads of 64 1 to 3%, none and none.
+// bf16 has fp32's exponents: no lift, and a maximum that seldom follows.
+template <typename E>
+constexpr float kAttnLift = std::is_same_v<E, __bf16> ? 0.0f : 11.0f;
+template <typename E>
+constexpr float kAttnRise = std::is_same_v<E, __bf16> ? 8.0f : 4.0f;
+
 // The running softmax of one query per lane, scores in units of log2.
 struct AttnSoftmax {
-    float max, use;  // the running maximum; the same where there is one, else 0
+    float max, use;  // the running maximum, less the lift; the same where there is one, else 0
     float sum;       // of the lane's own half of the keys
     __device__ __forceinline__ void init() {
         max = -__builtin_inff();
@@ -35,6 +49,12 @@ struct AttnSoftmax {
         return f;
     }
 };
+
+// The logarithm of a row's sum, the lift taken off where it is exact.
+template <typename E>
+__device__ __forceinline__ float attn_lse(float use, float sum) {
+    return ((use + kAttnLift<E>) + __builtin_amdgcn_logf(sum * __builtin_exp2f(-kAttnLift<E>))) * kAttnLn2;
+}
 
 // 1 / sum; 0 for a row that saw no key.
 __device__ __forceinline__ float attn_inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
@@ -154,10 +174,8 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_tile_kernel(A
 #pragma unroll
             for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[t][e]);
         mx = both_max(mx) * c;
-        // the maximum follows only where it would be passed by more than 2^8: probabilities
-        // are at most that, far inside the range of either type
-        if (__builtin_amdgcn_ballot_w64(mx > sm.max + 8.0f)) {
-            const float f = sm.raise(mx);
+        if (__builtin_amdgcn_ballot_w64(mx > sm.max + (kAttnLift<E> + kAttnRise<E>))) {
+            const float f = sm.raise(mx - kAttnLift<E>);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -223,7 +241,7 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_tile_kernel(A
     const int h = hk * p.group + g;
     if (p.lse && lane < 32)
         p.lse[((int64_t)b * p.hq + h) * p.tq + i] =
-            alive ? (sm.use + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -__builtin_inff();
+            alive ? attn_lse<E>(sm.use, sum) : -__builtin_inff();
     _Float16 *out = p.o + b * p.os[0] + i * p.os[1] + h * p.os[2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, acc[t], inv, d - 32 * t, lane, true);
@@ -334,8 +352,8 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_phase_kernel(
 #pragma unroll
                 for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[t][e]);
             mx = both_max(mx) * c;
-            if (__builtin_amdgcn_ballot_w64(mx > sm.max + 8.0f)) {
-                const float f = sm.raise(mx);
+            if (__builtin_amdgcn_ballot_w64(mx > sm.max + (kAttnLift<E> + kAttnRise<E>))) {
+                const float f = sm.raise(mx - kAttnLift<E>);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -392,7 +410,7 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_phase_kernel(
     const int h = hk * p.group + g;
     if (p.lse && lane < 32)
         p.lse[((int64_t)b * p.hq + h) * p.tq + i] =
-            alive ? (sm.use + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -__builtin_inff();
+            alive ? attn_lse<E>(sm.use, sum) : -__builtin_inff();
     _Float16 *out = p.o + b * p.os[0] + i * p.os[1] + h * p.os[2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) store_column<E>(out + 32 * t, acc[t], inv, d - 32 * t, lane, true);
@@ -476,8 +494,8 @@ __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
 #pragma unroll
         for (int e = 1; e < 16; ++e) mx = fmaxf(mx, x[e]);
         mx = both_max(mx) * c;
-        if (__builtin_amdgcn_ballot_w64(mx > sm.max + 8.0f)) {
-            const float f = sm.raise(mx);
+        if (__builtin_amdgcn_ballot_w64(mx > sm.max + (kAttnLift<E> + kAttnRise<E>))) {
+            const float f = sm.raise(mx - kAttnLift<E>);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -542,7 +560,7 @@ __global__ __launch_bounds__(256) void attention_few_kernel(AttnParams p) {
         const float inv = attn_inverse(sum);
         if (e == 0 && p.lse)
             p.lse[((int64_t)b * p.hq + h) * p.tq + ti] =
-                live ? (use + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -__builtin_inff();
+                live ? attn_lse<E>(use, sum) : -__builtin_inff();
         half4_t o;
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] = live ? from_f32<E>(v[k] * inv) : (_Float16)0.0f;
@@ -599,7 +617,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnParams p) {
     const float inv = attn_inverse(sum);
     if (l == 0 && p.lse)
         p.lse[((int64_t)b * p.hq + h) * p.tq + ti] =
-            live ? (use + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -__builtin_inff();
+            live ? attn_lse<E>(use, sum) : -__builtin_inff();
     if (e < p.d) {
         half4_t o;
 #pragma unroll

@@ -233,8 +233,8 @@ struct Halves {
 };
 // fp16 has 5 bits of exponent: in the gradients, probabilities (at most 1, 5e-5 in even rows of 20000
 // keys) are 2^15 times as large as operands, so that they stay normal numbers, and what is
-// summed of them is divided by that at the end.  (The forward pass divides by a row's own sum at the
-// end: next to its largest exponential, 1 or more, what the small ones lose does not count.)
+// summed of them is divided by that at the end.  (The forward pass knows no lse yet and lifts by less:
+// see kAttnLift.)
 template <typename E>
 constexpr float kLift = std::is_same_v<E, __bf16> ? 0.0f : 15.0f;
 template <typename E>

@@ -497,7 +497,8 @@ conv3d_status rope3d_backward(rope3d_plan_t p, const void *dq_out, const void *d
  * frame by itself; frame = 1 is causal token by token.  A query that sees no key has
  * o = 0, lse = -inf and no part in any gradient.
  * Arithmetic is fp32, o is rounded once; probabilities (and in the backward pass their
- * gradients) are rounded to the element type as operands of the second products.
+ * gradients) are rounded to the element type as operands of the second products (in fp16 the
+ * forward pass's no finer than in steps of 2^-35 of the query's largest one).
  * The forward pass never reads keys behind the last one that a query of the call sees, so a
  * cache may hold anything behind the tokens written so far.  Other tokens that a query does not
  * see do not reach it as long as they are finite: an infinite or NaN v that one query sees, or that
