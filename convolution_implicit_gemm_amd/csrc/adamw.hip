@@ -55,8 +55,12 @@ __device__ __forceinline__ int block_power(const float (&x)[4]) {
 // 2^-e of N blocks to a half wave, whose lanes all hold them: the first wave of the workgroup works
 // out those of all.  By powf, as a program that scales its states elementwise (ldexp of a tensor
 // is a product with its powf) takes it: powf is half an ulp off for a sixth of the powers, which decides
-// where values between two codes go that lie exactly on the border, and with gradients of
-// 8 bits and betas of few digits one in 250 does.  Codes are then that program's to the bit.
+// where values go that lie exactly on the border between two codes, both equally near, and with gradients of
+// 8 bits and betas of few digits one in 250 does.  Codes are then that program's to the bit, and weights
+// follow its weights; with 2^-e exact, one code in 250 is the other neighbour, and its weight a step later off by up to a
+// tenth of a step.  The price is time: 61 tensors of 14 million 39.8 us (2^-e exact: 35.2), 201 million weights 542 (534).
+// Against the definition in 64 bits neither is ahead by much: 1.28% of m's codes are the other neighbour (exact 1.16%), most
+// of them from the rounding of beta m + (1 - beta) g itself.
 template <int N>
 __device__ __forceinline__ void inverse_powers(const int (&e)[N], float (&inv)[N]) {
     static_assert(8 * N <= 64, "one wave for all");
@@ -191,7 +195,7 @@ __device__ __forceinline__ void new_states(const AdamwHyper &h, float x, float &
 }
 
 // A lane takes 4 adjacent elements at a time (one access of up to 16 bytes to each array, whole
-// lines of it to a wave), half a wave a block of 128, whose scale it finds by itself; a
+// lines of it to a wave), half a wave a block of 128, whose largest value it finds by itself; a
 // workgroup adamw_unit() adjacent elements of one tensor, all of them on their way at once, so that
 // workgroups that run together read and write adjacent memory: 201 million weights, 8-bit
 // states 538 us, 6.0 TB/s, bound by memory (with 24 times the elements to a workgroup, one after the

@@ -586,8 +586,8 @@ conv3d_status attention_backward(attention_plan_t p, const void *dout, const voi
  *          block of 128 elements (the last one may be shorter): uint8 [(count + 127) / 128]
  * In 8 bits a block's byte s and codes c stand for m = c 2^(s - 127) and sqrt(v) =
  * c 2^(s - 127), s - 127 the least power (from -126 on) at which the block's largest value is
- * 448 or less; the product with powf(2, 127 - s) is rounded to nearest, and a positive
- * sqrt(v) never to 0, so that no step divides by a state that vanished.  Zero bytes are the states before the first step.  The step itself
+ * 448 or less; values are rounded to the nearest code (of two that are as near, within fp32's rounding, either one),
+ * and a positive sqrt(v) never to 0, so that no step divides by a state that vanished.  Zero bytes are the states before the first step.  The step itself
  * uses the states before they are rounded.  A value that is not finite becomes a NaN code and
  * does not count for its block's scale.
  */
