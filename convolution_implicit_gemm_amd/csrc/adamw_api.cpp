@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <new>
@@ -53,6 +54,8 @@ conv3d_status hyper_of(const adamw_hyper *h, AdamwHyper *out) {
     out->lr_decay = (float)(h->lr * h->weight_decay);
     for (float x : {out->grad_scale, out->lr1, out->root2, out->eps, out->lr_decay})
         if (!std::isfinite(x)) return api_fail(CONV3D_ERR_INVALID_ARG, "a hyperparameter is past the range of fp32");
+    // the kernel's reciprocal of a subnormal is infinite, and 0 times that no number
+    if (h->eps > 0.0 && out->eps < FLT_MIN) return api_fail(CONV3D_ERR_INVALID_ARG, "eps is below 2^-126 and not 0");
     return CONV3D_OK;
 }
 static_assert(sizeof(AdamwHyper) == ADAMW_DEVICE_HYPER * sizeof(float), "the numbers in device memory");

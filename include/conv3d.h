@@ -620,7 +620,8 @@ void adamw_plan_destroy(adamw_plan_t p);
 /* The numbers that the kernels take, as fp32 (computed in 64 bits). */
 enum { ADAMW_DEVICE_HYPER = 9 };
 /* INVALID_ARG for lr, eps or weight_decay negative or not finite, betas outside [0, 1), a
- * grad_scale that is not finite, numbers past the range of fp32, or step < 1. */
+ * grad_scale that is not finite, numbers past the range of fp32, an eps below 2^-126 that is not 0 (with
+ * 0, an element without gradient or states is 0 / 0), or step < 1. */
 conv3d_status adamw_hyper_pack(const adamw_hyper *h, float *out);
 
 /*

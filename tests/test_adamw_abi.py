@@ -116,3 +116,19 @@ def test_binding_checks_the_lists():
             c3d.adamw_list(*args, master=[f])
     with pytest.raises(c3d.Conv3dError, match=r"grads\[1\] is missing"):
         c3d.adamw_list(None, [f, None], [f, f], [f, f], master=[f, f])
+
+
+@pytest.mark.parametrize("eps,ok", [(0.0, True), (2.0 ** -126, True), (1e-30, True), (1.1e-38, False), (1e-39, False),
+                                    (1e-45, False), (1e-60, False)])
+def test_eps_is_a_normal_number_or_zero(eps, ok):
+    hyper = c3d.make_adamw_hyper(1e-3, eps=eps)
+    if ok:
+        assert c3d.adamw_hyper_pack(hyper)[7] == eps or eps == 1e-30
+    else:
+        with pytest.raises(c3d.Conv3dError) as e:
+            c3d.adamw_hyper_pack(hyper)
+        assert e.value.status == BAD
+        lib, h = c3d.load_library(), ctypes.c_void_p()
+        assert lib.adamw_plan((c3d.adamw_tensor * 1)(tensor()), 1, 0, ctypes.byref(h)) == 0
+        assert lib.adamw_step(h, ctypes.byref(hyper), None, None) == BAD
+        lib.adamw_plan_destroy(h)

@@ -248,3 +248,16 @@ def test_states_have_the_bits_of_the_formula_in_fp32(state8):
         if want is not m:
             code = torch.where((code == 0) & (y > 0), torch.full_like(code, 2.0 ** -9), code)
         assert torch.equal(codes.view(torch.float8_e4m3fn).float(), code)
+
+
+@pytest.mark.parametrize("state8", [False, True])
+def test_the_least_eps_divides_nothing_by_it(state8):
+    n = 300
+    kind = torch.uint8 if state8 else torch.float32
+    m, v = (torch.zeros(n, dtype=kind, device="cuda:0") for _ in range(2))
+    ms, vs = (torch.zeros(3, dtype=torch.uint8, device="cuda:0") for _ in range(2))
+    w = torch.full((n,), 0.75, device="cuda:0")
+    lst = c3d.adamw_list(None, [torch.zeros(n, device="cuda:0")], [m], [v], master=[w], m_scale=[ms] if state8 else None,
+                         v_scale=[vs] if state8 else None)
+    c3d.adamw_step(lst, c3d.make_adamw_hyper(1e-3, weight_decay=0.0, eps=2.0 ** -126))
+    assert bool((w == 0.75).all())
