@@ -19,7 +19,8 @@ constexpr float kAttnLog2e = 1.44269504088896341f, kAttnLn2 = 0.6931471805599453
 
 // Exponentials are taken against the running maximum less kAttnLift, in units of log2, and the maximum
 // follows a step only where it would be passed by more than kAttnRise: they are then at most 2^15 in
-// fp16, which has few exponents and could not hold small ones otherwise.  Where many weak keys
+// fp16, which has few exponents and could not hold small ones otherwise (2^16 would be too large: the rounding of
+// scores may add 1 to the exponent from 2^24 on, in units of log2, where they tell keys apart no more).  Where many weak keys
 // stand beside a strong one whose value is next to nothing, the weak ones are the result: 36863 of
 // them 17.5 nats below lost a third of it without a lift, and lose at most 6e-4 with 2^11.  A maximum that follows at once
 // (lifts of 12 to 14) rescales the sums more often: 613 keys in heads of 80 7 to 8% more time, this rise 2%,

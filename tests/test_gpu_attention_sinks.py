@@ -72,20 +72,22 @@ def test_weak_keys_of_many_sizes(tq):
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("tq", [1, 40, 300])
-def test_large_scores_do_not_overflow(tq, dtype):
-    # scores of up to 2^22, four steps of 2^20 apart: the largest alone counts, and exponentials of it that are
-    # off by the rounding of such scores still fit
-    d, tk, dev = 64, 500, "cuda:0"
+@pytest.mark.parametrize("scale", [1.0, 13.0, 16.0])
+@pytest.mark.parametrize("most", [241.0, 247.0, 251.0, 253.0])
+def test_large_scores_do_not_overflow(most, scale, tq, dtype):
+    # scores of up to 2^22 scale (2^26, where fp32 counts in steps of 8), far apart: the largest alone counts, and
+    # its exponential, off by the rounding of such scores, still fits
+    d, tk, dev, top = 64, 500, "cuda:0", 251.0 * most * 64 * scale
     g = gen(4)
-    q = torch.full((1, tq, 2, d), 256.0, dtype=DTYPES[dtype], device=dev)
+    q = torch.full((1, tq, 2, d), 251.0, dtype=DTYPES[dtype], device=dev)
     k = (torch.randint(0, 4, (1, tk, 1, 1), generator=g, device=dev) * 64.0).to(DTYPES[dtype]).expand(1, tk, 1, d).contiguous()
-    k[0, 123], k[0, 321] = 256.0, 192.0
+    k[0, 123], k[0, 321] = most, 192.0
     v = torch.randn((1, tk, 1, d), generator=g, device=dev).to(DTYPES[dtype])
-    plan = c3d.attention_plan(c3d.make_attention_desc(1, tq, tk, 2, 1, d, scale=1.0,
+    plan = c3d.attention_plan(c3d.make_attention_desc(1, tq, tk, 2, 1, d, scale=scale,
                                                       flags=c3d.CONV3D_F_BF16 if dtype == "bf16" else 0))
     o, lse = torch.empty_like(q), torch.empty((1, 2, tq), device=dev)
     c3d.attention_forward(plan, q, k, v, o, lse, workspace=scratch(plan.workspace_bytes))
     want = v[0, 123, 0].double()
     # the largest's exponential rounds once as an operand, the result once
     assert_within(o[0], want.expand(tq, 2, d), (UNIT[o.dtype] + 16 * U24) * want.abs().expand(tq, 2, d), "o")
-    assert bool((((lse.double() - 2.0 ** 22) / 2.0 ** 22).abs() <= 8 * U24).all()) and math.isfinite(float(lse.sum()))
+    assert bool(((lse.double() / top - 1.0).abs() <= 8 * U24).all()) and math.isfinite(float(lse.sum()))
