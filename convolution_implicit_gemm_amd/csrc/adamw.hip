@@ -198,8 +198,8 @@ __device__ __forceinline__ void new_states(const AdamwHyper &h, float x, float &
 // lines of it to a wave), half a wave a block of 128, whose largest value it finds by itself; a
 // workgroup adamw_unit() adjacent elements of one tensor, all of them on their way at once, so that
 // workgroups that run together read and write adjacent memory: 201 million weights, 8-bit
-// states 538 us, 6.0 TB/s, bound by memory (with 24 times the elements to a workgroup, one after the
-// other, a fifth more).
+// states 537-542 us, 6.0 TB/s, bound by memory (with 24 times the elements to a workgroup, one after the
+// other, a fifth more); fp32 states 1024-1031 us, 5.5 TB/s.
 template <typename E, bool STATE8, bool GRAD32, bool FAR>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamwParams p) {
     constexpr int PARTS = adamw_unit(FAR) / 1024;

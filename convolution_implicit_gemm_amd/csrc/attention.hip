@@ -66,8 +66,10 @@ __device__ __forceinline__ float attn_inverse(float sum) { return sum == 0.0f ? 
 // the step before is computed.  More rows to a tile read K and V less often, more waves to a
 // row shorten the way through its keys: where the rows alone do not fill the card.  What is left
 // is the latency of a step: score products, softmax and output products of a wave depend on each other, and
-// the other wave of its SIMD fills only part of the gaps (9 frames of 1024 tokens, 16 heads of 128: 103-109 us,
-// 710-750 TFLOP/s, matrix cores busy 48%).  Deeper rings do not help: 3 and 4 steps in LDS were level to slower.
+// the other wave of its SIMD fills only part of the gaps (1024 tokens, 8 heads of 128: 16 us in tiles of 64 rows, 272
+// TFLOP/s; 4096 tokens, token by token, 16 heads of 128: 78 us in tiles of 128, 880 TFLOP/s).  Deeper rings do not
+// help: 3 and 4 steps in LDS were level to slower.  Heads up to 64 are held to 128 registers, two workgroups to a
+// CU; 128 rows of heads of 64 spill 6 of them.
 template <typename E, int DP, int RG, int KG, int BN>
 __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_tile_kernel(AttnParams p) {
     constexpr int NT = DP / 32, KK = DP / 16, XN = BN / 32, STEP = KG * BN, TILE = STEP * DP * 2;
@@ -257,9 +259,12 @@ __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_tile_kernel(A
 // K(t - 1) and V(t - 2), whose last readers were one phase and two phases ago, and sees that they have landed
 // at the end of the products that follow; the other group's first reads of them are two phases later.
 // 20480 tokens causal by frames of 4096, 16 heads of 128: 1709-1760 us, 1170-1205 TFLOP/s (the tile kernel 1904),
-// matrix cores busy 65% at the 1.7-1.8 GHz that power leaves.  At heads of 64 the vector units bound it: a
-// score costs as many of their cycles as at 128 for half the products (4096 rows on 20480 keys 392-405 us,
-// 850-880 TFLOP/s, vector units busy 63%, matrix cores 40%; two workgroups per CU were level).
+// matrix cores busy 65% at the 1.7-1.8 GHz that power leaves.  9 frames of 1024 tokens, 16 heads of 128: 101-108 us,
+// 710-764 TFLOP/s, busy 48%: 576 equal tiles on 256 CUs are 2.25 rounds, and take three.  At heads of 64 a
+// score costs as many cycles of the vector units as at 128 for half the products (4096 rows on 20480 keys 392-405 us,
+// 850-880 TFLOP/s, vector units busy 63%, matrix cores 40%).  Heads up to 64 are held to 128 registers, which
+// leaves room for two workgroups to a CU and spills 8 of them at 64, 2 at 32: with 256 registers and no spills the same
+// case, one workgroup to a CU, takes 394 us for 392.
 template <typename E, int DP>
 __global__ __launch_bounds__(512, DP <= 64 ? 4 : 2) void attention_phase_kernel(AttnParams p) {
     constexpr int BN = 64, NT = DP / 32, KK = DP / 16, TILE = BN * DP * 2;

@@ -70,8 +70,8 @@ struct Choice {
 
 enum Pass { kForward, kDq, kDkv };
 
-// Fitted to 3700 measured calls (heads of 32, 64, 96 and 128, 64 to 9216 tokens, 2 to 48 heads, with and
-// without a mask, 1 to 16 pieces): the choice is then 1 to 3% off the fastest kernel on average.
+// Fitted to 3700 timed calls (heads of 32, 64, 96 and 128, 64 to 9216 tokens, 2 to 48 heads, with and
+// without a mask, 1 to 16 pieces): over those calls the choice was 1 to 3% off the fastest kernel on average.
 // Per pass: the time of a call besides its steps (kDkv: with that of the row sums), of a
 // workgroup besides its steps, what joining the waves adds to that, the share of the longest workgroup
 // that the end of unequal ones waits for, a second launch to join pieces, and the partials' us per 2^20 or so values.

@@ -2,10 +2,11 @@
 // forward pass's lse, and delta_i = dout_i . o_i:
 //   dP_ij = dout_i . v_j,  dS_ij = P_ij (dP_ij - delta_i)
 //   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
-// Two kernels: one holds query rows and runs over the keys (dq), the other holds keys
-// and runs over the query rows (dk, dv).  S and dP are computed in both, seven products for
-// the five of the formula, so that every sum stays in the registers of one wave: no
-// atomics, no partial sums in memory, the same result in every call.
+// One kernel holds query rows and runs over the keys (dq), another holds keys and runs over the
+// query rows (dk, dv); a third is both in one launch.  S and dP are computed in both, seven products for
+// the five of the formula, so that a sum is one workgroup's own: its waves' parts meet in LDS, in a fixed order.
+// Where few keys meet many queries, a key tile's steps are split over workgroups, which leave fp32 partials of dk
+// and dv in the workspace; a join kernel adds them in their order.  No atomics: the same result in every call.
 #include "attention_common.h"
 
 namespace c3d {
@@ -39,8 +40,9 @@ constexpr int kFewKeys = 160, kFewSpan = 512;
 //
 // Three products for two of the forward pass, and the exponentials once more; K and V of a step are in LDS,
 // read as they lie and transposed.  20480 tokens causal by frames of 4096, 16 heads of 128: 2502 us, 1236 TFLOP/s,
-// matrix cores busy 65%, power-bound as the forward pass; 3 samples of 1543 tokens, 12 heads of 80: 38 us, busy 27%, the
-// latency of its steps.
+// matrix cores busy 65%, power-bound as the forward pass; 3 samples of 1543 tokens, 12 heads of 80 on 4: 38 us, busy 27%: a
+// step of 128 rows is 2.1 us, 1.9 of it products (of 96 elements for 80), but a workgroup has about five, and 6.5 us of
+// its own around them (the first loads, the waves' join, the stores) that no other one on its CU covers.
 //
 // READY: nlse and ndelta are there, from a launch of this kernel without dq.
 template <int DP, int RG, int KG, int BN>
@@ -235,7 +237,9 @@ __global__ __launch_bounds__(512) void attention_dq_kernel(AttnParams p) {
 //
 // 20480 tokens causal by frames of 4096, 16 heads of 128: 3566 us, 1155 TFLOP/s over its four products, matrix cores
 // busy 55%, LDS 41%: a SIMD's two waves hold 256 accumulators, and what a wave reads of Q and dout
-// feeds only its 32 keys.  One wave per SIMD with 64 keys, its steps pipelined, reads half of that
+// feeds only its 32 keys.  At heads of 128 the 256 registers do not hold all: 18 to 32 are spilled, and one of them,
+// the lane's offset of the rows' numbers, is reloaded in every step behind the next tiles' loads, for which the first two
+// waves then wait too.  One wave per SIMD with 64 keys, its steps pipelined, reads half of that
 // and took 4686 us: nothing fills its softmax.  3 samples of 1543 tokens, 12 heads of 80 on 4: 50 us and 6 for the join.
 template <int DP, int KW, int QG, int BM>
 constexpr int dkv_lds() {

@@ -195,8 +195,8 @@ hipError_t launch_attention_grad(const AttnParams &p, const AttnGradKinds &k, hi
 constexpr int kAdamwBlock = 128;    // elements that share a scale
 constexpr int kAdamwTensors = 48;   // of a launch: their table travels in the kernel's arguments (4 KiB)
 // Elements of a workgroup.  far: the step's tensors are larger than the last-level cache (256 MB)
-// and go past the caches.  201 million weights, 8-bit states, 3.2 GB: 548 us, through the caches
-// 7% more; 14 million in 61 tensors, 133 MB: past the caches 15% more than 39 us.
+// and go past the caches.  201 million weights, 8-bit states, 3.2 GB: 537-542 us, through the caches
+// 7% more; 14 million in 61 tensors, 133 MB: past the caches 15% more than 38-40 us.
 constexpr int adamw_unit(bool far) { return far ? 2048 : 1024; }
 constexpr int64_t kAdamwCached = (int64_t)256 << 20;
 struct AdamwTensor {
