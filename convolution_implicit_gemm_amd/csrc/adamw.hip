@@ -251,7 +251,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwParams p) {
             float root;
             new_states(h, x, m[k][i], v[k][i], root);
             // the instruction's reciprocal, an ulp off at most: 2^-23 of the step, not of the weight; the
-            // denominator is at least a root of 2^-149, never a subnormal, unless eps is one
+            // denominator is 0 or at least a root of 2^-149 or eps, never a subnormal (hyper_of refuses such an eps)
             w[k][i] = fmaf(w[k][i], keep, -h.lr1 * m[k][i] * __builtin_amdgcn_rcpf(fmaf(root, h.root2, h.eps)));
             if (STATE8) v[k][i] = root;
         }
